@@ -288,6 +288,98 @@ qlq_status qlq_kv_dequantize(const void* k_codes, const void* k_scales, const vo
                              const void* v_scales, int64_t T, int64_t H, int64_t D,
                              void* k_bf16, void* v_bf16, hipStream_t stream);
 
+/* -------------------------------------------------- between the linears */
+
+/* The rest of a decoder layer, in the library's 8-bit forms: norm to the next linear's codes,
+ * rotary positions, writing the KV cache and attention over it ("Nano-vLLM-MoE" README, section
+ * "KV cache compression": quantized per token at run time, paged in blocks). */
+
+/* RMS norm of each row, with an optional residual added first:
+ *   h = x + residual (fp32), residual_out = bf16(h),
+ *   y = h / sqrt(mean_k(h^2) + eps) * weight   (fp32)  ->  y_bf16 = bf16(y)
+ * x, residual, residual_out, y bf16 [M, K]; weight bf16 [K].  residual may be NULL (then
+ * residual_out must be NULL too), residual_out may be NULL.  y and residual_out may be the
+ * same buffers as x or residual (not each other).  eps > 0.  |h| below 2^60 (its square is summed in fp32). */
+qlq_status qlq_rms_norm(const void* x_bf16, const void* residual_bf16, const void* weight_bf16, int64_t M, int64_t K,
+                        float eps, void* y_bf16, void* residual_out_bf16, hipStream_t stream);
+
+/* The same norm, written as the codes of a static or dynamic W8A8 linear's input:
+ *   static:  yq = sat(round-to-nearest-even(y / input_scale))
+ *   dynamic: y_scale[m] = absmax_k |y[m,k]| / qmax (1 for an all-zero row), yq by it
+ * with qmax 127 (INT8) or 448 (e4m3fn).  y is the fp32 value (not rounded to bf16 first) and the
+ * quotient is fp32 to within one unit in the last place.  yq [M, K] one byte per code, not
+ * overlapping any input; y_scale fp32 [M] (device).  residual_out as above. */
+qlq_status qlq_rms_norm_quant_static(const void* x_bf16, const void* residual_bf16, const void* weight_bf16, int64_t M,
+                                     int64_t K, float eps, float input_scale, qlq_qtype qtype, void* yq,
+                                     void* residual_out_bf16, hipStream_t stream);
+qlq_status qlq_rms_norm_quant_dynamic(const void* x_bf16, const void* residual_bf16, const void* weight_bf16, int64_t M,
+                                      int64_t K, float eps, qlq_qtype qtype, void* yq, float* y_scale,
+                                      void* residual_out_bf16, hipStream_t stream);
+
+/* Rotary positions on x bf16 [T, H, D] (token stride in elements; heads and channels dense):
+ * with theta = positions[t] * inv_freq[i] (64 bits), c = factor cos(theta), s = factor sin(theta),
+ *   (a, b) -> (a c - b s, a s + b c),  i < rotary_dim / 2,
+ * on channels (i, i + rotary_dim / 2), or (2i, 2i + 1) with interleaved != 0; channels from
+ * rotary_dim on are copied.  rotary_dim even, 2 .. D; D a multiple of 8, at most 512.  positions
+ * int32 or int64 [T] (positions_64); inv_freq fp64 [rotary_dim / 2]; both on the device.  out may
+ * be x (same stride).  Positions within +-2^40. */
+qlq_status qlq_rope(const void* x_bf16, int64_t x_stride, int64_t T, int64_t H, int64_t D, const void* positions,
+                    int positions_64, const double* inv_freq, int64_t rotary_dim, float factor, int interleaved,
+                    void* out_bf16, int64_t out_stride, hipStream_t stream);
+
+/* Cache entries of k and v (bf16 [T, H, D], token strides in elements) by the codec's rules
+ * (qlq_kv_quantize), written to slots[t] of a cache of `pool` slots (k_codes [pool, H, D] and so
+ * on).  A slot outside 0 .. pool-1 (padding: -1) is not written; slots must not repeat within a
+ * call.  slots int32 or int64 [T] on the device.  D a multiple of 32, at most 512; code buffers
+ * 16-byte aligned. */
+qlq_status qlq_kv_append(const void* k_bf16, int64_t k_stride, const void* v_bf16, int64_t v_stride, int64_t T,
+                         int64_t H, int64_t D, const void* slots, int slots_64, int64_t pool, void* k_codes,
+                         void* k_scales, void* v_codes, void* v_scales, hipStream_t stream);
+
+/* qlq_rope of q [T, Hq, D] and k [T, Hk, D] and qlq_kv_append of the rotated k and of v, in one
+ * kernel.  K is quantized from the rotated fp32 value (not rounded to bf16 first). */
+qlq_status qlq_rope_kv_append(const void* q_bf16, int64_t q_stride, const void* k_bf16, int64_t k_stride,
+                              const void* v_bf16, int64_t v_stride, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
+                              const void* positions, int positions_64, const double* inv_freq, int64_t rotary_dim,
+                              float factor, int interleaved, const void* slots, int slots_64, int64_t pool,
+                              void* k_codes, void* k_scales, void* v_codes, void* v_scales, void* q_out_bf16,
+                              int64_t q_out_stride, hipStream_t stream);
+
+/* qlq_kv_dequantize of chosen slots: k, v bf16 [n, H, D] (dense, 16-byte aligned), row i from
+ * slots[i]; zeros for a slot outside the pool.  Slots may repeat. */
+qlq_status qlq_kv_gather(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                         int64_t pool, int64_t H, int64_t D, const void* slots, int slots_64, int64_t n, void* k_bf16,
+                         void* v_bf16, hipStream_t stream);
+
+/* Attention of q over a paged cache of such entries.  Sequence b holds seq_lens[b] tokens; token
+ * t is entry  block_table[b][t / page_size] * page_size + t % page_size.  Its query tokens are q
+ * rows q_start[b] .. q_start[b+1]-1 (q_start NULL: T = B, row b alone), the last of its cached
+ * tokens (append them first): query i of nq is at position p = seq_lens[b] - nq + i and sees
+ * tokens t <= p (causal; all tokens otherwise) with t > p - window (window 0: no such bound;
+ * window needs causal).  Query head h reads KV head h / (Hq / Hk).
+ *   out = softmax_t(scale q . k_t) v_t with k_t = k_code k_scale and v_t = v_code v_scale, not
+ *   rounded to bf16; lse (or NULL) = log sum_t exp(scale q . k_t), fp32 [T, Hq]
+ * fp32 accumulation, weights in 11 bits.  A row that sees no token gives zeros and lse -inf;
+ * rows of q outside every sequence are left as they were in out and lse.
+ * q bf16 [T, Hq, D], token stride in elements (a multiple of 8); out bf16 [T, Hq, D] dense; D 32,
+ * 64, 96, 128, 192 or 256; page_size a power of two; pool a multiple of it.  block_table int32
+ * [B, max_pages], seq_lens int32 [B], q_start int32 [B + 1], on the device: lengths are read there
+ * (the host does not wait for them) and bounded by 0 .. max_pages * page_size and 0 .. T; a token
+ * whose page is outside the pool is left out, never read.
+ * workspace: qlq_kv_attention_workspace_bytes(...), 256-byte aligned, zero-filled before its
+ * first use and left so for the next call; it serves this operator's calls only, one stream at
+ * a time. */
+qlq_status qlq_kv_attention(const void* q_bf16, int64_t q_stride, int64_t T, int64_t B, int64_t Hq, int64_t Hk,
+                            int64_t D, const void* k_codes, const void* k_scales, const void* v_codes,
+                            const void* v_scales, int64_t pool, const int32_t* block_table, int64_t max_pages,
+                            int64_t page_size, const int32_t* seq_lens, const int32_t* q_start, float scale, int causal,
+                            int64_t window, void* out_bf16, float* lse, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream);
+
+/* Workspace bytes of qlq_kv_attention for these sizes (one_each: q_start is NULL); 0 when the
+ * call needs none, or for sizes that the call refuses. */
+size_t qlq_kv_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int one_each);
+
 /* ------------------------------------------------------------- test hooks */
 
 /* The launch plan a GEMM call takes for these sizes when x is 16-byte aligned (what

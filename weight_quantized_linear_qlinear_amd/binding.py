@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import math
 import os
 import threading
 
@@ -57,6 +58,34 @@ _SIGNATURES = {
                                    _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p]),
     "qlq_kv_dequantize": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64,
                                      _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_void_p]),
+    "qlq_rms_norm": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_float,
+                                _c.c_void_p, _c.c_void_p, _c.c_void_p]),
+    "qlq_rms_norm_quant_static": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64,
+                                             _c.c_float, _c.c_float, _c.c_int, _c.c_void_p, _c.c_void_p,
+                                             _c.c_void_p]),
+    "qlq_rms_norm_quant_dynamic": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64,
+                                              _c.c_float, _c.c_int, _c.c_void_p, _c.c_void_p, _c.c_void_p,
+                                              _c.c_void_p]),
+    "qlq_rope": (_c.c_int, [_c.c_void_p, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_int,
+                            _c.c_void_p, _c.c_int64, _c.c_float, _c.c_int, _c.c_void_p, _c.c_int64, _c.c_void_p]),
+    "qlq_kv_append": (_c.c_int, [_c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_int64,
+                                 _c.c_int64, _c.c_void_p, _c.c_int, _c.c_int64, _c.c_void_p, _c.c_void_p,
+                                 _c.c_void_p, _c.c_void_p, _c.c_void_p]),
+    "qlq_rope_kv_append": (_c.c_int, [_c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64,
+                                      _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_int,
+                                      _c.c_void_p, _c.c_int64, _c.c_float, _c.c_int, _c.c_void_p, _c.c_int,
+                                      _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p,
+                                      _c.c_int64, _c.c_void_p]),
+    "qlq_kv_gather": (_c.c_int, [_c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64, _c.c_int64,
+                                 _c.c_int64, _c.c_void_p, _c.c_int, _c.c_int64, _c.c_void_p, _c.c_void_p,
+                                 _c.c_void_p]),
+    "qlq_kv_attention": (_c.c_int, [_c.c_void_p, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int64,
+                                    _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_int64,
+                                    _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_float,
+                                    _c.c_int, _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_size_t,
+                                    _c.c_void_p]),
+    "qlq_kv_attention_workspace_bytes": (_c.c_size_t, [_c.c_int64, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int64,
+                                                       _c.c_int]),
     "qlq_linear": (_c.c_int, [_c.c_int, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_void_p,
                               _c.c_int64, _c.c_int, _c.c_float, _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_void_p,
                               _c.c_size_t, _c.c_void_p]),
@@ -447,3 +476,375 @@ def kv_dequantize(q: QuantizedKV, k_out: torch.Tensor | None = None, v_out: torc
     _check(lib().qlq_kv_dequantize(_ptr(q.k_codes), _ptr(q.k_scales), _ptr(q.v_codes), _ptr(q.v_scales), T, H, D,
                                    _ptr(k_out), _ptr(v_out), _stream(q.k_codes.device)))
     return k_out, v_out
+
+
+def kv_cache(slots: int, heads: int, head_dim: int, device: torch.device | str | None = None) -> QuantizedKV:
+    """An empty cache of `slots` token entries (codes zero, scales one) for kv_append and kv_attention."""
+    if slots < 1 or heads < 1 or head_dim < 32 or head_dim % 32 != 0:
+        raise ValueError("slots and heads must be >= 1 and head_dim a multiple of 32")
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    return QuantizedKV(torch.zeros((slots, heads, head_dim), dtype=torch.int8, device=dev),
+                       torch.ones((slots, heads, head_dim // 32), dtype=torch.float16, device=dev),
+                       torch.zeros((slots, heads, head_dim), dtype=torch.uint8, device=dev),
+                       torch.ones((slots, heads), dtype=torch.float16, device=dev))
+
+
+# ---------------------------------------------------------------------- between the linears
+def _enqueue(dev: torch.device, fn, *args):
+    """fn(*args, the current stream of dev), with dev as the current device."""
+    if dev.index == torch.cuda.current_device():
+        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if status != 0:
+        _check(status)
+
+
+def _on(dev: torch.device, *ts):
+    """Dense tensors (or None) on the GPU `dev`."""
+    for t in ts:
+        if t is not None:
+            if t.device != dev:
+                raise ValueError(f"all tensors must be on one GPU (got {t.device} and {dev})")
+            if not t.is_contiguous():
+                raise ValueError("qlq needs contiguous (row-major) tensors")
+
+
+def _addr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _norm_inputs(x, weight, residual, residual_out):
+    if not x.is_cuda:
+        raise ValueError("qlq operates on GPU tensors only")
+    bf = torch.bfloat16
+    if x.dim() != 2 or x.dtype != bf:
+        raise ValueError("x must be a 2-D bf16 tensor")
+    if weight.dtype != bf or weight.dim() != 1 or weight.shape[0] != x.shape[1]:
+        raise ValueError(f"weight must be bf16 [{x.shape[1]}]")
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+    else:
+        if residual_out is None:
+            residual_out = torch.empty_like(x)
+        for t in (residual, residual_out):
+            if t.dtype != bf or t.shape != x.shape:
+                raise ValueError(f"residual and residual_out must be bf16 {list(x.shape)}")
+    _on(x.device, x, weight, residual, residual_out)
+    return residual_out
+
+
+def _norm_codes(x, qtype, out):
+    if out is None:
+        return torch.empty(x.shape, dtype=code_dtype(qtype), device=x.device)
+    if out.element_size() != 1 or out.shape != x.shape:
+        raise ValueError(f"out must be 1-byte codes {list(x.shape)}")
+    _on(x.device, out)
+    return out
+
+
+def rms_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, residual: torch.Tensor | None = None,
+             out: torch.Tensor | None = None, residual_out: torch.Tensor | None = None):
+    """RMS norm of x [M, K] bf16 rows: y bf16 [M, K]; with a residual, (y, h) where h = bf16(x + residual) and
+    y is the norm of the unrounded sum.  out and residual_out may be x or residual."""
+    residual_out = _norm_inputs(x, weight, residual, residual_out)
+    if out is None:
+        out = torch.empty_like(x)
+    elif out.dtype != torch.bfloat16 or out.shape != x.shape:
+        raise ValueError(f"out must be bf16 {list(x.shape)}")
+    else:
+        _on(x.device, out)
+    _enqueue(x.device, lib().qlq_rms_norm, x.data_ptr(), _addr(residual), weight.data_ptr(), x.shape[0], x.shape[1],
+             eps, out.data_ptr(), _addr(residual_out))
+    return out if residual is None else (out, residual_out)
+
+
+def rms_norm_quant_static(x: torch.Tensor, weight: torch.Tensor, input_scale: float, qtype: str, eps: float = 1e-6,
+                          residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                          residual_out: torch.Tensor | None = None):
+    """rms_norm straight to the codes of a static W8A8 linear's input: xq [M, K]; with a residual, (xq, h)."""
+    q = _qtype(qtype)
+    residual_out = _norm_inputs(x, weight, residual, residual_out)
+    out = _norm_codes(x, qtype, out)
+    _enqueue(x.device, lib().qlq_rms_norm_quant_static, x.data_ptr(), _addr(residual), weight.data_ptr(), x.shape[0],
+             x.shape[1], eps, float(input_scale), q, out.data_ptr(), _addr(residual_out))
+    return out if residual is None else (out, residual_out)
+
+
+def rms_norm_quant_dynamic(x: torch.Tensor, weight: torch.Tensor, qtype: str, eps: float = 1e-6,
+                           residual: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                           x_scale: torch.Tensor | None = None, residual_out: torch.Tensor | None = None):
+    """rms_norm straight to per-token codes and scales (qlinear_w8a8_dynamic's input): (xq [M, K], x_scale fp32
+    [M]); with a residual, (xq, x_scale, h)."""
+    q = _qtype(qtype)
+    residual_out = _norm_inputs(x, weight, residual, residual_out)
+    out = _norm_codes(x, qtype, out)
+    if x_scale is None:
+        x_scale = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+    elif x_scale.dtype != torch.float32 or x_scale.numel() != x.shape[0]:
+        raise ValueError(f"x_scale must be fp32 [{x.shape[0]}]")
+    else:
+        _on(x.device, x_scale)
+    _enqueue(x.device, lib().qlq_rms_norm_quant_dynamic, x.data_ptr(), _addr(residual), weight.data_ptr(), x.shape[0],
+             x.shape[1], eps, q, out.data_ptr(), x_scale.data_ptr(), _addr(residual_out))
+    return (out, x_scale) if residual is None else (out, x_scale, residual_out)
+
+
+def rope_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: dict | None = None,
+                  device: torch.device | str | None = None):
+    """(inv_freq fp64 [rotary_dim / 2] on the GPU, attention_factor): rotary frequencies base^(-2i / rotary_dim),
+    scaled for long contexts by `scaling`:
+      None
+      {"type": "linear", "factor": f}      every frequency / f
+      {"type": "ntk", "factor": f}         base * f^(rotary_dim / (rotary_dim - 2))
+      {"type": "yarn", "factor": f, "original_max_positions": n, "beta_fast": 32, "beta_slow": 1,
+       "attention_factor": 0.1 ln f + 1}   frequencies / f below beta_slow turns over n positions, unchanged above
+                                           beta_fast, a ramp between (by channel)
+      {"type": "llama3", "factor": f, "original_max_positions": n, "low_freq_factor": 1, "high_freq_factor": 4}
+                                           / f for wavelengths above n / low, unchanged below n / high, blended
+                                           between (by wavelength)"""
+    R = int(rotary_dim)
+    if R < 2 or R % 2 != 0:
+        raise ValueError("rotary_dim must be even and >= 2")
+    if not (math.isfinite(base) and base > 1.0):
+        raise ValueError("base must be finite and > 1")
+    kind, factor, extra = None, 1.0, {}
+    if scaling is not None:
+        extra = dict(scaling)
+        kind = extra.pop("type", None)
+        known = {"linear": set(), "ntk": set(), "yarn": {"original_max_positions", "beta_fast", "beta_slow",
+                                                         "attention_factor"},
+                 "llama3": {"original_max_positions", "low_freq_factor", "high_freq_factor"}}
+        if kind not in known:
+            raise ValueError(f"scaling type must be one of {sorted(known)}")
+        factor = float(extra.pop("factor", 1.0))
+        if not (math.isfinite(factor) and factor > 0.0):
+            raise ValueError("scaling factor must be finite and > 0")
+        if set(extra) - known[kind]:
+            raise ValueError(f"unknown {kind} scaling keys {sorted(set(extra) - known[kind])}")
+        if kind in ("yarn", "llama3") and not extra.get("original_max_positions", 0) > 0:
+            raise ValueError(f"{kind} scaling needs original_max_positions")
+    if kind == "ntk":
+        if R == 2:
+            raise ValueError("ntk scaling needs rotary_dim > 2")
+        base = base * factor ** (R / (R - 2))
+    f = [base ** (-2.0 * i / R) for i in range(R // 2)]
+    attention_factor = 1.0
+    if kind == "linear":
+        f = [v / factor for v in f]
+    elif kind == "yarn":
+        n = float(extra["original_max_positions"])
+
+        def channel(turns):      # the (fractional) pair index that makes `turns` turns over n positions
+            return R * math.log(n / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+
+        lo = max(math.floor(channel(float(extra.get("beta_fast", 32.0)))), 0)
+        hi = min(math.ceil(channel(float(extra.get("beta_slow", 1.0)))), R - 1)
+        ramp = [min(max((i - lo) / max(hi - lo, 1e-3), 0.0), 1.0) for i in range(R // 2)]
+        f = [v / factor * r + v * (1.0 - r) for v, r in zip(f, ramp)]
+        attention_factor = float(extra.get("attention_factor", 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0))
+    elif kind == "llama3":
+        n = float(extra["original_max_positions"])
+        low, high = float(extra.get("low_freq_factor", 1.0)), float(extra.get("high_freq_factor", 4.0))
+        if not 0.0 < low < high:
+            raise ValueError("llama3 scaling needs 0 < low_freq_factor < high_freq_factor")
+        smooth = [min(max((n * v / (2.0 * math.pi) - low) / (high - low), 0.0), 1.0) for v in f]
+        f = [v / factor * (1.0 - s) + v * s for v, s in zip(f, smooth)]
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    return torch.tensor(f, dtype=torch.float64, device=dev), attention_factor
+
+
+def _token_rows(t: torch.Tensor, name: str) -> int:
+    """Token stride of a bf16 GPU tensor [T, H, D] whose heads and channels are dense."""
+    if not t.is_cuda:
+        raise ValueError("qlq operates on GPU tensors only")
+    if t.dim() != 3 or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be bf16 [T, H, D]")
+    st, sh, sd = t.stride()
+    T, H, D = t.shape
+    if (sd != 1 and D > 1) or (sh != D and H > 1):
+        raise ValueError(f"{name} must be dense in its heads and channels (only the token stride is free)")
+    return st if T > 1 else H * D
+
+
+def _indices(t: torch.Tensor, n: int, dev: torch.device, name: str) -> int:
+    """1 for int64, 0 for int32 indices [n] on dev."""
+    if t.dtype not in (torch.int64, torch.int32) or t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name} must be int32 or int64 [{n}]")
+    _on(dev, t)
+    return int(t.dtype == torch.int64)
+
+
+def _frequencies(inv_freq: torch.Tensor, dev: torch.device) -> int:
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be fp64 [rotary_dim / 2] (rope_inv_freq)")
+    _on(dev, inv_freq)
+    return 2 * inv_freq.shape[0]
+
+
+def _cache_entries(c: QuantizedKV, H: int, D: int, dev: torch.device) -> int:
+    """Slots of a cache for H heads of D channels."""
+    P = c.k_codes.shape[0]
+    if D % 32 != 0:
+        raise ValueError("head_dim must be a multiple of 32")
+    if (c.k_codes.shape != (P, H, D) or c.v_codes.shape != (P, H, D) or c.k_scales.shape != (P, H, D // 32)
+            or c.v_scales.shape != (P, H)):
+        raise ValueError(f"the cache must hold [slots, {H}, {D}] entries")
+    if (c.k_codes.element_size() != 1 or c.v_codes.element_size() != 1 or c.k_scales.dtype != torch.float16
+            or c.v_scales.dtype != torch.float16):
+        raise ValueError("the cache must hold 1-byte codes and float16 scales")
+    _on(dev, c.k_codes, c.k_scales, c.v_codes, c.v_scales)
+    return P
+
+
+def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, attention_factor: float = 1.0,
+         interleaved: bool = False, out: torch.Tensor | None = None) -> torch.Tensor:
+    """Rotary positions on the first 2 * len(inv_freq) channels of x [T, H, D] bf16 (pairs (i, i + R/2), or (2i,
+    2i+1) interleaved); the token stride of x is free.  out may be x."""
+    xs = _token_rows(x, "x")
+    T, H, D = x.shape
+    R = _frequencies(inv_freq, x.device)
+    p64 = _indices(positions, T, x.device, "positions")
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=x.device)
+    os_ = _token_rows(out, "out")
+    if out.shape != x.shape or out.device != x.device:
+        raise ValueError(f"out must be bf16 {list(x.shape)} on {x.device}")
+    _enqueue(x.device, lib().qlq_rope, x.data_ptr(), xs, T, H, D, positions.data_ptr(), p64, inv_freq.data_ptr(), R,
+             float(attention_factor), int(interleaved), out.data_ptr(), os_)
+    return out
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, cache: QuantizedKV, slots: torch.Tensor) -> QuantizedKV:
+    """Quantize k, v [T, H, D] bf16 (as kv_quantize; token strides free) into cache entries slots [T].  A slot
+    outside the cache (padding: -1) is not written; slots must not repeat.  Returns the cache."""
+    ks, vs = _token_rows(k, "k"), _token_rows(v, "v")
+    if k.shape != v.shape or k.device != v.device:
+        raise ValueError("k and v must have the same shape and device")
+    T, H, D = k.shape
+    P = _cache_entries(cache, H, D, k.device)
+    s64 = _indices(slots, T, k.device, "slots")
+    _enqueue(k.device, lib().qlq_kv_append, k.data_ptr(), ks, v.data_ptr(), vs, T, H, D, slots.data_ptr(), s64, P,
+             cache.k_codes.data_ptr(), cache.k_scales.data_ptr(), cache.v_codes.data_ptr(), cache.v_scales.data_ptr())
+    return cache
+
+
+def rope_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
+                   cache: QuantizedKV, slots: torch.Tensor, attention_factor: float = 1.0, interleaved: bool = False,
+                   q_out: torch.Tensor | None = None) -> torch.Tensor:
+    """rope of q [T, Hq, D] and k [T, Hk, D], and kv_append of the rotated k and of v, in one kernel.  q, k and v
+    may be views of one projection's output.  Returns the rotated q (q_out may be q)."""
+    qs, ks, vs = _token_rows(q, "q"), _token_rows(k, "k"), _token_rows(v, "v")
+    T, Hq, D = q.shape
+    dev = q.device
+    if k.shape != v.shape or k.shape[0] != T or k.shape[2] != D or k.device != dev or v.device != dev:
+        raise ValueError("k and v must be [T, Hk, D] with q's T, D and device")
+    Hk = k.shape[1]
+    P = _cache_entries(cache, Hk, D, dev)
+    R = _frequencies(inv_freq, dev)
+    p64, s64 = _indices(positions, T, dev, "positions"), _indices(slots, T, dev, "slots")
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    os_ = _token_rows(q_out, "q_out")
+    if q_out.shape != q.shape or q_out.device != dev:
+        raise ValueError(f"q_out must be bf16 {list(q.shape)} on {dev}")
+    _enqueue(dev, lib().qlq_rope_kv_append, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, Hq, Hk, D,
+             positions.data_ptr(), p64, inv_freq.data_ptr(), R, float(attention_factor), int(interleaved),
+             slots.data_ptr(), s64, P, cache.k_codes.data_ptr(), cache.k_scales.data_ptr(), cache.v_codes.data_ptr(),
+             cache.v_scales.data_ptr(), q_out.data_ptr(), os_)
+    return q_out
+
+
+def kv_gather(cache: QuantizedKV, slots: torch.Tensor, k_out: torch.Tensor | None = None,
+              v_out: torch.Tensor | None = None):
+    """Cache entries slots [n] as dense bf16 (K, V) [n, H, D]; zeros for a slot outside the cache."""
+    dev = cache.k_codes.device
+    if not cache.k_codes.is_cuda:
+        raise ValueError("qlq operates on GPU tensors only")
+    _, H, D = cache.k_codes.shape
+    P = _cache_entries(cache, H, D, dev)
+    n = slots.shape[0] if slots.dim() == 1 else -1
+    s64 = _indices(slots, n, dev, "slots")
+    outs = []
+    for t in (k_out, v_out):
+        if t is None:
+            t = torch.empty((n, H, D), dtype=torch.bfloat16, device=dev)
+        elif t.dtype != torch.bfloat16 or t.shape != (n, H, D):
+            raise ValueError(f"k_out and v_out must be bf16 [{n}, {H}, {D}]")
+        else:
+            _on(dev, t)
+        outs.append(t)
+    _enqueue(dev, lib().qlq_kv_gather, cache.k_codes.data_ptr(), cache.k_scales.data_ptr(), cache.v_codes.data_ptr(),
+             cache.v_scales.data_ptr(), P, H, D, slots.data_ptr(), s64, n, outs[0].data_ptr(), outs[1].data_ptr())
+    return outs[0], outs[1]
+
+
+def kv_attention_workspace_bytes(T: int, B: int, Hq: int, Hk: int, D: int, one_each: bool = True) -> int:
+    """Workspace of kv_attention for T query tokens of B sequences (one_each: without q_start)."""
+    return int(lib().qlq_kv_attention_workspace_bytes(T, B, Hq, Hk, D, int(one_each)))
+
+
+_attention_workspaces: dict = {}
+
+
+def _attention_workspace(dev: torch.device, nbytes: int) -> torch.Tensor | None:
+    """A zero-filled workspace of this stream, grown on demand; inside a graph capture, one of the graph's own
+    (its zero fill is recorded with it), so that graphs and streams never share one."""
+    if nbytes == 0:
+        return None
+    if torch.cuda.is_current_stream_capturing():
+        return torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+    key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
+    ws = _attention_workspaces.get(key)
+    if ws is None or ws.numel() < nbytes:
+        ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+        _attention_workspaces[key] = ws
+    return ws
+
+
+def kv_attention(q: torch.Tensor, cache: QuantizedKV, block_table: torch.Tensor, seq_lens: torch.Tensor,
+                 page_size: int, q_start: torch.Tensor | None = None, scale: float | None = None, causal: bool = True,
+                 window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of q [T, Hq, D] bf16 over a paged cache (kv_append): out bf16 [T, Hq, D].
+
+    block_table int32 [B, pages] holds each sequence's page numbers (token t is cache entry
+    block_table[b][t // page_size] * page_size + t % page_size), seq_lens int32 [B] its cached tokens.  Without
+    q_start, row b of q is the last token of sequence b; with q_start int32 [B + 1], rows q_start[b] ..
+    q_start[b+1]-1 are its last tokens.  A query sees the tokens up to its own (causal), and no more than `window`
+    of them if that is not 0.  scale defaults to D^-0.5; lse fp32 [T, Hq], if given, receives log sum exp of the
+    scaled scores.  Rows that see nothing give zeros (lse -inf); rows of no sequence are left as they were.
+    The lengths stay on the device: nothing here waits for them."""
+    qs = _token_rows(q, "q")
+    T, Hq, D = q.shape
+    dev = q.device
+    if cache.k_codes.dim() != 3:
+        raise ValueError("the cache must hold [slots, heads, head_dim] entries")
+    Hk = cache.k_codes.shape[1]
+    P = _cache_entries(cache, Hk, D, dev)
+    if block_table.dim() != 2 or block_table.dtype != torch.int32:
+        raise ValueError("block_table must be int32 [B, pages]")
+    B = block_table.shape[0]
+    if seq_lens.dtype != torch.int32 or seq_lens.shape != (B,):
+        raise ValueError(f"seq_lens must be int32 [{B}]")
+    if q_start is not None and (q_start.dtype != torch.int32 or q_start.shape != (B + 1,)):
+        raise ValueError(f"q_start must be int32 [{B + 1}]")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    elif out.dtype != torch.bfloat16 or out.shape != q.shape:
+        raise ValueError(f"out must be bf16 {list(q.shape)}")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, Hq)):
+        raise ValueError(f"lse must be fp32 [{T}, {Hq}]")
+    _on(dev, block_table, seq_lens, q_start, out, lse, workspace)
+    L = lib()
+    if workspace is None:
+        need = L.qlq_kv_attention_workspace_bytes(T, B, Hq, Hk, D, int(q_start is None))
+        workspace = _attention_workspace(dev, need)
+    _enqueue(dev, L.qlq_kv_attention, q.data_ptr(), qs, T, B, Hq, Hk, D, cache.k_codes.data_ptr(),
+             cache.k_scales.data_ptr(), cache.v_codes.data_ptr(), cache.v_scales.data_ptr(), P,
+             block_table.data_ptr(), block_table.shape[1], page_size, seq_lens.data_ptr(), _addr(q_start),
+             D ** -0.5 if scale is None else float(scale), int(causal), int(window), out.data_ptr(), _addr(lse),
+             _addr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
+    return out

@@ -772,6 +772,307 @@ qlq_status qlq_linear(qlq_scheme scheme, const void* x_bf16, int64_t M, int64_t 
   return launch_gemm(g, stream);
 }
 
+// ---------------------------------------------------------- between the linears
+
+static qlq_status check_norm(const void* x, const void* residual, const void* w, int64_t M, int64_t K, float eps,
+                             const void* y, const void* residual_out) {
+  if (!x || !w || !y) return fail(QLQ_ERR_INVALID_ARG, "null pointer");
+  if (residual_out && !residual) return fail(QLQ_ERR_INVALID_ARG, "residual_out needs a residual");
+  if (residual_out && residual_out == y) return fail(QLQ_ERR_INVALID_ARG, "y and residual_out must be two buffers");
+  if (qlq_status st = check_dims(M, K, 1)) return st;
+  if (!std::isfinite(eps) || !(eps > 0.0f)) return fail(QLQ_ERR_INVALID_ARG, "eps must be finite and > 0");
+  if (!aligned(x, 2) || !aligned(residual, 2) || !aligned(w, 2) || !aligned(residual_out, 2))
+    return fail(QLQ_ERR_INVALID_ARG, "misaligned pointer");
+  return QLQ_OK;
+}
+
+qlq_status qlq_rms_norm(const void* x, const void* residual, const void* w, int64_t M, int64_t K, float eps, void* y,
+                        void* residual_out, hipStream_t stream) {
+  if (qlq_status st = check_norm(x, residual, w, M, K, eps, y, residual_out)) return st;
+  if (!aligned(y, 2)) return fail(QLQ_ERR_INVALID_ARG, "misaligned pointer");
+  return hip_status(qlq::launch_rms_norm(x, residual, w, (int)M, (int)K, eps, 0, 0, 1.0f, y, nullptr, residual_out,
+                                         stream),
+                    "rms_norm");
+}
+
+qlq_status qlq_rms_norm_quant_static(const void* x, const void* residual, const void* w, int64_t M, int64_t K,
+                                     float eps, float input_scale, qlq_qtype qtype, void* yq, void* residual_out,
+                                     hipStream_t stream) {
+  if (qlq_status st = check_norm(x, residual, w, M, K, eps, yq, residual_out)) return st;
+  if (qlq_status st = check_qtype(qtype)) return st;
+  if (qlq_status st = check_scale(input_scale, "input_scale")) return st;
+  return hip_status(qlq::launch_rms_norm(x, residual, w, (int)M, (int)K, eps, 1, (int)qtype, input_scale, yq, nullptr,
+                                         residual_out, stream),
+                    "rms_norm_quant_static");
+}
+
+qlq_status qlq_rms_norm_quant_dynamic(const void* x, const void* residual, const void* w, int64_t M, int64_t K,
+                                      float eps, qlq_qtype qtype, void* yq, float* y_scale, void* residual_out,
+                                      hipStream_t stream) {
+  if (!y_scale) return fail(QLQ_ERR_INVALID_ARG, "null pointer");
+  if (qlq_status st = check_norm(x, residual, w, M, K, eps, yq, residual_out)) return st;
+  if (qlq_status st = check_qtype(qtype)) return st;
+  if (!aligned(y_scale, 4)) return fail(QLQ_ERR_INVALID_ARG, "misaligned pointer");
+  return hip_status(qlq::launch_rms_norm(x, residual, w, (int)M, (int)K, eps, 2, (int)qtype, 1.0f, yq, y_scale,
+                                         residual_out, stream),
+                    "rms_norm_quant_dynamic");
+}
+
+// Tokens, heads and channels of a rope / append call (D_step: what head_dim must be a multiple of).
+static qlq_status check_heads(int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t D_step) {
+  if (T < 1 || D < 1 || Hq < 0 || Hk < 0 || Hq + Hk < 1) return fail(QLQ_ERR_INVALID_ARG, "T, heads and D must be >= 1");
+  if (D % D_step != 0 || D > 512)
+    return fail(QLQ_ERR_INVALID_ARG, "head_dim D must be a multiple of %lld, at most 512", (long long)D_step);
+  if (T > kMaxDim || Hq > 65536 || Hk > 65536) return fail(QLQ_ERR_INVALID_ARG, "sizes above T = 2^24 or 65536 heads are not supported");
+  return QLQ_OK;
+}
+
+static qlq_status check_stride(int64_t stride, int64_t T, int64_t H, int64_t D, const char* name) {
+  if (T > 1 && stride < H * D) return fail(QLQ_ERR_INVALID_ARG, "%s token stride %lld is below a token's %lld elements", name,
+                                           (long long)stride, (long long)(H * D));
+  if (stride < 0 || stride > (int64_t(1) << 36)) return fail(QLQ_ERR_INVALID_ARG, "%s token stride out of range", name);
+  return QLQ_OK;
+}
+
+static qlq_status check_rotary(const void* positions, const double* inv_freq, int64_t R, int64_t D, float factor) {
+  if (!positions || !inv_freq) return fail(QLQ_ERR_INVALID_ARG, "null pointer");
+  if (R < 2 || R % 2 != 0 || R > D) return fail(QLQ_ERR_INVALID_ARG, "rotary_dim must be even, 2 .. head_dim");
+  if (!std::isfinite(factor)) return fail(QLQ_ERR_INVALID_ARG, "factor must be finite");
+  if (!aligned(inv_freq, 8)) return fail(QLQ_ERR_INVALID_ARG, "misaligned pointer");
+  return QLQ_OK;
+}
+
+static qlq_status check_cache(const void* kc, const void* ks, const void* vc, const void* vs, const void* slots,
+                              int slots_64, int64_t pool) {
+  if (!kc || !ks || !vc || !vs || !slots) return fail(QLQ_ERR_INVALID_ARG, "null pointer");
+  if (pool < 1 || pool >= (int64_t(1) << 31)) return fail(QLQ_ERR_INVALID_ARG, "the cache must have 1 .. 2^31 - 1 slots");
+  if (!aligned(kc, 16) || !aligned(vc, 16)) return fail(QLQ_ERR_INVALID_ARG, "cache codes must be 16-byte aligned");
+  if (!aligned(ks, 2) || !aligned(vs, 2) || !aligned(slots, slots_64 ? 8 : 4))
+    return fail(QLQ_ERR_INVALID_ARG, "misaligned pointer");
+  return QLQ_OK;
+}
+
+static bool rows16(const void* p, int64_t stride, int64_t D) { return !p || (aligned(p, 16) && stride % 8 == 0 && D % 8 == 0); }
+
+qlq_status qlq_rope(const void* x, int64_t x_stride, int64_t T, int64_t H, int64_t D, const void* positions,
+                    int positions_64, const double* inv_freq, int64_t rotary_dim, float factor, int interleaved,
+                    void* out, int64_t out_stride, hipStream_t stream) {
+  if (!x || !out) return fail(QLQ_ERR_INVALID_ARG, "null pointer");
+  if (qlq_status st = check_heads(T, H, 0, D, 8)) return st;
+  if (qlq_status st = check_rotary(positions, inv_freq, rotary_dim, D, factor)) return st;
+  if (qlq_status st = check_stride(x_stride, T, H, D, "x")) return st;
+  if (qlq_status st = check_stride(out_stride, T, H, D, "out")) return st;
+  if (x == out && x_stride != out_stride && T > 1)
+    return fail(QLQ_ERR_INVALID_ARG, "rotating in place needs equal strides");
+  if (!aligned(x, 2) || !aligned(out, 2) || !aligned(positions, positions_64 ? 8 : 4))
+    return fail(QLQ_ERR_INVALID_ARG, "misaligned pointer");
+  qlq::RopeArgs a{};
+  a.q = static_cast<const uint16_t*>(x);
+  a.q_stride = x_stride;
+  a.q_out = static_cast<uint16_t*>(out);
+  a.q_out_stride = out_stride;
+  a.positions = positions;
+  a.pos64 = positions_64 ? 1 : 0;
+  a.inv_freq = inv_freq;
+  a.factor = factor;
+  a.R = (int)rotary_dim;
+  a.interleaved = interleaved ? 1 : 0;
+  a.T = (int)T;
+  a.Hq = (int)H;
+  a.D = (int)D;
+  a.vec_in = rows16(x, x_stride, D);
+  a.vec_out = rows16(out, out_stride, D);
+  return hip_status(qlq::launch_rope_kv(a, stream), "rope");
+}
+
+qlq_status qlq_rope_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                              int64_t v_stride, int64_t T, int64_t Hq, int64_t Hk, int64_t D, const void* positions,
+                              int positions_64, const double* inv_freq, int64_t rotary_dim, float factor,
+                              int interleaved, const void* slots, int slots_64, int64_t pool, void* k_codes,
+                              void* k_scales, void* v_codes, void* v_scales, void* q_out, int64_t q_out_stride,
+                              hipStream_t stream) {
+  if (!q || !k || !v || !q_out) return fail(QLQ_ERR_INVALID_ARG, "null pointer");
+  if (Hq < 1 || Hk < 1) return fail(QLQ_ERR_INVALID_ARG, "T, heads and D must be >= 1");
+  if (qlq_status st = check_heads(T, Hq, Hk, D, 32)) return st;
+  if (qlq_status st = check_rotary(positions, inv_freq, rotary_dim, D, factor)) return st;
+  if (qlq_status st = check_stride(q_stride, T, Hq, D, "q")) return st;
+  if (qlq_status st = check_stride(k_stride, T, Hk, D, "k")) return st;
+  if (qlq_status st = check_stride(v_stride, T, Hk, D, "v")) return st;
+  if (qlq_status st = check_stride(q_out_stride, T, Hq, D, "q_out")) return st;
+  if (q == q_out && q_stride != q_out_stride && T > 1)
+    return fail(QLQ_ERR_INVALID_ARG, "rotating in place needs equal strides");
+  if (qlq_status st = check_cache(k_codes, k_scales, v_codes, v_scales, slots, slots_64, pool)) return st;
+  if (!aligned(q, 2) || !aligned(k, 2) || !aligned(v, 2) || !aligned(q_out, 2) ||
+      !aligned(positions, positions_64 ? 8 : 4))
+    return fail(QLQ_ERR_INVALID_ARG, "misaligned pointer");
+  qlq::RopeArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.q_out_stride = q_out_stride;
+  a.positions = positions;
+  a.pos64 = positions_64 ? 1 : 0;
+  a.inv_freq = inv_freq;
+  a.factor = factor;
+  a.R = (int)rotary_dim;
+  a.interleaved = interleaved ? 1 : 0;
+  a.T = (int)T;
+  a.Hq = (int)Hq;
+  a.Hk = a.Hv = (int)Hk;
+  a.D = (int)D;
+  a.slots = slots;
+  a.slot64 = slots_64 ? 1 : 0;
+  a.pool = pool;
+  a.k_codes = static_cast<uint8_t*>(k_codes);
+  a.k_scales = static_cast<uint16_t*>(k_scales);
+  a.v_codes = static_cast<uint8_t*>(v_codes);
+  a.v_scales = static_cast<uint16_t*>(v_scales);
+  a.vec_in = rows16(q, q_stride, D) && rows16(k, k_stride, D) && rows16(v, v_stride, D);
+  a.vec_out = rows16(q_out, q_out_stride, D);
+  return hip_status(qlq::launch_rope_kv(a, stream), "rope_kv_append");
+}
+
+qlq_status qlq_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t T, int64_t H,
+                         int64_t D, const void* slots, int slots_64, int64_t pool, void* k_codes, void* k_scales,
+                         void* v_codes, void* v_scales, hipStream_t stream) {
+  if (!k || !v) return fail(QLQ_ERR_INVALID_ARG, "null pointer");
+  if (qlq_status st = check_heads(T, 0, H, D, 32)) return st;
+  if (qlq_status st = check_stride(k_stride, T, H, D, "k")) return st;
+  if (qlq_status st = check_stride(v_stride, T, H, D, "v")) return st;
+  if (qlq_status st = check_cache(k_codes, k_scales, v_codes, v_scales, slots, slots_64, pool)) return st;
+  if (!aligned(k, 2) || !aligned(v, 2)) return fail(QLQ_ERR_INVALID_ARG, "misaligned pointer");
+  qlq::RopeArgs a{};
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.T = (int)T;
+  a.Hk = a.Hv = (int)H;
+  a.D = (int)D;
+  a.slots = slots;
+  a.slot64 = slots_64 ? 1 : 0;
+  a.pool = pool;
+  a.k_codes = static_cast<uint8_t*>(k_codes);
+  a.k_scales = static_cast<uint16_t*>(k_scales);
+  a.v_codes = static_cast<uint8_t*>(v_codes);
+  a.v_scales = static_cast<uint16_t*>(v_scales);
+  a.vec_in = rows16(k, k_stride, D) && rows16(v, v_stride, D);
+  a.vec_out = 1;
+  return hip_status(qlq::launch_rope_kv(a, stream), "kv_append");
+}
+
+qlq_status qlq_kv_gather(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                         int64_t pool, int64_t H, int64_t D, const void* slots, int slots_64, int64_t n, void* k_bf16,
+                         void* v_bf16, hipStream_t stream) {
+  if (!k_bf16 || !v_bf16) return fail(QLQ_ERR_INVALID_ARG, "null pointer");
+  if (qlq_status st = check_kv_dims(n, H, D)) return st;
+  if (qlq_status st = check_cache(k_codes, k_scales, v_codes, v_scales, slots, slots_64, pool)) return st;
+  if (!aligned(k_bf16, 16) || !aligned(v_bf16, 16)) return fail(QLQ_ERR_INVALID_ARG, "outputs must be 16-byte aligned");
+  return hip_status(qlq::launch_kv_gather(k_codes, k_scales, v_codes, v_scales, pool, (int)H, (int)D, slots,
+                                          slots_64 ? 1 : 0, n, k_bf16, v_bf16, stream),
+                    "kv_gather");
+}
+
+// Attention workspace: a counter region of one fixed size for every plan (so that one call's
+// partial sums never land on another's counters), then the chunks' partial rows.
+constexpr size_t kAttnCounterBytes = 65536;
+
+static bool attn_dims_ok(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D) {
+  return T >= 1 && B >= 1 && Hq >= 1 && Hk >= 1 && T <= kMaxDim && B <= 65536 && Hq <= 4096 && Hq % Hk == 0 &&
+         (D == 32 || D == 64 || D == 96 || D == 128 || D == 192 || D == 256);
+}
+
+static size_t attn_partial_bytes(const qlq::KvAttnPlan& p, int64_t Hk, int64_t D) {
+  return p.split ? (size_t)p.items * (size_t)Hk * (size_t)p.tile_rows * (size_t)(D + 4) * 4 : 0;
+}
+
+size_t qlq_kv_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int one_each) {
+  if (!attn_dims_ok(T, B, Hq, Hk, D) || (one_each && T != B)) return 0;
+  const qlq::KvAttnPlan p = qlq::plan_kv_attention(T, B, Hk, Hq / Hk, one_each != 0);
+  return p.split ? kAttnCounterBytes + attn_partial_bytes(p, Hk, D) : 0;
+}
+
+qlq_status qlq_kv_attention(const void* q, int64_t q_stride, int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D,
+                            const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                            int64_t pool, const int32_t* block_table, int64_t max_pages, int64_t page_size,
+                            const int32_t* seq_lens, const int32_t* q_start, float scale, int causal, int64_t window,
+                            void* out, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  if (!q || !out || !block_table || !seq_lens) return fail(QLQ_ERR_INVALID_ARG, "null pointer");
+  if (T < 1 || B < 1 || Hq < 1 || Hk < 1 || max_pages < 1) return fail(QLQ_ERR_INVALID_ARG, "sizes must be >= 1");
+  if (Hq % Hk != 0) return fail(QLQ_ERR_INVALID_ARG, "query heads (%lld) must be a multiple of KV heads (%lld)",
+                                (long long)Hq, (long long)Hk);
+  if (D != 32 && D != 64 && D != 96 && D != 128 && D != 192 && D != 256)
+    return fail(QLQ_ERR_UNSUPPORTED, "head_dim D must be 32, 64, 96, 128, 192 or 256");
+  if (!attn_dims_ok(T, B, Hq, Hk, D))
+    return fail(QLQ_ERR_INVALID_ARG, "sizes above T = 2^24, B = 65536 or 4096 query heads are not supported");
+  if (!q_start && T != B) return fail(QLQ_ERR_INVALID_ARG, "without q_start, q must have one row per sequence");
+  if (qlq_status st = check_stride(q_stride, T, Hq, D, "q")) return st;
+  if (q_stride % 8 != 0 || !aligned(q, 16)) return fail(QLQ_ERR_INVALID_ARG, "q rows must be 16-byte aligned");
+  if (page_size < 1 || page_size > (1 << 20) || (page_size & (page_size - 1)) != 0)
+    return fail(QLQ_ERR_INVALID_ARG, "page_size must be a power of two, at most 2^20");
+  if (qlq_status st = check_cache(k_codes, k_scales, v_codes, v_scales, block_table, 0, pool)) return st;
+  if (!aligned(k_scales, 16)) return fail(QLQ_ERR_INVALID_ARG, "cache scales must be 16-byte aligned");
+  if (pool % page_size != 0) return fail(QLQ_ERR_INVALID_ARG, "the cache's slots must be a multiple of page_size");
+  if (max_pages * page_size >= (int64_t(1) << 31) - 65536)
+    return fail(QLQ_ERR_INVALID_ARG, "max_pages * page_size must be below 2^31 - 65536");
+  if (!std::isfinite(scale)) return fail(QLQ_ERR_INVALID_ARG, "scale must be finite");
+  if (window < 0 || window >= (int64_t(1) << 30)) return fail(QLQ_ERR_INVALID_ARG, "window must be 0 .. 2^30 - 1");
+  if (window > 0 && !causal) return fail(QLQ_ERR_INVALID_ARG, "a window needs causal attention");
+  if (!aligned(out, 16) || !aligned(seq_lens, 4) || !aligned(q_start, 4) || !aligned(lse, 4))
+    return fail(QLQ_ERR_INVALID_ARG, "misaligned pointer");
+  const qlq::KvAttnPlan p = qlq::plan_kv_attention(T, B, Hk, Hq / Hk, q_start == nullptr);
+  const size_t partial = attn_partial_bytes(p, Hk, D);
+  if (p.grid >= (int64_t(1) << 31) || partial >= ((size_t)1 << 31) ||
+      (p.split && (size_t)p.items * (size_t)Hk * 4 > kAttnCounterBytes))
+    return fail(QLQ_ERR_UNSUPPORTED, "sizes too large for one call");
+  if (p.split) {
+    const size_t need = kAttnCounterBytes + partial;
+    if (!workspace || workspace_bytes < need)
+      return fail(QLQ_ERR_INVALID_ARG, "workspace too small: need %zu bytes, got %zu", need,
+                  workspace ? workspace_bytes : (size_t)0);
+    if (!aligned(workspace, 256)) return fail(QLQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  }
+  qlq::KvAttnArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = q_stride;
+  a.out = static_cast<uint16_t*>(out);
+  a.lse = lse;
+  a.k_codes = static_cast<const uint8_t*>(k_codes);
+  a.k_scales = static_cast<const uint16_t*>(k_scales);
+  a.v_codes = static_cast<const uint8_t*>(v_codes);
+  a.v_scales = static_cast<const uint16_t*>(v_scales);
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.q_start = q_start;
+  a.T = (int)T;
+  a.B = (int)B;
+  a.Hq = (int)Hq;
+  a.Hk = (int)Hk;
+  a.G = (int)(Hq / Hk);
+  a.page_shift = 0;
+  while ((int64_t(1) << a.page_shift) < page_size) ++a.page_shift;
+  a.pages = (int)(pool >> a.page_shift);
+  a.max_pages = (int)max_pages;
+  a.max_tokens = (int)(max_pages * page_size);
+  a.scale = scale;
+  a.causal = causal ? 1 : 0;
+  a.window = (int)window;
+  a.split = p.split ? 1 : 0;
+  a.target = p.target;
+  a.chunk_step = p.chunk_step;
+  a.tile_rows = p.tile_rows;
+  if (p.split) {
+    a.counters = static_cast<uint32_t*>(workspace);
+    a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAttnCounterBytes);
+    a.partials_bytes = (uint32_t)partial;
+  }
+  return hip_status(qlq::launch_kv_attention(a, p, (int)D, stream), "kv_attention");
+}
+
 // ------------------------------------------------------------------ test hooks
 
 int qlq_scale_is_calibrated(float s) { return calibrated_scale(s) ? 1 : 0; }

@@ -78,6 +78,68 @@ hipError_t launch_kv_dequantize(const void* kq, const void* ks, const void* vq, 
 hipError_t launch_quant_act_dynamic(const void* x, int M, int K, int qtype, void* xq, float* x_scale,
                                    hipStream_t st);
 
+// RMS norm (rms_norm.hip).  out: 0 bf16, 1 codes at input_scale, 2 codes at the row's own scale.
+hipError_t launch_rms_norm(const void* x, const void* residual, const void* w, int M, int K, float eps, int out,
+                           int qtype, float input_scale, void* y, float* y_scale, void* residual_out, hipStream_t st);
+
+// Rotary positions and cache writing (rope_kv.hip).  Token t's head rows: Hq of q (rotated to
+// q_out), Hk of k (rotated, stored), Hv (Hk or 0) of v (stored); strides are per token, in elements.
+struct RopeArgs {
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  uint16_t* q_out;
+  int64_t q_out_stride;
+  const void* positions;       // int32 or int64 [T]
+  int pos64;
+  const double* inv_freq;      // [R / 2]
+  float factor;
+  int R, interleaved;          // rotated channels (0: none)
+  int T, Hq, Hk, Hv, D;
+  const void* slots;           // int32 or int64 [T]
+  int slot64;
+  int64_t pool;                // slots of the cache
+  uint8_t* k_codes;
+  uint16_t* k_scales;
+  uint8_t* v_codes;
+  uint16_t* v_scales;
+  int vec_in, vec_out;         // 16-byte aligned rows
+};
+hipError_t launch_rope_kv(const RopeArgs& a, hipStream_t st);
+hipError_t launch_kv_gather(const void* kq, const void* ks, const void* vq, const void* vs, int64_t pool, int H, int D,
+                            const void* slots, int slot64, int64_t n, void* ko, void* vo, hipStream_t st);
+
+// Attention over the paged cache (kv_attention.hip).
+struct KvAttnArgs {
+  const uint16_t* q;           // bf16, token stride q_stride elements
+  int64_t q_stride;
+  uint16_t* out;               // bf16 [T, Hq, D]
+  float* lse;                  // fp32 [T, Hq] or null
+  const uint8_t* k_codes;
+  const uint16_t* k_scales;
+  const uint8_t* v_codes;
+  const uint16_t* v_scales;
+  const int32_t* block_table;  // [B, max_pages]
+  const int32_t* seq_lens;     // [B]
+  const int32_t* q_start;      // [B + 1] or null (one query token per sequence)
+  int T, B, Hq, Hk, G;
+  int page_shift, pages, max_pages, max_tokens;
+  float scale;
+  int causal, window;
+  int split, target, chunk_step, tile_rows;
+  uint32_t* counters;
+  float* partials;
+  uint32_t partials_bytes;
+};
+struct KvAttnPlan {
+  int R = 1, waves = 8;        // 16-row subtiles per workgroup, waves per workgroup
+  bool split = false;          // token chunks joined across workgroups
+  int target = 1;              // chunks wanted per KV head, all sequences together
+  int chunk_step = 0, tile_rows = 0;
+  int64_t items = 0, grid = 0;
+};
+KvAttnPlan plan_kv_attention(int64_t T, int64_t B, int64_t Hk, int64_t G, bool one_each);
+hipError_t launch_kv_attention(const KvAttnArgs& a, const KvAttnPlan& p, int D, hipStream_t st);
+
 // Raises kernel k's dynamic-LDS limit to `bytes` on the current device, once per
 // device (bit d of `done` records device d; devices past 63 set it every call).
 inline hipError_t set_lds_limit(const void* k, int bytes, std::atomic<uint64_t>& done) {

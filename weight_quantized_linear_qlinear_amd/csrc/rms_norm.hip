@@ -1,0 +1,257 @@
+// RMS norm with the residual's addition, to bf16 or straight to the next linear's 8-bit codes.
+//
+//   h = x + residual (fp32, not rounded; residual_out = bf16(h)),
+//   rho = 1 / sqrt(mean_k h^2 + eps),   y = h * rho * w   (fp32),
+//   out: bf16(y)  |  sat(rne(y / input_scale))  |  s = absmax_k |y| / qmax, sat(rne(y / s)).
+//
+// The codes are taken from the fp32 y: one rounding, where a norm to bf16 followed by the
+// quantizer has two (and two more passes over the rows).  Sums and the statistics are fp32.
+// The division of the codes is RcpDiv's (an fp32 quotient to within one ulp) for scales in
+// [2^-100, 2^100], the IEEE one outside.
+//
+// Bound by HBM for many rows (2 K bytes of x, 2 K of the residual in and out, K of codes per
+// row) and by latency for few: a row is read once, kept in registers as fp32 (8 elements per
+// 16-byte chunk, NC chunks per thread) and written once.
+#include "qlq_device.h"
+#include "qlq_launch.h"
+
+namespace qlq {
+
+namespace {
+
+enum NormOut : int { kNormBf16 = 0, kNormStatic = 1, kNormDynamic = 2 };
+
+struct NormArgs {
+  const uint16_t* x;
+  const uint16_t* res;       // or null
+  const uint16_t* w;
+  void* y;                   // bf16 [M,K] or codes [M,K]; may be x or res (bf16)
+  float* y_scale;            // [M], dynamic only
+  uint16_t* res_out;         // or null; may be x or res
+  int M, K;
+  float eps, input_scale;
+  int fp8;
+};
+
+__device__ __forceinline__ float wave_sum(float v) {
+  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+
+__device__ __forceinline__ float wave_absmax(float v) {
+  for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
+  return v;
+}
+
+__device__ __forceinline__ bool rcp_scale(float s) { return s >= 0x1p-100f && s <= 0x1p100f; }
+
+__device__ __forceinline__ uint32_t code1(float v, int fp8) {
+  return fp8 ? f32_to_e4m3_sat(v) : f32_to_i8_sat(v);
+}
+
+template <class DIV>
+__device__ __forceinline__ uint32_t code4(const float* v, int fp8, const DIV& dv) {
+  const float a = dv(v[0]), b = dv(v[1]), c = dv(v[2]), d = dv(v[3]);
+  if (fp8) return f32x4_to_e4m3x4_sat(a, b, c, d);
+  return f32_to_i8_sat(a) | (f32_to_i8_sat(b) << 8) | (f32_to_i8_sat(c) << 16) | (f32_to_i8_sat(d) << 24);
+}
+
+struct IeeeDiv {
+  float s;
+  __device__ __forceinline__ explicit IeeeDiv(float s_) : s(s_) {}
+  __device__ __forceinline__ float operator()(float x) const { return x / s; }
+};
+
+// A workgroup's sum or maximum per row of T threads (T = 64: a wave; else through `red`).
+template <int T, bool MAX>
+__device__ __forceinline__ float row_reduce(float v, float* red) {
+  v = MAX ? wave_absmax(v) : wave_sum(v);
+  if constexpr (T > 64) {
+    const int w = threadIdx.x >> 6;
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[w] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int i = 1; i < T / 64; ++i) v = MAX ? fmaxf(v, red[i]) : v + red[i];
+  }
+  return v;
+}
+
+// T threads per row (64: four rows per workgroup of 256; 256 or 1024: one row per workgroup),
+// up to NC chunks of 8 elements per thread: K <= 8 T NC, K % 8 == 0, aligned pointers.
+template <int OUT, int T, int NC>
+__global__ __launch_bounds__(T == 64 ? 256 : T) void rms_norm_kernel(NormArgs a) {
+  constexpr int RPW = T == 64 ? 4 : 1;
+  __shared__ float red[T > 64 ? T / 64 : 1];
+  const int t = T == 64 ? (threadIdx.x & 63) : threadIdx.x;
+  const int m = blockIdx.x * RPW + (T == 64 ? (threadIdx.x >> 6) : 0);
+  if (m >= a.M) return;                                       // whole waves; T > 64 has no idle row
+  const int nv = a.K / 8;
+  const int64_t base = (int64_t)m * a.K;
+  u32x4 xr[NC], rr[NC], wr[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int i = t + c * T;
+    const bool in = i < nv;
+    xr[c] = in ? ld16_stream(a.x + base + i * 8) : (u32x4){0u, 0u, 0u, 0u};
+    if (a.res) rr[c] = in ? ld16_stream(a.res + base + i * 8) : (u32x4){0u, 0u, 0u, 0u};
+  }
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int i = t + c * T;
+    wr[c] = i < nv ? ld16(a.w + i * 8) : (u32x4){0u, 0u, 0u, 0u};
+  }
+  float h[NC][8];
+  float ss = 0.0f;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const uint32_t xd[4] = {xr[c].x, xr[c].y, xr[c].z, xr[c].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      h[c][2 * e] = bf16_bits_to_f32(xd[e] & 0xFFFF);
+      h[c][2 * e + 1] = bf16_bits_to_f32(xd[e] >> 16);
+    }
+    if (a.res) {
+      const uint32_t rd[4] = {rr[c].x, rr[c].y, rr[c].z, rr[c].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        h[c][2 * e] += bf16_bits_to_f32(rd[e] & 0xFFFF);
+        h[c][2 * e + 1] += bf16_bits_to_f32(rd[e] >> 16);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(h[c][e], h[c][e], ss);
+  }
+  ss = row_reduce<T, false>(ss, red);
+  const float rho = 1.0f / sqrtf(ss / (float)a.K + a.eps);
+  if (a.res_out) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int i = t + c * T;
+      if (i < nv)
+        st16(a.res_out + base + i * 8, (u32x4){pack_bf16x2(h[c][0], h[c][1]), pack_bf16x2(h[c][2], h[c][3]),
+                                               pack_bf16x2(h[c][4], h[c][5]), pack_bf16x2(h[c][6], h[c][7])});
+    }
+  }
+  float am = 0.0f;
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const uint32_t wd[4] = {wr[c].x, wr[c].y, wr[c].z, wr[c].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      h[c][2 * e] = h[c][2 * e] * rho * bf16_bits_to_f32(wd[e] & 0xFFFF);
+      h[c][2 * e + 1] = h[c][2 * e + 1] * rho * bf16_bits_to_f32(wd[e] >> 16);
+      if constexpr (OUT == kNormDynamic)
+        am = fmaxf(am, fmaxf(fabsf(h[c][2 * e]), fabsf(h[c][2 * e + 1])));
+    }
+  }
+  if constexpr (OUT == kNormBf16) {
+    uint16_t* y = static_cast<uint16_t*>(a.y) + base;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const int i = t + c * T;
+      if (i < nv)
+        st16(y + i * 8, (u32x4){pack_bf16x2(h[c][0], h[c][1]), pack_bf16x2(h[c][2], h[c][3]),
+                                pack_bf16x2(h[c][4], h[c][5]), pack_bf16x2(h[c][6], h[c][7])});
+    }
+  } else {
+    float s = a.input_scale;
+    if constexpr (OUT == kNormDynamic) {
+      am = row_reduce<T, true>(am, red);
+      s = am == 0.0f ? 1.0f : am / (a.fp8 ? 448.0f : 127.0f);
+      if (t == 0) a.y_scale[m] = s;
+    }
+    uint8_t* y = static_cast<uint8_t*>(a.y) + base;
+    auto emit = [&](const auto& dv) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        const int i = t + c * T;
+        if (i < nv)
+          *reinterpret_cast<u32x2*>(y + i * 8) = (u32x2){code4(h[c], a.fp8, dv), code4(h[c] + 4, a.fp8, dv)};
+      }
+    };
+    if (rcp_scale(s)) emit(RcpDivAny(s));
+    else emit(IeeeDiv(s));
+  }
+}
+
+// Any K and alignment: element by element, x and the residual read again by each pass.  Only
+// the last pass writes, each element by the thread that has just read it, so the outputs may
+// be the inputs here too.
+template <int OUT>
+__global__ __launch_bounds__(256) void rms_norm_any_kernel(NormArgs a) {
+  __shared__ float red[4];
+  const int t = threadIdx.x, m = blockIdx.x;
+  const int64_t base = (int64_t)m * a.K;
+  auto load = [&](int k) {
+    const float v = bf16_bits_to_f32(a.x[base + k]);
+    return a.res ? v + bf16_bits_to_f32(a.res[base + k]) : v;
+  };
+  float ss = 0.0f;
+  for (int k = t; k < a.K; k += 256) {
+    const float v = load(k);
+    ss = __builtin_fmaf(v, v, ss);
+  }
+  ss = row_reduce<256, false>(ss, red);
+  const float rho = 1.0f / sqrtf(ss / (float)a.K + a.eps);
+  float s = a.input_scale;
+  if constexpr (OUT == kNormDynamic) {
+    float am = 0.0f;
+    for (int k = t; k < a.K; k += 256) am = fmaxf(am, fabsf(load(k) * rho * bf16_bits_to_f32(a.w[k])));
+    am = row_reduce<256, true>(am, red);
+    s = am == 0.0f ? 1.0f : am / (a.fp8 ? 448.0f : 127.0f);
+    if (t == 0) a.y_scale[m] = s;
+  }
+  const bool rcp = OUT != kNormBf16 && rcp_scale(s);
+  const RcpDivAny dv(rcp ? s : 1.0f);
+  for (int k = t; k < a.K; k += 256) {
+    const float v = load(k);
+    const float y = v * rho * bf16_bits_to_f32(a.w[k]);
+    if (a.res_out) a.res_out[base + k] = (uint16_t)(pack_bf16x2(v, v) & 0xFFFF);
+    if constexpr (OUT == kNormBf16) static_cast<uint16_t*>(a.y)[base + k] = (uint16_t)(pack_bf16x2(y, y) & 0xFFFF);
+    else static_cast<uint8_t*>(a.y)[base + k] = (uint8_t)code1(rcp ? dv(y) : y / s, a.fp8);
+  }
+}
+
+template <int OUT>
+hipError_t launch_norm(const NormArgs& a, bool vec, hipStream_t st) {
+  const int nv = a.K / 8;
+  if (!vec || nv > 1024 * 8) {
+    rms_norm_any_kernel<OUT><<<a.M, 256, 0, st>>>(a);
+  } else if (a.M >= 1024 && nv <= 64 * 8) {
+    // Many rows: a wave per row, no barrier.
+    const int g = (a.M + 3) / 4;
+    if (nv <= 64) rms_norm_kernel<OUT, 64, 1><<<g, 256, 0, st>>>(a);
+    else if (nv <= 128) rms_norm_kernel<OUT, 64, 2><<<g, 256, 0, st>>>(a);
+    else if (nv <= 256) rms_norm_kernel<OUT, 64, 4><<<g, 256, 0, st>>>(a);
+    else rms_norm_kernel<OUT, 64, 8><<<g, 256, 0, st>>>(a);
+  } else if (nv <= 256 * 8) {
+    if (nv <= 256) rms_norm_kernel<OUT, 256, 1><<<a.M, 256, 0, st>>>(a);
+    else if (nv <= 512) rms_norm_kernel<OUT, 256, 2><<<a.M, 256, 0, st>>>(a);
+    else if (nv <= 1024) rms_norm_kernel<OUT, 256, 4><<<a.M, 256, 0, st>>>(a);
+    else rms_norm_kernel<OUT, 256, 8><<<a.M, 256, 0, st>>>(a);
+  } else {
+    rms_norm_kernel<OUT, 1024, 8><<<a.M, 1024, 0, st>>>(a);
+  }
+  return hipGetLastError();
+}
+
+bool al(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace
+
+hipError_t launch_rms_norm(const void* x, const void* residual, const void* w, int M, int K, float eps, int out,
+                           int qtype, float input_scale, void* y, float* y_scale, void* residual_out, hipStream_t st) {
+  NormArgs a{static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(residual), static_cast<const uint16_t*>(w),
+             y, y_scale, static_cast<uint16_t*>(residual_out), M, K, eps, input_scale, qtype == kFp8 ? 1 : 0};
+  const bool vec = K % 8 == 0 && al(x, 16) && al(residual, 16) && al(w, 16) && al(residual_out, 16) &&
+                   al(y, out == kNormBf16 ? 16 : 8);
+  switch (out) {
+    case kNormBf16: return launch_norm<kNormBf16>(a, vec, st);
+    case kNormStatic: return launch_norm<kNormStatic>(a, vec, st);
+    default: return launch_norm<kNormDynamic>(a, vec, st);
+  }
+}
+
+}  // namespace qlq
