@@ -362,7 +362,7 @@ qlq_status qlq_kv_gather(const void* k_codes, const void* k_scales, const void* 
  * fp32 accumulation, weights in 11 bits.  A row that sees no token gives zeros and lse -inf;
  * rows of q outside every sequence are left as they were in out and lse.
  * q bf16 [T, Hq, D], token stride in elements (a multiple of 8); out bf16 [T, Hq, D] dense; D 32,
- * 64, 96, 128, 192 or 256; page_size a power of two; pool a multiple of it.  block_table int32
+ * 64, 96, 128, 192 or 256; page_size a power of two, 16 .. 2^20; pool a multiple of it.  block_table int32
  * [B, max_pages], seq_lens int32 [B], q_start int32 [B + 1], on the device: lengths are read there
  * (the host does not wait for them) and bounded by 0 .. max_pages * page_size and 0 .. T; a token
  * whose page is outside the pool is left out, never read.

@@ -143,7 +143,7 @@ def test_attention_refusals():
     attn("misaligned", vs=ODD)
     attn("misaligned", sl=ctypes.c_void_p(0x10002))
     attn("misaligned", lse=ctypes.c_void_p(0x10002))
-    for page in (0, 3, 24, 1 << 21):
+    for page in (0, 3, 8, 24, 1 << 21):
         attn("power of two", page=page)
     attn("multiple of page_size", pool=1000)
     attn("2^31", mp=1 << 27, page=16)
@@ -152,21 +152,25 @@ def test_attention_refusals():
     attn("window", window=-1)
     attn("causal", window=5, causal=0)
     need = qlq.kv_attention_workspace_bytes(4, 4, 32, 8, 128)
-    assert need > 65536
-    attn("workspace", wb=need - 1)
+    assert need > 131072
+    attn("workspace", wb=need - 256)
     attn("workspace", ws=None)
     attn("256-byte", ws=ctypes.c_void_p(0x10010))
     attn("not supported", B=65537, T=65537)
+    attn("not supported", Hq=1032, Hk=8, qs=1032 * 128)
+    attn("too large", status=2, B=60000, T=60000, mp=1 << 17, page=16)
 
 
 def test_workspace_sizes():
     w = qlq.kv_attention_workspace_bytes
     assert w(0, 0, 32, 8, 128) == 0 and w(4, 4, 32, 5, 128) == 0 and w(4, 4, 32, 8, 100) == 0
     assert w(5, 4, 32, 8, 128) == 0 and w(5, 4, 32, 8, 128, one_each=False) > 0
-    assert w(100000, 4, 32, 8, 128, one_each=False) == 0       # enough query tiles: no token chunks
     for B in (1, 7, 64, 300, 1000):
-        for Hq, Hk in ((1, 1), (28, 4), (32, 8), (64, 1), (128, 128), (4096, 4096)):
-            assert w(B, B, Hq, Hk, 128) < (1 << 31)
+        for Hq, Hk in ((1, 1), (28, 4), (32, 8), (64, 1), (128, 128), (1023, 1023), (1024, 1024)):
+            for D in (32, 128, 256):
+                for one in (True, False):
+                    assert 131072 < w(B, B, Hq, Hk, D, one) < (1 << 31)
+                    assert w(B, B, Hq, Hk, D, one) % 256 == 0
 
 
 def test_binding_refusals():

@@ -786,21 +786,21 @@ def kv_attention_workspace_bytes(T: int, B: int, Hq: int, Hk: int, D: int, one_e
     return int(lib().qlq_kv_attention_workspace_bytes(T, B, Hq, Hk, D, int(one_each)))
 
 
+_ATTENTION_COUNTER_BYTES = 131072
 _attention_workspaces: dict = {}
 
 
-def _attention_workspace(dev: torch.device, nbytes: int) -> torch.Tensor | None:
-    """A zero-filled workspace of this stream, grown on demand; inside a graph capture, one of the graph's own
-    (its zero fill is recorded with it), so that graphs and streams never share one."""
-    if nbytes == 0:
-        return None
-    if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=dev)
+def _attention_workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
+    """A workspace of this stream with its counters zeroed, grown on demand; inside a graph capture, one of the
+    graph's own (its zero fill is recorded with it), so that graphs and streams never share one."""
+    capturing = torch.cuda.is_current_stream_capturing()
     key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
-    ws = _attention_workspaces.get(key)
+    ws = None if capturing else _attention_workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
-        ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
-        _attention_workspaces[key] = ws
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        ws[:_ATTENTION_COUNTER_BYTES].zero_()
+        if not capturing:
+            _attention_workspaces[key] = ws
     return ws
 
 
@@ -811,7 +811,7 @@ def kv_attention(q: torch.Tensor, cache: QuantizedKV, block_table: torch.Tensor,
     """Attention of q [T, Hq, D] bf16 over a paged cache (kv_append): out bf16 [T, Hq, D].
 
     block_table int32 [B, pages] holds each sequence's page numbers (token t is cache entry
-    block_table[b][t // page_size] * page_size + t % page_size), seq_lens int32 [B] its cached tokens.  Without
+    block_table[b][t // page_size] * page_size + t % page_size; page_size a power of two from 16), seq_lens int32 [B] its cached tokens.  Without
     q_start, row b of q is the last token of sequence b; with q_start int32 [B + 1], rows q_start[b] ..
     q_start[b+1]-1 are its last tokens.  A query sees the tokens up to its own (causal), and no more than `window`
     of them if that is not 0.  scale defaults to D^-0.5; lse fp32 [T, Hq], if given, receives log sum exp of the

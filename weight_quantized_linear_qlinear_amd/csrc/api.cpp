@@ -978,22 +978,24 @@ qlq_status qlq_kv_gather(const void* k_codes, const void* k_scales, const void* 
 }
 
 // Attention workspace: a counter region of one fixed size for every plan (so that one call's
-// partial sums never land on another's counters), then the chunks' partial rows.
-constexpr size_t kAttnCounterBytes = 65536;
+// partial sums never land on another's counters), then two partial tiles per wave.  Counters: one
+// per level of joining (three), slot and head.
+constexpr size_t kAttnCounterBytes = 131072;
+constexpr int64_t kMaxAttnHeads = 1024;
 
 static bool attn_dims_ok(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D) {
-  return T >= 1 && B >= 1 && Hq >= 1 && Hk >= 1 && T <= kMaxDim && B <= 65536 && Hq <= 4096 && Hq % Hk == 0 &&
+  return T >= 1 && B >= 1 && Hq >= 1 && Hk >= 1 && T <= kMaxDim && B <= 65536 && Hq <= kMaxAttnHeads && Hq % Hk == 0 &&
          (D == 32 || D == 64 || D == 96 || D == 128 || D == 192 || D == 256);
 }
 
 static size_t attn_partial_bytes(const qlq::KvAttnPlan& p, int64_t Hk, int64_t D) {
-  return p.split ? (size_t)p.items * (size_t)Hk * (size_t)p.tile_rows * (size_t)(D + 4) * 4 : 0;
+  return (size_t)p.waves * 2 * (size_t)Hk * (size_t)p.tile_rows * (size_t)(D + 4) * 4;
 }
 
 size_t qlq_kv_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int one_each) {
   if (!attn_dims_ok(T, B, Hq, Hk, D) || (one_each && T != B)) return 0;
   const qlq::KvAttnPlan p = qlq::plan_kv_attention(T, B, Hk, Hq / Hk, one_each != 0);
-  return p.split ? kAttnCounterBytes + attn_partial_bytes(p, Hk, D) : 0;
+  return (kAttnCounterBytes + attn_partial_bytes(p, Hk, D) + 255) / 256 * 256;
 }
 
 qlq_status qlq_kv_attention(const void* q, int64_t q_stride, int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D,
@@ -1008,12 +1010,12 @@ qlq_status qlq_kv_attention(const void* q, int64_t q_stride, int64_t T, int64_t 
   if (D != 32 && D != 64 && D != 96 && D != 128 && D != 192 && D != 256)
     return fail(QLQ_ERR_UNSUPPORTED, "head_dim D must be 32, 64, 96, 128, 192 or 256");
   if (!attn_dims_ok(T, B, Hq, Hk, D))
-    return fail(QLQ_ERR_INVALID_ARG, "sizes above T = 2^24, B = 65536 or 4096 query heads are not supported");
+    return fail(QLQ_ERR_INVALID_ARG, "sizes above T = 2^24, B = 65536 or 1024 query heads are not supported");
   if (!q_start && T != B) return fail(QLQ_ERR_INVALID_ARG, "without q_start, q must have one row per sequence");
   if (qlq_status st = check_stride(q_stride, T, Hq, D, "q")) return st;
   if (q_stride % 8 != 0 || !aligned(q, 16)) return fail(QLQ_ERR_INVALID_ARG, "q rows must be 16-byte aligned");
-  if (page_size < 1 || page_size > (1 << 20) || (page_size & (page_size - 1)) != 0)
-    return fail(QLQ_ERR_INVALID_ARG, "page_size must be a power of two, at most 2^20");
+  if (page_size < 16 || page_size > (1 << 20) || (page_size & (page_size - 1)) != 0)
+    return fail(QLQ_ERR_INVALID_ARG, "page_size must be a power of two, 16 .. 2^20");
   if (qlq_status st = check_cache(k_codes, k_scales, v_codes, v_scales, block_table, 0, pool)) return st;
   if (!aligned(k_scales, 16)) return fail(QLQ_ERR_INVALID_ARG, "cache scales must be 16-byte aligned");
   if (pool % page_size != 0) return fail(QLQ_ERR_INVALID_ARG, "the cache's slots must be a multiple of page_size");
@@ -1025,17 +1027,14 @@ qlq_status qlq_kv_attention(const void* q, int64_t q_stride, int64_t T, int64_t 
   if (!aligned(out, 16) || !aligned(seq_lens, 4) || !aligned(q_start, 4) || !aligned(lse, 4))
     return fail(QLQ_ERR_INVALID_ARG, "misaligned pointer");
   const qlq::KvAttnPlan p = qlq::plan_kv_attention(T, B, Hk, Hq / Hk, q_start == nullptr);
-  const size_t partial = attn_partial_bytes(p, Hk, D);
-  if (p.grid >= (int64_t(1) << 31) || partial >= ((size_t)1 << 31) ||
-      (p.split && (size_t)p.items * (size_t)Hk * 4 > kAttnCounterBytes))
+  const size_t partial = attn_partial_bytes(p, Hk, D), need = kAttnCounterBytes + partial;
+  if (p.tiles * (max_pages * page_size / 32 + 1) >= (int64_t(1) << 31) || partial >= ((size_t)1 << 31) ||
+      (size_t)p.waves * 2 * (size_t)Hk * 12 > kAttnCounterBytes || p.waves > 4096)
     return fail(QLQ_ERR_UNSUPPORTED, "sizes too large for one call");
-  if (p.split) {
-    const size_t need = kAttnCounterBytes + partial;
-    if (!workspace || workspace_bytes < need)
-      return fail(QLQ_ERR_INVALID_ARG, "workspace too small: need %zu bytes, got %zu", need,
-                  workspace ? workspace_bytes : (size_t)0);
-    if (!aligned(workspace, 256)) return fail(QLQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  }
+  if (!workspace || workspace_bytes < need)
+    return fail(QLQ_ERR_INVALID_ARG, "workspace too small: need %zu bytes, got %zu", need,
+                workspace ? workspace_bytes : (size_t)0);
+  if (!aligned(workspace, 256)) return fail(QLQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   qlq::KvAttnArgs a{};
   a.q = static_cast<const uint16_t*>(q);
   a.q_stride = q_stride;
@@ -1061,15 +1060,13 @@ qlq_status qlq_kv_attention(const void* q, int64_t q_stride, int64_t T, int64_t 
   a.scale = scale;
   a.causal = causal ? 1 : 0;
   a.window = (int)window;
-  a.split = p.split ? 1 : 0;
-  a.target = p.target;
-  a.chunk_step = p.chunk_step;
+  a.parts = p.parts;
   a.tile_rows = p.tile_rows;
-  if (p.split) {
-    a.counters = static_cast<uint32_t*>(workspace);
-    a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAttnCounterBytes);
-    a.partials_bytes = (uint32_t)partial;
-  }
+  a.hw_shift = p.hw_shift;
+  a.level_counters = (int)(p.waves * 2 * Hk);
+  a.counters = static_cast<uint32_t*>(workspace);
+  a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAttnCounterBytes);
+  a.partials_bytes = (uint32_t)partial;
   return hip_status(qlq::launch_kv_attention(a, p, (int)D, stream), "kv_attention");
 }
 

@@ -14,18 +14,20 @@
 // whose absolute error stays under 2^-25 of it), and the weights' rounding to 11 bits is the
 // only other one (2^-12 of a weight; the output's own rounding to bf16 is 2^-9).
 //
-// Layout.  A workgroup takes one KV head, 16 R query rows (nq x G rows packed, so that the
-// heads of a group share every K and V load) and a run of tokens; its NW waves take 32 tokens
-// each in turn, on their own, and are summed through LDS at the end.  S^T = K Q^T (tokens are
+// Layout.  A wave takes one KV head, 16 R query rows (nq x G rows packed, so that the heads of
+// a group share every K and V load) and a run of tokens, 32 at a time, on its own; the waves of
+// a workgroup take neighbouring heads, whose entries lie side by side.  S^T = K Q^T (tokens are
 // the rows): lane l holds query l % 16 and tokens 4 (l / 16) + j, which is the operand that
 // O^T = V^T P^T wants, so the weights never cross lanes.  V^T needs, per lane, one channel of
 // eight tokens: each lane loads the same few channels of its eight tokens and transposes bytes
 // pairwise while converting.
 //
 // Work is cut on the device, from the lengths it finds there (the host knows none of them and
-// waits for nothing): every workgroup sums the sequences' tokens, derives one chunk length
-// that gives about `target` workgroups, and finds its (sequence, query tile, chunk).  Chunks
-// of one tile are joined by the last workgroup to finish, in the order of the chunks.
+// waits for nothing): every wave sums the sequences' tiles of 32 tokens and takes an equal run
+// of them, so that ragged batches load the chip evenly.  Tiles that several waves share are
+// joined by the last to finish, in the order of the chunks.
+#include <type_traits>
+
 #include "qlq_device.h"
 #include "qlq_launch.h"
 
@@ -67,8 +69,17 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t w) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI));
 }
 
+// Memory that no kernel writes meanwhile, read through the scalar cache.
+typedef __attribute__((address_space(4))) const int32_t ConstInt;
+
+template <bool NT, class T>
+__device__ __forceinline__ T ld(const T* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(p);
+  return *p;
+}
+
 // BYTES (2, 4, 8 or 16) at p, aligned to BYTES, as dwords (2 bytes: the low half).
-template <int BYTES>
+template <int BYTES, bool NT = false>
 struct Raw {
   static constexpr int N = BYTES < 4 ? 1 : BYTES / 4;
   uint32_t d[N];
@@ -78,10 +89,10 @@ struct Raw {
     } else if constexpr (BYTES == 4) {
       d[0] = *reinterpret_cast<const uint32_t*>(p);
     } else if constexpr (BYTES == 8) {
-      const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+      const u32x2 v = ld<NT>(reinterpret_cast<const u32x2*>(p));
       d[0] = v.x, d[1] = v.y;
     } else {
-      const u32x4 v = ld16(p);
+      const u32x4 v = ld<NT>(reinterpret_cast<const u32x4*>(p));
       d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
     }
   }
@@ -100,8 +111,8 @@ struct Pieces {
 };
 
 // Products of one piece: o[n][r] += V^T[channel 2 P c + n][8 tokens] P^T[8 tokens][query].
-template <int P, int R>
-__device__ __forceinline__ void pv_piece(const Raw<2 * P> (&v)[8], const f16x8 (&w)[R], f32x4 (*o)[R]) {
+template <int P, int R, bool NT>
+__device__ __forceinline__ void pv_piece(const Raw<2 * P, NT> (&v)[8], const f16x8 (&w)[R], f32x4 (*o)[R]) {
   constexpr int DW = Raw<2 * P>::N;
 #pragma unroll
   for (int d = 0; d < DW; ++d) {
@@ -122,38 +133,38 @@ __device__ __forceinline__ void pv_piece(const Raw<2 * P> (&v)[8], const f16x8 (
 #pragma unroll
       for (int r = 0; r < R; ++r) o[4 * d + n][r] = mfma_f16_k32(av, w[r], o[4 * d + n][r]);
     }
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
-// One token's K scales (NG fp16).
+// One token's K scales, NG fp16 as raw dwords (aligned to their size's largest power of two).
 template <int NG>
 struct KScales {
-  float s[NG];
+  static constexpr int N = (NG + 1) / 2;
+  uint32_t d[N];
   __device__ __forceinline__ void load(const uint16_t* p) {
-    if constexpr (NG % 8 == 0) {
+    if constexpr (NG == 8) {
       const u32x4 v = ld16(p);
-      s[0] = f16_lo(v.x), s[1] = f16_hi(v.x), s[2] = f16_lo(v.y), s[3] = f16_hi(v.y);
-      s[4] = f16_lo(v.z), s[5] = f16_hi(v.z), s[6] = f16_lo(v.w), s[7] = f16_hi(v.w);
+      d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
     } else if constexpr (NG == 4) {
       const u32x2 v = *reinterpret_cast<const u32x2*>(p);
-      s[0] = f16_lo(v.x), s[1] = f16_hi(v.x), s[2] = f16_lo(v.y), s[3] = f16_hi(v.y);
+      d[0] = v.x, d[1] = v.y;
     } else if constexpr (NG % 2 == 0) {
 #pragma unroll
-      for (int i = 0; i < NG; i += 2) {
-        const uint32_t v = *reinterpret_cast<const uint32_t*>(p + i);
-        s[i] = f16_lo(v), s[i + 1] = f16_hi(v);
-      }
+      for (int i = 0; i < N; ++i) d[i] = *reinterpret_cast<const uint32_t*>(p + 2 * i);
     } else {
 #pragma unroll
-      for (int i = 0; i < NG; ++i) s[i] = f16_lo(p[i]);
+      for (int i = 0; i < N; ++i) d[i] = p[2 * i] | (2 * i + 1 < NG ? (uint32_t)p[2 * i + 1] << 16 : 0u);
     }
   }
+  __device__ __forceinline__ float get(int i) const { return i & 1 ? f16_hi(d[i / 2]) : f16_lo(d[i / 2]); }
 };
 
-// Sequence b: its query tokens, its cached tokens, and how many of those any query can see.
+// Sequence b: its query tokens, its cached tokens, and the first of those any query can see
+// (rounded down to a tile of 32).
 struct Extent {
   int qs, nq, L, begin;
-  __device__ __forceinline__ int range() const { return L - begin; }
+  __device__ __forceinline__ int units() const { return max(1, (L - begin + 31) >> 5); }   // tiles of 32 tokens
 };
 
 __device__ __forceinline__ Extent extent_of(const KvAttnArgs& a, int b) {
@@ -167,151 +178,242 @@ __device__ __forceinline__ Extent extent_of(const KvAttnArgs& a, int b) {
     e.nq = 1;
   }
   e.L = min(max(a.seq_lens[b], 0), a.max_tokens);
-  e.begin = (a.window > 0 && e.nq > 0) ? max(0, e.L - e.nq - a.window + 1) : 0;
-  e.begin = min(e.begin, e.L);
+  e.begin = a.window > 0 ? min(max(0, e.L - e.nq - a.window + 1), e.L) & ~31 : 0;
   return e;
 }
 
-__device__ __forceinline__ int64_t wave_sum64(int64_t v) {
-  for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
-  return v;
+// Cross-lane steps in the vector unit (no trip through LDS).
+template <int N>
+__device__ __forceinline__ int row_ror(int v) {               // within 16 lanes
+  return __builtin_amdgcn_mov_dpp(v, 0x120 + N, 0xf, 0xf, true);
 }
 
-__device__ __forceinline__ int wave_scan(int v, int lane) {   // inclusive
-  for (int off = 1; off < 64; off <<= 1) {
-    const int u = __shfl_up(v, off, 64);
-    if (lane >= off) v += u;
+template <class OP>
+__device__ __forceinline__ int row16(int v, OP op) {          // over 16 lanes, to each of them
+  v = op(v, row_ror<8>(v));
+  v = op(v, row_ror<4>(v));
+  v = op(v, row_ror<2>(v));
+  return op(v, row_ror<1>(v));
+}
+
+template <class OP>
+__device__ __forceinline__ int across16(int v, OP op) {       // over lanes l, l ^ 16, l ^ 32, l ^ 48
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = op((int)a[0], (int)a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return op((int)b[0], (int)b[1]);
+}
+
+struct AddI {
+  __device__ __forceinline__ int operator()(int a, int b) const { return a + b; }
+};
+struct MaxI {
+  __device__ __forceinline__ int operator()(int a, int b) const { return max(a, b); }
+};
+struct AddF {
+  __device__ __forceinline__ int operator()(int a, int b) const {
+    return __builtin_bit_cast(int, __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b));
   }
-  return v;
-}
-
-struct Item {
-  int b, qt, ch, nch, first;     // first: item index of chunk 0 of this (sequence, tile)
-  Extent e;
-  bool found;
+};
+struct MaxF {
+  __device__ __forceinline__ int operator()(int a, int b) const {
+    return __builtin_bit_cast(int, fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
+  }
 };
 
-// Finds item `item`: every wave on its own, 64 sequences at a time.
+__device__ __forceinline__ float max_across16(float v) {
+  return __builtin_bit_cast(float, across16(__builtin_bit_cast(int, v), MaxF()));
+}
+__device__ __forceinline__ float sum_across16(float v) {
+  return __builtin_bit_cast(float, across16(__builtin_bit_cast(int, v), AddF()));
+}
+__device__ __forceinline__ float max_row16(float v) {
+  return __builtin_bit_cast(float, row16(__builtin_bit_cast(int, v), MaxF()));
+}
+__device__ __forceinline__ float sum_row16(float v) {
+  return __builtin_bit_cast(float, row16(__builtin_bit_cast(int, v), AddF()));
+}
+
+__device__ __forceinline__ int wave_sum(int v) { return across16(row16(v, AddI()), AddI()); }
+__device__ __forceinline__ int wave_max(int v) { return across16(row16(v, MaxI()), MaxI()); }
+
+__device__ __forceinline__ int wave_scan(int v) {             // inclusive
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);    // row_shr 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast 15 into rows 1, 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast 31 into rows 2, 3
+  return v;
+}
+
+// The work of one KV head is a line of units (32 tokens of one query tile), tile after tile;
+// wave w of its waves takes units w U .. (w + 1) U - 1, whatever tiles they belong to.
+// `mine` is the extent of sequence `lane` (nq 0 past the last), kept for the first 64.
+struct Line {
+  int total, longest;            // units of all tiles, and of the longest one
+};
+
 template <int TR>
-__device__ __forceinline__ Item find_item(const KvAttnArgs& a, int item, int lane) {
-  Item it;
-  it.found = false;
-  int64_t C = (int64_t)1 << 40;
-  if (a.split) {
-    int64_t total = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 64) {
-      int64_t w = 0;
-      if (b0 + lane < a.B) {
-        const Extent e = extent_of(a, b0 + lane);
-        w = (int64_t)((e.nq * a.G + TR - 1) / TR) * e.range();
-      }
-      total += wave_sum64(w);
-    }
-    C = (total + a.target - 1) / a.target;
-    C = (C + a.chunk_step - 1) / a.chunk_step * a.chunk_step;
-    if (C < a.chunk_step) C = a.chunk_step;
+__device__ __forceinline__ Line line_of(const KvAttnArgs& a, const Extent& mine, int lane) {
+  Line r{0, 1};
+  for (int b0 = 0; b0 < a.B; b0 += 64) {
+    Extent e = mine;
+    if (b0) e = b0 + lane < a.B ? extent_of(a, b0 + lane) : Extent{};
+    const int n = (e.nq * a.G + TR - 1) / TR;
+    r.total += wave_sum(n * e.units());
+    r.longest = max(r.longest, wave_max(n ? e.units() : 1));
   }
+  r.total = __builtin_amdgcn_readfirstlane(r.total);
+  r.longest = __builtin_amdgcn_readfirstlane(r.longest);
+  return r;
+}
+
+struct Tile {
+  Extent e;
+  int b, qt;                     // sequence, query tile
+  int begin, units;              // its place on the line
+};
+
+// The tile that unit u belongs to (0 <= u < total): every wave on its own, 64 sequences at a time.
+template <int TR>
+__device__ __forceinline__ Tile tile_of(const KvAttnArgs& a, const Extent& mine, int u, int lane) {
+  Tile t{};
   int before = 0;
   for (int b0 = 0; b0 < a.B; b0 += 64) {
-    int n = 0, nch = 1;
-    Extent e{};
-    if (b0 + lane < a.B) {
-      e = extent_of(a, b0 + lane);
-      const int nqt = (e.nq * a.G + TR - 1) / TR;
-      nch = max(1, (int)((e.range() + C - 1) / C));
-      n = nqt * nch;
-    }
-    const int inc = before + wave_scan(n, lane);
-    const uint64_t hit = __ballot(n > 0 && item < inc && item >= inc - n);
+    Extent e = mine;
+    if (b0) e = b0 + lane < a.B ? extent_of(a, b0 + lane) : Extent{};
+    const int n = (e.nq * a.G + TR - 1) / TR * e.units();
+    const int inc = before + wave_scan(n);
+    const uint64_t hit = __ballot(u < inc && u >= inc - n);
     if (hit) {
-      const int src = __ffsll((unsigned long long)hit) - 1;
-      it.b = b0 + src;
-      it.nch = __shfl(nch, src, 64);
-      const int begin = __shfl(inc - n, src, 64), tiles = __shfl(n, src, 64) / it.nch;
-      const int rel = item - begin;
-      it.qt = tiles - 1 - rel / it.nch;                    // the longest causal tiles first
-      it.ch = rel % it.nch;
-      it.first = item - it.ch;
-      it.e.qs = __shfl(e.qs, src, 64);
-      it.e.nq = __shfl(e.nq, src, 64);
-      it.e.L = __shfl(e.L, src, 64);
-      it.e.begin = __shfl(e.begin, src, 64);
-      it.found = true;
-      return it;
+      const int src = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
+      auto of = [&](int v) { return __builtin_amdgcn_readlane(v, src); };
+      t.e.qs = of(e.qs);
+      t.e.nq = of(e.nq);
+      t.e.L = of(e.L);
+      t.e.begin = of(e.begin);
+      t.b = b0 + src;
+      t.units = t.e.units();
+      const int begin = of(inc - n);
+      t.qt = (u - begin) / t.units;
+      t.begin = begin + t.qt * t.units;
+      return t;
     }
-    before = __shfl(inc, 63, 64);
+    before = __builtin_amdgcn_readlane(inc, 63);
   }
-  return it;
+  return t;
 }
 
-// The row sums of the workgroup's waves, per 16-row subtile: acc[w][row][D + 4].
-template <int NG, int NW>
-struct Smem {
-  static constexpr int D = 32 * NG, LD = D + 4;
-  static constexpr int kMaxChunks = 256;
-  union {
-    float acc[NW][16][LD];
-    float f[16][kMaxChunks];
-    int slot[NW][2][32];
+// A wave's LDS: the token scales of its tile, or the factors of the chunks that it joins.
+constexpr int kJoin = 16;        // chunks joined at a time
+constexpr int kWaves = 4;
+
+template <int NG>
+union WaveLds {
+  struct {
+    float ks[NG][32];            // K scales by group and token
+    float lv[32], rv[32];        // log2 and reciprocal of the V scales
   };
-  float m[NW][16], l[NW][16];
-  float red[NW * 64 * 4];
-  int last;
+  struct {
+    float f[16][kJoin];          // by row and chunk
+    float inv[16];               // a row's reciprocal sum
+  };
 };
 
-template <int NG, int R, int NW>
-__global__ __launch_bounds__(NW * 64) void kv_attention_kernel(KvAttnArgs a) {
+// W floats (2, or a multiple of 4) to a partial row at float offset `at`.
+template <int W>
+__device__ __forceinline__ void store_run(__amdgpu_buffer_rsrc_t rs, int64_t at, const float* v) {
+  if constexpr (W == 2) {
+    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, (f32x2){v[0], v[1]}), rs, (int)(at * 4), 0, kCachePolicySc1);
+  } else {
+#pragma unroll
+    for (int e = 0; e < W; e += 4) store_partial(rs, (at + e) / 4, (f32x4){v[e], v[e + 1], v[e + 2], v[e + 3]});
+  }
+}
+
+// W values (even) times f to bf16 at p.
+template <int W>
+__device__ __forceinline__ void store_out(uint16_t* p, const float* v, float f) {
+  uint32_t d[W / 2];
+#pragma unroll
+  for (int e = 0; e < W; e += 2) d[e / 2] = pack_bf16x2(v[e] * f, v[e + 1] * f);
+  if constexpr (W == 2) {
+    *reinterpret_cast<uint32_t*>(p) = d[0];
+  } else if constexpr (W == 4) {
+    *reinterpret_cast<u32x2*>(p) = (u32x2){d[0], d[1]};
+  } else {
+#pragma unroll
+    for (int e = 0; e < W / 2; e += 4) st16(p + 2 * e, (u32x4){d[e], d[e + 1], d[e + 2], d[e + 3]});
+  }
+}
+
+#ifndef QTGT
+#define QTGT 256
+#endif
+#ifndef QMINT
+#define QMINT 1
+#endif
+template <int NG, int R>
+__global__ __launch_bounds__(kWaves * 64) void kv_attention_kernel(KvAttnArgs a) {
   constexpr int D = 32 * NG, TR = 16 * R;
-  typedef Smem<NG, NW> S;
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  S& sm = *reinterpret_cast<S*>(smem_raw);
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int c16 = lane & 15, g4 = lane >> 4;
-  // The heads of one item sit on one XCD (workgroup b goes to XCD b % 8): a token's scales of
-  // all heads share cache lines.
-  const int x = blockIdx.x & 7, li = blockIdx.x >> 3;
-  const int item = (li / a.Hk) * 8 + x, h = li % a.Hk;
-  const Item it = find_item<TR>(a, __builtin_amdgcn_readfirstlane(item), lane);
-  if (!it.found) return;                                     // uniform for the workgroup
+  // Codes are read once per 16 R rows: streamed past the caches where a head's row fills whole
+  // cache lines (128 bytes); shorter ones share lines between waves.
+  constexpr bool NT = R == 1 && NG % 4 == 0;
+  __shared__ __align__(16) WaveLds<NG> lds[kWaves];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  WaveLds<NG>& mine = lds[wave];
+  // HW neighbouring KV heads per workgroup, one per wave (a token's entries of all heads lie
+  // side by side, and reading them together is what HBM rewards), and kWaves / HW waves on a
+  // head's line.  The head groups of one part sit on one XCD (workgroup b goes to XCD b % 8),
+  // whose L2 they share for the scales.
+  const int HW = 1 << a.hw_shift, HG = a.Hk >> a.hw_shift, TS = kWaves >> a.hw_shift;
+  int part = blockIdx.x / HG, hg = blockIdx.x % HG;
+  if (a.parts % 8 == 0) {
+    const int li = blockIdx.x >> 3;
+    part = (li / HG) * 8 + (blockIdx.x & 7);
+    hg = li % HG;
+  }
+  const int h = hg * HW + (wave & (HW - 1)), me = part * TS + (wave >> a.hw_shift);   // head, place on its line
+  const Extent mine_e = lane < a.B ? extent_of(a, lane) : Extent{};
+  const Line line = line_of<TR>(a, mine_e, lane);
+  // An equal share of the units, but while there are few, shares that keep the longest tile in
+  // kJoin chunks (one joining instead of two) as long as a wave then has QMINT units at most.
+  const int P = a.parts * TS;
+  const int U = max(max(1, (line.total + P - 1) / P), min((line.longest + kJoin - 1) / kJoin, QMINT));
+  const int u_end = min(line.total, (me + 1) * U);
+  for (int u = me * U; u < u_end;) {
+  const Tile it = tile_of<TR>(a, mine_e, u, lane);
+  const int u_next = min(u_end, it.begin + it.units);
+  // This tile's chunks: one per wave that its units reach
+  const int wf = it.begin / U, nch = (it.begin + it.units - 1) / U - wf + 1, ch = me - wf;
   const int nq = it.e.nq, L = it.e.L, r0 = it.qt * TR, rows = nq * a.G;
   const int i0 = r0 / a.G, i1 = min(nq - 1, (r0 + TR - 1) / a.G);
   const int p0 = L - nq;                                     // position of query 0
   const int tend = min(max(a.causal ? p0 + i1 + 1 : L, 0), L);
-  const int tbeg = a.window > 0 ? min(max(0, p0 + i0 - a.window + 1), tend) : 0;
-  const int per = ((tend - tbeg + it.nch - 1) / it.nch + 31) & ~31;
-  const int c0 = min(tbeg + it.ch * per, tend), c1 = min(c0 + per, tend);
+  const int tbeg = a.window > 0 ? min(max(0, p0 + i0 - a.window + 1), tend) & ~31 : 0;
+  const int c0 = max(tbeg, it.e.begin + 32 * (u - it.begin));              // a multiple of 32
+  const int c1 = min(tend, it.e.begin + 32 * (u_next - it.begin));
+  u = u_next;
 
-  // q: per query row a power of two into [-1, 1), fp16.
-  f16x8 qf[R][NG];
-  float cs[R];
+  int c16 = lane & 15, g4 = lane >> 4;
+  asm volatile("" : "+v"(c16), "+v"(g4));                    // (nothing computed from them outlives a tile)
+  // Channels of a group that lane group g4 holds of K and q: 8 g4 on, or (two groups loaded at
+  // once, 16 bytes per lane, and their halves swapped between the wave's halves) kq on.
+  const int kq = ((g4 & 1) << 4) | ((g4 >> 1) << 3);
+
+  // q's rows (packed: query token, then head of the group); their first use is further down.
+  u32x4 qraw[R][NG];
   int qpos[R];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int row = r0 + 16 * r + c16;
     const bool live = row < rows;
-    const int i = live ? row / a.G : 0, g = live ? row % a.G : 0;
+    const int i = live ? row / a.G : i0, g = live ? row - i * a.G : 0;
     qpos[r] = live ? p0 + i : -1;
-    const uint16_t* qp = a.q + (int64_t)(it.e.qs + i) * a.q_stride + (int64_t)(h * a.G + g) * D + 8 * g4;
-    float f[NG][8], am = 0.0f;
+    const uint16_t* qp = a.q + (int64_t)(it.e.qs + i) * a.q_stride + (int64_t)(h * a.G + g) * D + (NG % 2 == 0 ? kq : 8 * g4);
 #pragma unroll
-    for (int n = 0; n < NG; ++n) {
-      const u32x4 v = live ? ld16(qp + 32 * n) : (u32x4){0u, 0u, 0u, 0u};
-      const uint32_t d[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        f[n][2 * e] = bf16_bits_to_f32(d[e] & 0xFFFF);
-        f[n][2 * e + 1] = bf16_bits_to_f32(d[e] >> 16);
-        am = fmaxf(am, fmaxf(fabsf(f[n][2 * e]), fabsf(f[n][2 * e + 1])));
-      }
-    }
-    am = fmaxf(am, __shfl_xor(am, 16, 64));
-    am = fmaxf(am, __shfl_xor(am, 32, 64));
-    const int ex = am > 0.0f ? __builtin_amdgcn_frexp_expf(am) : 0;   // am < 2^ex
-#pragma unroll
-    for (int n = 0; n < NG; ++n)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) qf[r][n][e] = (_Float16)__builtin_ldexpf(f[n][e], -ex);
-    cs[r] = __builtin_ldexpf(a.scale * kLog2e, ex);
+    for (int n = 0; n < NG; ++n) qraw[r][n] = ld16(qp + 32 * n);
   }
 
   f32x4 o[2 * NG][R];
@@ -323,112 +425,169 @@ __global__ __launch_bounds__(NW * 64) void kv_attention_kernel(KvAttnArgs a) {
 #pragma unroll
   for (int r = 0; r < R; ++r) m[r] = kNegInf, l[r] = 0.0f;
 
-  const int32_t* table = a.block_table + (int64_t)it.b * a.max_pages;
-  const int page_mask = (1 << a.page_shift) - 1;
-  const int hk = a.Hk;
+  const int hk = a.Hk, page_mask = (1 << a.page_shift) - 1;
   typedef Pieces<NG> P1;
   typedef Pieces<(P1::Rest > 0 ? P1::Rest : 1)> P2;          // NG <= 8, no 7: at most two pieces
   constexpr int RB1 = 2 * P1::P, RB2 = 2 * P2::P;
   constexpr bool kTwo = P1::Rest > 0;
   static_assert(!kTwo || P2::Rest == 0, "two pieces at most");
 
-  auto slot_of = [&](int base) {                             // lanes 0..31 (repeated above): token base + lane
-    const int t = base + (lane & 31);
-    int s = -1;
-    if (t < c1) {
-      const int page = table[t >> a.page_shift];
-      if (page >= 0 && page < a.pages) s = (page << a.page_shift) | (t & page_mask);
-    }
-    return s;
+  // Tiles start at multiples of 32 tokens and pages hold 16 or more, so each half of a tile lies
+  // in one page: its first entry is uniform, and all addresses are a uniform base plus an offset
+  // that a lane keeps.  -1: the page is outside the pool (its tokens are left out).
+  const ConstInt* table = (const ConstInt*)(uintptr_t)(a.block_table + (int64_t)it.b * a.max_pages);
+  auto page_of = [&](int t) { return table[min(t, a.max_tokens - 1) >> a.page_shift]; };
+  auto entry_of = [&](int page, int t) {
+    return page >= 0 && page < a.pages ? (page << a.page_shift) + (t & page_mask) : -1;
   };
+  const uint32_t row_bytes = (uint32_t)hk * D;               // from one token to the next
+  const uint32_t koff = c16 * row_bytes + (NG % 2 == 0 ? 16 : 8) * g4;
+  const uint32_t voff1 = 4 * g4 * row_bytes + RB1 * c16, voff2 = 4 * g4 * row_bytes + 32 * P1::P + RB2 * c16;
 
-  int next_slot = slot_of(c0 + 32 * wave);
-  int buf = 0;
-  for (int base = c0 + 32 * wave; base < c1; base += 32 * NW) {
-    const int my = next_slot;
-    const bool all_valid = __ballot(my < 0) == 0;
-    if (lane < 32) sm.slot[wave][buf][lane] = my;
+  // Pipeline: while a tile is computed, the next one's K, scales and V are in flight (K and the
+  // scales from the moment the scores are done, V from the moment the values are), and the pages
+  // of the one after that.  Loads come back in the order of their issue, so what is wanted first
+  // is asked for first, and none of them is behind a branch (past the last tile they read the
+  // pool's first entries).
+  constexpr int KI = NG % 2 == 0 ? NG / 2 : NG;
+  typedef typename std::conditional<NG % 2 == 0, u32x4, u32x2>::type KRaw;
+  KRaw kr[2][KI];
+  KScales<NG> ksr;
+  uint32_t vsr = 0;
+  Raw<RB1, NT> v1[8];
+  Raw<RB2, NT> v2[8];
+  auto load_k = [&](int e0, int e1) {                        // and the scales: one token per lane
+    const int64_t at = ((int64_t)(max(lane & 16 ? e1 : e0, 0) + c16)) * hk + h;
+    ksr.load(a.k_scales + at * NG);
+    vsr = a.v_scales[at];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint8_t* p = a.k_codes + ((int64_t)max(u ? e1 : e0, 0) * hk + h) * D;
+#pragma unroll
+      for (int n = 0; n < KI; ++n) {
+        if constexpr (NG % 2 == 0) kr[u][n] = ld<NT>(reinterpret_cast<const u32x4*>(p + 64 * n + koff));
+        else kr[u][n] = *reinterpret_cast<const u32x2*>(p + 32 * n + koff);
+      }
+    }
+  };
+  auto load_v = [&](int e0, int e1) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint8_t* p = a.v_codes + ((int64_t)max(u ? e1 : e0, 0) * hk + h) * D;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v1[4 * u + j].load(p + (size_t)j * row_bytes + voff1);
+        if constexpr (kTwo) v2[4 * u + j].load(p + (size_t)j * row_bytes + voff2);
+      }
+    }
+  };
+  auto wave_sync = [] {                                      // this wave's LDS writes before its reads
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    int kslot[2];
-    int vslot[2][4];
+  };
+
+  constexpr int STEP = 32;
+  const int first = c0;
+  int e0 = entry_of(page_of(first), first), e1 = entry_of(page_of(first + 16), first + 16);
+  int g0 = page_of(first + STEP), g1 = page_of(first + STEP + 16);       // the next tile's pages
+  load_k(e0, e1);
+  __builtin_amdgcn_sched_barrier(0);
+  load_v(e0, e1);
+  __builtin_amdgcn_sched_barrier(0);
+
+  // q: per query row a power of two into [-1, 1), fp16; rows past the last are zero.
+  f16x8 qf[R][NG];
+  float cs[R];
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      kslot[u] = max(sm.slot[wave][buf][16 * u + c16], 0);
-      const i32x4 v = *reinterpret_cast<const i32x4*>(&sm.slot[wave][buf][16 * u + 4 * g4]);
+  for (int r = 0; r < R; ++r) {
+    const bool live = r0 + 16 * r + c16 < rows;
+    float f[NG][8], am = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) vslot[u][j] = v[j];
-    }
-    buf ^= 1;
-    // loads of the tile
-    u32x2 kr[2][NG];
+    for (int n = 0; n < NG; ++n) {
+      const uint32_t d[4] = {qraw[r][n].x, qraw[r][n].y, qraw[r][n].z, qraw[r][n].w};
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const uint8_t* p = a.k_codes + ((int64_t)kslot[u] * hk + h) * D + 8 * g4;
-#pragma unroll
-      for (int n = 0; n < NG; ++n) kr[u][n] = *reinterpret_cast<const u32x2*>(p + 32 * n);
-    }
-    KScales<NG> ks[2][4];
-    uint32_t vsb[2][4];
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int64_t at = (int64_t)max(vslot[u][j], 0) * hk + h;
-        ks[u][j].load(a.k_scales + at * NG);
-        vsb[u][j] = a.v_scales[at];
+      for (int e = 0; e < 4; ++e) {
+        f[n][2 * e] = live ? bf16_bits_to_f32(d[e] & 0xFFFF) : 0.0f;
+        f[n][2 * e + 1] = live ? bf16_bits_to_f32(d[e] >> 16) : 0.0f;
+        am = fmaxf(am, fmaxf(fabsf(f[n][2 * e]), fabsf(f[n][2 * e + 1])));
       }
-    Raw<RB1> v1[8];
-    Raw<RB2> v2[8];
+    }
+    am = max_across16(am);
+    const int ex = am > 0.0f ? __builtin_amdgcn_frexp_expf(am) : 0;   // am < 2^ex
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int n = 0; n < NG; ++n)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint8_t* p = a.v_codes + ((int64_t)max(vslot[u][j], 0) * hk + h) * D;
-        v1[4 * u + j].load(p + RB1 * c16);
-        if constexpr (kTwo) v2[4 * u + j].load(p + 32 * P1::P + RB2 * c16);
-      }
-    next_slot = slot_of(base + 32 * NW);
+      for (int e = 0; e < 8; ++e) qf[r][n][e] = (_Float16)__builtin_ldexpf(f[n][e], -ex);
+    cs[r] = __builtin_ldexpf(a.scale * kLog2e, ex);
+  }
+
+  for (int base = first; base < c1; base += STEP) {
+    const bool all_valid = e0 >= 0 && e1 >= 0 && base + 32 <= c1;
+    const int n0 = entry_of(g0, base + STEP), n1 = entry_of(g1, base + STEP + 16);
+    const int t0 = base + 4 * g4;                            // this lane's first token (u = j = 0)
+    auto there = [&](int u, int j) { return (u ? e1 : e0) >= 0 && t0 + 16 * u + j < c1; };
+    // V scales into the exponent.  A scale of zero (an entry never written) counts as the
+    // smallest one: its codes are zero too.  Tokens that are not there count as scale 1.
+    if (lane < 32) {
+      const bool in = all_valid || ((lane & 16 ? e1 : e0) >= 0 && base + lane < c1);
+      const float sv = in ? fmaxf(f16_lo(vsr), 0x1p-24f) : 1.0f;
+      mine.lv[lane] = __builtin_amdgcn_logf(sv);
+      mine.rv[lane] = __builtin_amdgcn_rcpf(sv);
+#pragma unroll
+      for (int n = 0; n < NG; ++n) mine.ks[n][lane] = ksr.get(n);
+    }
+    wave_sync();
 
     // S^T: tokens 16 u + 4 g4 + j, query c16
     float s[R][2][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[r][u][j] = 0.0f;
-#pragma unroll
       for (int n = 0; n < NG; ++n) {
-        const f16x8 kf = i8x8_to_f16(kr[u][n]);
+        u32x2 kw;
+        if constexpr (NG % 2 == 0) {
+          if (n % 2 == 0) {
+            const auto lo = __builtin_amdgcn_permlane32_swap(kr[u][n / 2].x, kr[u][n / 2].z, false, false);
+            const auto hi = __builtin_amdgcn_permlane32_swap(kr[u][n / 2].y, kr[u][n / 2].w, false, false);
+            kr[u][n / 2] = (u32x4){lo[0], hi[0], lo[1], hi[1]};
+            kw = (u32x2){lo[0], hi[0]};
+          } else {
+            kw = (u32x2){kr[u][n / 2].z, kr[u][n / 2].w};
+          }
+        } else {
+          kw = (u32x2){kr[u][n].x, kr[u][n].y};
+        }
+        const f16x8 kf = i8x8_to_f16(kw);
+        const f32x4 ks = *reinterpret_cast<const f32x4*>(&mine.ks[n][16 * u + 4 * g4]);
 #pragma unroll
         for (int r = 0; r < R; ++r) {
           const f32x4 d = mfma_f16_k32(kf, qf[r][n], (f32x4){0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-          for (int j = 0; j < 4; ++j) s[r][u][j] = __builtin_fmaf(ks[u][j].s[n], d[j], s[r][u][j]);
+          for (int j = 0; j < 4; ++j) s[r][u][j] = n == 0 ? ks[j] * d[j] : __builtin_fmaf(ks[j], d[j], s[r][u][j]);
         }
+        if constexpr (NG > 4 || R > 1) __builtin_amdgcn_sched_barrier(0);
       }
+      __builtin_amdgcn_sched_barrier(0);                     // (fewer registers at once)
     }
-    // V scales into the exponent.  A scale of zero (an entry never written) counts as the
-    // smallest one: its codes are zero too.
     float lv[2][4], rv[2][4];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float sv = fmaxf(f16_lo(vsb[u][j]), 0x1p-24f);
-        if (!all_valid && vslot[u][j] < 0) sv = 1.0f;
-        lv[u][j] = __builtin_amdgcn_logf(sv);
-        rv[u][j] = __builtin_amdgcn_rcpf(sv);
-      }
+    for (int u = 0; u < 2; ++u) {
+      *reinterpret_cast<f32x4*>(lv[u]) = *reinterpret_cast<const f32x4*>(&mine.lv[16 * u + 4 * g4]);
+      *reinterpret_cast<f32x4*>(rv[u]) = *reinterpret_cast<const f32x4*>(&mine.rv[16 * u + 4 * g4]);
+    }
+    load_k(n0, n1);
+    __builtin_amdgcn_sched_barrier(0);
+    g0 = page_of(base + 2 * STEP);
+    g1 = page_of(base + 2 * STEP + 16);
+
     // whole tile visible to every row of this workgroup?
     const int tmin_p = p0 + i0, tmax_p = p0 + i1;
     const bool open = all_valid && (!a.causal || base + 31 <= tmin_p) && (a.window <= 0 || base > tmax_p - a.window);
     if (!all_valid) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (vslot[i >> 2][i & 3] < 0) {
+        if (!there(i >> 2, i & 3)) {
           v1[i].clear();
           if constexpr (kTwo) v2[i].clear();
         }
@@ -443,15 +602,14 @@ __global__ __launch_bounds__(NW * 64) void kv_attention_kernel(KvAttnArgs a) {
         for (int j = 0; j < 4; ++j) {
           float v = __builtin_fmaf(s[r][u][j], cs[r], lv[u][j]);
           if (!open) {
-            const int t = base + 16 * u + 4 * g4 + j;
-            const bool see = vslot[u][j] >= 0 && (!a.causal || t <= qpos[r]) && (a.window <= 0 || t > qpos[r] - a.window);
+            const int t = t0 + 16 * u + j;
+            const bool see = there(u, j) && (!a.causal || t <= qpos[r]) && (a.window <= 0 || t > qpos[r] - a.window);
             v = see ? v : kNegInf;
           }
           s[r][u][j] = v;
           mx = fmaxf(mx, v);
         }
-      mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-      mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+      mx = max_across16(mx);
       const float mn = fmaxf(m[r], mx);
       const float ref = mn == kNegInf ? 0.0f : mn;
       if (__ballot(mn > m[r])) {
@@ -472,180 +630,141 @@ __global__ __launch_bounds__(NW * 64) void kv_attention_kernel(KvAttnArgs a) {
           w[r][4 * u + j] = (_Float16)e;
         }
     }
-    pv_piece<P1::P, R>(v1, w, o);
-    if constexpr (kTwo) pv_piece<P2::P, R>(v2, w, o + 2 * P1::P);
+    pv_piece<P1::P, R, NT>(v1, w, o);
+    if constexpr (kTwo) pv_piece<P2::P, R, NT>(v2, w, o + 2 * P1::P);
+    load_v(n0, n1);
+    e0 = n0;
+    e1 = n1;
   }
-#pragma unroll
-  for (int r = 0; r < R; ++r) {                              // l over the lane groups of a query
-    l[r] += __shfl_xor(l[r], 16, 64);
-    l[r] += __shfl_xor(l[r], 32, 64);
-  }
-
-  // Sum over the waves, 16 rows at a time; thread (row, part) holds 2 NG channels of a row.
-  constexpr int SEG = 16, CH = 2 * NG;
-  const bool split = it.nch > 1;
-  const int64_t tile_base = ((int64_t)item * hk + h) * a.tile_rows;       // this chunk's partial rows
+  // A lane has, per 16-row subtile, channels 2 P (4 g4 + j) .. + 2 P - 1 of each piece of its row.
+  // (The copies keep the compiler from computing addresses ahead of the tile loop.)
+  constexpr int W1 = 2 * P1::P, W2 = 2 * P2::P;
+  asm volatile("" : "+v"(c16), "+v"(g4));
+  const bool split = nch > 1;
   const __amdgpu_buffer_rsrc_t rs = partial_rsrc(a.partials, a.partials_bytes);
+  // A wave has at most two chunks of tiles that it shares: the tile that began before it (slot
+  // 2 w) and the one that goes on after it (2 w + 1).  Partial row: [D sums][M, L, -, -].
+  auto slot_of = [&](int c) { return 2 * (wf + c) + (c == 0 ? 1 : 0); };
+  auto part_row = [&](int c, int row) { return (int64_t)((slot_of(c) * hk + h) * a.tile_rows + row) * (D + 4); };
+  auto out_row = [&](int grow) {                             // index of [token][query head]
+    const int i = grow / a.G;
+    return (int64_t)(it.e.qs + i) * a.Hq + h * a.G + (grow - i * a.G);
+  };
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    __syncthreads();
-    if (g4 == 0) {
-      sm.m[wave][c16] = m[r];
-      sm.l[wave][c16] = l[r];
-    }
-    __syncthreads();
-    float M = kNegInf;
-    for (int w2 = 0; w2 < NW; ++w2) M = fmaxf(M, sm.m[w2][c16]);
-    const float f = M == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m[r] - M);
-#pragma unroll
-    for (int n = 0; n < 2 * NG; ++n) {
-      // tile n, element j: channel of column c = 4 g4 + j
-      constexpr int W1 = 2 * P1::P;
+    const float L = sum_across16(l[r]);                      // over the lane groups of a query
+    const int row = 16 * r + c16;
+    if (r0 + row < rows) {
+      float v1r[4][W1], v2r[4][W2];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int ch = n < W1 ? (4 * g4 + j) * W1 + n : 32 * P1::P + (4 * g4 + j) * RB2 + (n - W1);
-        sm.acc[wave][c16][ch] = o[n][r][j] * f;
+#pragma unroll
+        for (int n = 0; n < W1; ++n) v1r[j][n] = o[n][r][j];
+        if constexpr (kTwo)
+#pragma unroll
+          for (int n = 0; n < W2; ++n) v2r[j][n] = o[W1 + n][r][j];
       }
-    }
-    __syncthreads();
-    for (int idx = tid; idx < 16 * SEG; idx += NW * 64) {
-      const int row = idx / SEG, part = idx % SEG;
-      const int grow = r0 + 16 * r + row;
-      if (grow >= rows) continue;
-      float Mr = kNegInf, Lr = 0.0f;
-      for (int w2 = 0; w2 < NW; ++w2) Mr = fmaxf(Mr, sm.m[w2][row]);
-      if (Mr != kNegInf)
-        for (int w2 = 0; w2 < NW; ++w2) Lr += sm.l[w2][row] * __builtin_amdgcn_exp2f(sm.m[w2][row] - Mr);
-      float v[CH];
-#pragma unroll
-      for (int e = 0; e < CH; ++e) v[e] = 0.0f;
-      for (int w2 = 0; w2 < NW; ++w2)
-#pragma unroll
-        for (int e = 0; e < CH; ++e) v[e] += sm.acc[w2][row][part * CH + e];
       if (!split) {
-        const float inv = Lr > 0.0f ? 1.0f / Lr : 0.0f;
-        const int i = grow / a.G, g = grow % a.G;
-        uint32_t* out = reinterpret_cast<uint32_t*>(a.out + ((int64_t)(it.e.qs + i) * a.Hq + h * a.G + g) * D + part * CH);
+        const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+        const int64_t at = out_row(r0 + row);
+        uint16_t* out = a.out + at * D;
 #pragma unroll
-        for (int e = 0; e < CH; e += 2) out[e / 2] = pack_bf16x2(v[e] * inv, v[e + 1] * inv);
-        if (a.lse && part == 0)
-          a.lse[(int64_t)(it.e.qs + i) * a.Hq + h * a.G + g] = Lr > 0.0f ? (Mr + __builtin_amdgcn_logf(Lr)) * kLn2 : kNegInf;
+        for (int j = 0; j < 4; ++j) {
+          store_out<W1>(out + (4 * g4 + j) * W1, v1r[j], inv);
+          if constexpr (kTwo) store_out<W2>(out + 32 * P1::P + (4 * g4 + j) * W2, v2r[j], inv);
+        }
+        if (a.lse && g4 == 0) a.lse[at] = L > 0.0f ? (m[r] + __builtin_amdgcn_logf(L)) * kLn2 : kNegInf;
       } else {
-        const int64_t p = (tile_base + 16 * r + row) * (D + 4);          // [D sums][M, L, -, -]
+        const int64_t p = part_row(ch, row);
 #pragma unroll
-        for (int e = 0; e < CH; e += 2)
-          __builtin_amdgcn_raw_buffer_store_b64(
-              (u32x2){__builtin_bit_cast(uint32_t, v[e]), __builtin_bit_cast(uint32_t, v[e + 1])}, rs,
-              (int)((p + part * CH + e) * 4), 0, kCachePolicySc1);
-        if (part == 0)
-          __builtin_amdgcn_raw_buffer_store_b64(
-              (u32x2){__builtin_bit_cast(uint32_t, Mr), __builtin_bit_cast(uint32_t, Lr)}, rs, (int)((p + D) * 4), 0,
-              kCachePolicySc1);
+        for (int j = 0; j < 4; ++j) {
+          store_run<W1>(rs, p + (4 * g4 + j) * W1, v1r[j]);
+          if constexpr (kTwo) store_run<W2>(rs, p + 32 * P1::P + (4 * g4 + j) * W2, v2r[j]);
+        }
+        if (g4 == 0) {
+          const float ml[2] = {m[r], L};
+          store_run<2>(rs, p + D, ml);
+        }
       }
     }
   }
-  if (!split) return;
+  if (!split) continue;
 
-  // Join the chunks: the last workgroup of this (tile, head) to arrive, in chunk order.
-  wait_stores_performed();
-  __syncthreads();
-  uint32_t* counter = a.counters + (int64_t)it.first * hk + h;
-  if (tid == 0) sm.last = arrive(counter) + 1u == (uint32_t)it.nch;
-  __syncthreads();
-  if (!sm.last) return;
-  if (tid == 0) reset_counter(counter);
-  constexpr int DP = D / 4;                                  // 16-byte parts of a row
-  // One chunk's (M, L) of a row, and 16 bytes of its sums.
-  auto load_ml = [&](int64_t row) {
-    return __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, (int)((row + D) * 4), 0, kCachePolicySc1));
-  };
-  auto part_row = [&](int ch, int row) { return (((int64_t)(it.first + ch) * hk + h) * a.tile_rows + row) * (D + 4); };
-  for (int r = 0; r < R; ++r) {
-    const int live = min(16, rows - r0 - 16 * r);
-    if (live <= 0) break;
-    __syncthreads();
-    // factors 2^(M_c - M) / L of every chunk, 16 threads per row
-    const int frow = tid >> 4, fl = tid & 15;
-    if (frow < 16) {
-      float M = kNegInf;
-      const bool on = frow < live;
-      for (int c = fl; on && c < it.nch; c += 16) {
-        const f32x2 ml = load_ml(part_row(c, 16 * r + frow));
-        M = fmaxf(M, ml.x);
-      }
-      for (int off = 1; off < 16; off <<= 1) M = fmaxf(M, __shfl_xor(M, off, 64));
-      float Ls = 0.0f;
-      for (int c = fl; on && c < it.nch; c += 16) {
-        const f32x2 ml = load_ml(part_row(c, 16 * r + frow));
+  // Join the chunks, kJoin at a time, then those groups, and so on: the last wave of a group to
+  // finish joins it (always in chunk order) into the group's first partial rows, the last group
+  // of all into the output.
+  for (int level = 0, stride = 1;; ++level, stride *= kJoin) {
+    const int ch0 = ch - ch % (stride * kJoin);
+    const int n = min(kJoin, (nch - ch0 + stride - 1) / stride);
+    const bool done = stride * kJoin >= nch;                 // one group: joins into the output
+    wait_stores_performed();
+    uint32_t* counter = a.counters + level * a.level_counters + slot_of(ch0) * hk + h;
+    int last = 0;
+    if (lane == 0) {
+      last = arrive(counter) + 1u == (uint32_t)n;
+      if (last) reset_counter(counter);
+    }
+    if (!__builtin_amdgcn_readfirstlane(last)) break;
+    constexpr int DP = D / 4, RP = DP <= 64 ? 64 / DP : 1;   // 16-byte parts of a row, rows at a time
+    for (int r = 0; r < R; ++r) {
+      const int live = min(16, rows - r0 - 16 * r);
+      if (live <= 0) break;
+      wave_sync();
+      // factors 2^(M_c - M) of the chunks: four rows at a time, 16 lanes (chunks) per row
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int row = 4 * q + g4, c = c16;
+        if (4 * q >= live) break;                            // uniform
+        const int64_t p = part_row(ch0 + min(c, n - 1) * stride, 16 * r + min(row, live - 1));
+        f32x2 ml = __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, (int)((p + D) * 4), 0, kCachePolicySc1));
+        if (c >= n) ml = (f32x2){kNegInf, 0.0f};
+        const float M = max_row16(ml.x);
         const float f = M == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ml.x - M);
-        sm.f[frow][c] = f;
-        Ls = __builtin_fmaf(ml.y, f, Ls);
+        const float L = sum_row16(ml.y * f);
+        mine.f[row][c] = f;
+        if (c == 0 && row < live) {
+          if (!done) {
+            const float out[2] = {M, L};
+            store_run<2>(rs, p + D, out);
+          } else if (a.lse) {
+            a.lse[out_row(r0 + 16 * r + row)] = L > 0.0f ? (M + __builtin_amdgcn_logf(L)) * kLn2 : kNegInf;
+          }
+        }
+        if (c == 0) mine.inv[row] = L > 0.0f ? 1.0f / L : 0.0f;
       }
-      for (int off = 1; off < 16; off <<= 1) Ls += __shfl_xor(Ls, off, 64);
-      if (on && fl == 0) {
-        sm.l[0][frow] = Ls > 0.0f ? 1.0f / Ls : 0.0f;
-        if (a.lse) {
-          const int grow = r0 + 16 * r + frow;
-          a.lse[(int64_t)(it.e.qs + grow / a.G) * a.Hq + h * a.G + grow % a.G] =
-              Ls > 0.0f ? (M + __builtin_amdgcn_logf(Ls)) * kLn2 : kNegInf;
+      wave_sync();
+      // sums: 64 lanes over (row, part)
+      for (int b = 0; b < live * DP; b += 64) {
+        const int id = min(b + lane, live * DP - 1), row = id / DP, dp = id % DP;
+        f32x4 v[kJoin];
+#pragma unroll
+        for (int c = 0; c < kJoin; ++c)
+          v[c] = load_partial(rs, part_row(ch0 + min(c, n - 1) * stride, 16 * r + row) / 4 + dp);
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kJoin; ++c) sum += v[c] * mine.f[row][c];   // f is 0 past the last
+        const float inv = mine.inv[row];
+        if (b + lane < live * DP) {
+          if (done) {
+            uint32_t* out = reinterpret_cast<uint32_t*>(a.out + out_row(r0 + 16 * r + row) * D + dp * 4);
+            out[0] = pack_bf16x2(sum.x * inv, sum.y * inv);
+            out[1] = pack_bf16x2(sum.z * inv, sum.w * inv);
+          } else {
+            store_partial(rs, part_row(ch0, 16 * r + row) / 4 + dp, sum);
+          }
         }
       }
     }
-    __syncthreads();
-    // `groups` threads share one 16-byte part of a row, each a share of the chunks
-    const int parts = live * DP;
-    const int groups = max(1, NW * 64 / parts);
-    f32x4* red = reinterpret_cast<f32x4*>(sm.red);
-    for (int p0i = 0; p0i < parts; p0i += NW * 64) {         // one pass unless parts > threads
-      const int id = p0i + (groups > 1 ? tid % parts : tid);
-      const int grp = groups > 1 ? tid / parts : 0;
-      const bool on = id < parts && grp < groups;
-      const int row = on ? id / DP : 0, dp = on ? id % DP : 0;
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-      if (on) {
-        const int lo = it.nch * grp / groups, hi = it.nch * (grp + 1) / groups;
-#pragma unroll 4
-        for (int c = lo; c < hi; ++c) {
-          const f32x4 v = load_partial(rs, part_row(c, 16 * r + row) / 4 + dp);
-          acc += v * sm.f[row][c];
-        }
-      }
-      if (groups > 1) {
-        __syncthreads();
-        red[tid] = acc;
-        __syncthreads();
-        if (on && grp == 0)
-          for (int k = 1; k < groups; ++k) acc += red[k * parts + id];
-      }
-      if (on && grp == 0) {
-        const float inv = sm.l[0][row];
-        const int grow = r0 + 16 * r + row;
-        uint32_t* out = reinterpret_cast<uint32_t*>(
-            a.out + ((int64_t)(it.e.qs + grow / a.G) * a.Hq + h * a.G + grow % a.G) * D + dp * 4);
-        out[0] = pack_bf16x2(acc.x * inv, acc.y * inv);
-        out[1] = pack_bf16x2(acc.z * inv, acc.w * inv);
-      }
-    }
+    if (done) break;
   }
-}
-
-template <int NG, int R, int NW>
-hipError_t launch_one(const KvAttnArgs& a, int grid, hipStream_t st) {
-  static std::atomic<uint64_t> done{0};
-  constexpr int bytes = (int)sizeof(Smem<NG, NW>);
-  static_assert(bytes <= 160 * 1024, "LDS");
-  const void* k = reinterpret_cast<const void*>(kv_attention_kernel<NG, R, NW>);
-  if (hipError_t e = set_lds_limit(k, bytes, done); e != hipSuccess) return e;
-  kv_attention_kernel<NG, R, NW><<<grid, NW * 64, bytes, st>>>(a);
-  return hipGetLastError();
+  }
 }
 
 template <int NG>
 hipError_t launch_ng(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t st) {
-  switch (p.R) {
-    case 1: return launch_one<NG, 1, 8>(a, p.grid, st);
-    default: return launch_one<NG, 2, 4>(a, p.grid, st);
-  }
+  if (p.R == 1) kv_attention_kernel<NG, 1><<<(int)p.grid, kWaves * 64, 0, st>>>(a);
+  else kv_attention_kernel<NG, 2><<<(int)p.grid, kWaves * 64, 0, st>>>(a);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -655,19 +774,16 @@ KvAttnPlan plan_kv_attention(int64_t T, int64_t B, int64_t Hk, int64_t G, bool o
   const int64_t rows = one_each ? G : (T + B - 1) / B * G;   // query rows of an average sequence
   p.R = rows <= 16 ? 1 : 2;
   const int64_t TR = 16 * p.R;
-  p.waves = p.R == 1 ? 8 : 4;
-  // Query tiles: of every sequence together, at most
-  const int64_t tiles = one_each ? B * ((G + TR - 1) / TR) : T * G / TR + B;
-  // About two workgroups of eight waves per CU; at most 256 chunks of a tile are joined.
-  int64_t target = (p.R == 1 ? 512 : 1024) / Hk;
-  target = target < 1 ? 1 : target > 256 ? 256 : target;
-  p.split = tiles < 4 * target;
-  p.target = (int)target;
-  p.chunk_step = 32 * p.waves;
-  const int64_t items = tiles + (p.split ? target : 0);
-  p.grid = (int64_t)((items + 7) / 8 * 8) * Hk;
+  // Neighbouring KV heads per workgroup: a power of two that divides Hk, at most the waves.
+  while ((2 << p.hw_shift) <= kWaves && Hk % (2 << p.hw_shift) == 0) ++p.hw_shift;
+  // One workgroup of four waves per CU (two measured slower, see above).
+  const int64_t HG = Hk >> p.hw_shift;
+  const int64_t parts = QTGT / HG;
+  p.parts = (int)(parts >= 8 ? parts / 8 * 8 : parts < 1 ? 1 : parts);
+  p.grid = p.parts * HG;
+  p.waves = p.parts * (kWaves >> p.hw_shift);
   p.tile_rows = (int)(one_each && G < TR ? G : TR);
-  p.items = items;
+  p.tiles = one_each ? B * ((G + TR - 1) / TR) : T * G / TR + B;
   return p;
 }
 

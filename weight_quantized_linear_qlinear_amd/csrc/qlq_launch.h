@@ -125,17 +125,18 @@ struct KvAttnArgs {
   int page_shift, pages, max_pages, max_tokens;
   float scale;
   int causal, window;
-  int split, target, chunk_step, tile_rows;
+  int parts, tile_rows, hw_shift, level_counters;
   uint32_t* counters;
   float* partials;
   uint32_t partials_bytes;
 };
 struct KvAttnPlan {
-  int R = 1, waves = 8;        // 16-row subtiles per workgroup, waves per workgroup
-  bool split = false;          // token chunks joined across workgroups
-  int target = 1;              // chunks wanted per KV head, all sequences together
-  int chunk_step = 0, tile_rows = 0;
-  int64_t items = 0, grid = 0;
+  int R = 1;                   // 16-row subtiles per workgroup
+  int hw_shift = 0;            // log2 of the KV heads per workgroup
+  int parts = 1;               // workgroups per group of heads
+  int64_t waves = 1;           // waves per head
+  int tile_rows = 0;           // rows of a partial
+  int64_t tiles = 0, grid = 0; // query tiles at most, workgroups
 };
 KvAttnPlan plan_kv_attention(int64_t T, int64_t B, int64_t Hk, int64_t G, bool one_each);
 hipError_t launch_kv_attention(const KvAttnArgs& a, const KvAttnPlan& p, int D, hipStream_t st);
