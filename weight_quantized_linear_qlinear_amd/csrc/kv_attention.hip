@@ -133,7 +133,6 @@ __device__ __forceinline__ void pv_piece(const Raw<2 * P, NT> (&v)[8], const f16
 #pragma unroll
       for (int r = 0; r < R; ++r) o[4 * d + n][r] = mfma_f16_k32(av, w[r], o[4 * d + n][r]);
     }
-    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -207,9 +206,6 @@ __device__ __forceinline__ int across16(int v, OP op) {       // over lanes l, l
 struct AddI {
   __device__ __forceinline__ int operator()(int a, int b) const { return a + b; }
 };
-struct MaxI {
-  __device__ __forceinline__ int operator()(int a, int b) const { return max(a, b); }
-};
 struct AddF {
   __device__ __forceinline__ int operator()(int a, int b) const {
     return __builtin_bit_cast(int, __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b));
@@ -235,8 +231,6 @@ __device__ __forceinline__ float sum_row16(float v) {
 }
 
 __device__ __forceinline__ int wave_sum(int v) { return across16(row16(v, AddI()), AddI()); }
-__device__ __forceinline__ int wave_max(int v) { return across16(row16(v, MaxI()), MaxI()); }
-
 __device__ __forceinline__ int wave_scan(int v) {             // inclusive
   v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);    // row_shr 1, 2, 4, 8
   v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
@@ -250,23 +244,15 @@ __device__ __forceinline__ int wave_scan(int v) {             // inclusive
 // The work of one KV head is a line of units (32 tokens of one query tile), tile after tile;
 // wave w of its waves takes units w U .. (w + 1) U - 1, whatever tiles they belong to.
 // `mine` is the extent of sequence `lane` (nq 0 past the last), kept for the first 64.
-struct Line {
-  int total, longest;            // units of all tiles, and of the longest one
-};
-
 template <int TR>
-__device__ __forceinline__ Line line_of(const KvAttnArgs& a, const Extent& mine, int lane) {
-  Line r{0, 1};
+__device__ __forceinline__ int total_units(const KvAttnArgs& a, const Extent& mine, int lane) {
+  int total = 0;
   for (int b0 = 0; b0 < a.B; b0 += 64) {
     Extent e = mine;
     if (b0) e = b0 + lane < a.B ? extent_of(a, b0 + lane) : Extent{};
-    const int n = (e.nq * a.G + TR - 1) / TR;
-    r.total += wave_sum(n * e.units());
-    r.longest = max(r.longest, wave_max(n ? e.units() : 1));
+    total += wave_sum((e.nq * a.G + TR - 1) / TR * e.units());
   }
-  r.total = __builtin_amdgcn_readfirstlane(r.total);
-  r.longest = __builtin_amdgcn_readfirstlane(r.longest);
-  return r;
+  return __builtin_amdgcn_readfirstlane(total);
 }
 
 struct Tile {
@@ -348,12 +334,6 @@ __device__ __forceinline__ void store_out(uint16_t* p, const float* v, float f) 
   }
 }
 
-#ifndef QTGT
-#define QTGT 256
-#endif
-#ifndef QMINT
-#define QMINT 1
-#endif
 template <int NG, int R>
 __global__ __launch_bounds__(kWaves * 64) void kv_attention_kernel(KvAttnArgs a) {
   constexpr int D = 32 * NG, TR = 16 * R;
@@ -376,12 +356,8 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attention_kernel(KvAttnArgs a)
   }
   const int h = hg * HW + (wave & (HW - 1)), me = part * TS + (wave >> a.hw_shift);   // head, place on its line
   const Extent mine_e = lane < a.B ? extent_of(a, lane) : Extent{};
-  const Line line = line_of<TR>(a, mine_e, lane);
-  // An equal share of the units, but while there are few, shares that keep the longest tile in
-  // kJoin chunks (one joining instead of two) as long as a wave then has QMINT units at most.
-  const int P = a.parts * TS;
-  const int U = max(max(1, (line.total + P - 1) / P), min((line.longest + kJoin - 1) / kJoin, QMINT));
-  const int u_end = min(line.total, (me + 1) * U);
+  const int total = total_units<TR>(a, mine_e, lane);
+  const int U = max(1, (total + a.parts * TS - 1) / (a.parts * TS)), u_end = min(total, (me + 1) * U);
   for (int u = me * U; u < u_end;) {
   const Tile it = tile_of<TR>(a, mine_e, u, lane);
   const int u_next = min(u_end, it.begin + it.units);
@@ -448,12 +424,13 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attention_kernel(KvAttnArgs a)
   // scales from the moment the scores are done, V from the moment the values are), and the pages
   // of the one after that.  Loads come back in the order of their issue, so what is wanted first
   // is asked for first, and none of them is behind a branch (past the last tile they read the
-  // pool's first entries).
+  // pool's first entries).  A second buffer changed nothing (1 % slower): the loads are bound by
+  // bandwidth, not by their latency.
   constexpr int KI = NG % 2 == 0 ? NG / 2 : NG;
   typedef typename std::conditional<NG % 2 == 0, u32x4, u32x2>::type KRaw;
   KRaw kr[2][KI];
   KScales<NG> ksr;
-  uint32_t vsr = 0;
+  uint32_t vsr;
   Raw<RB1, NT> v1[8];
   Raw<RB2, NT> v2[8];
   auto load_k = [&](int e0, int e1) {                        // and the scales: one token per lane
@@ -469,6 +446,7 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attention_kernel(KvAttnArgs a)
         else kr[u][n] = *reinterpret_cast<const u32x2*>(p + 32 * n + koff);
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
   auto load_v = [&](int e0, int e1) {
 #pragma unroll
@@ -480,6 +458,7 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attention_kernel(KvAttnArgs a)
         if constexpr (kTwo) v2[4 * u + j].load(p + (size_t)j * row_bytes + voff2);
       }
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
   auto wave_sync = [] {                                      // this wave's LDS writes before its reads
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -487,14 +466,10 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attention_kernel(KvAttnArgs a)
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
   };
 
-  constexpr int STEP = 32;
-  const int first = c0;
-  int e0 = entry_of(page_of(first), first), e1 = entry_of(page_of(first + 16), first + 16);
-  int g0 = page_of(first + STEP), g1 = page_of(first + STEP + 16);       // the next tile's pages
+    int e0 = entry_of(page_of(c0), c0), e1 = entry_of(page_of(c0 + 16), c0 + 16);   // of the tile's halves
+  int g0 = page_of(c0 + 32), g1 = page_of(c0 + 48);          // the next tile's pages
   load_k(e0, e1);
-  __builtin_amdgcn_sched_barrier(0);
   load_v(e0, e1);
-  __builtin_amdgcn_sched_barrier(0);
 
   // q: per query row a power of two into [-1, 1), fp16; rows past the last are zero.
   f16x8 qf[R][NG];
@@ -522,9 +497,9 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attention_kernel(KvAttnArgs a)
     cs[r] = __builtin_ldexpf(a.scale * kLog2e, ex);
   }
 
-  for (int base = first; base < c1; base += STEP) {
+  for (int base = c0; base < c1; base += 32) {
     const bool all_valid = e0 >= 0 && e1 >= 0 && base + 32 <= c1;
-    const int n0 = entry_of(g0, base + STEP), n1 = entry_of(g1, base + STEP + 16);
+    const int n0 = entry_of(g0, base + 32), n1 = entry_of(g1, base + 48);
     const int t0 = base + 4 * g4;                            // this lane's first token (u = j = 0)
     auto there = [&](int u, int j) { return (u ? e1 : e0) >= 0 && t0 + 16 * u + j < c1; };
     // V scales into the exponent.  A scale of zero (an entry never written) counts as the
@@ -566,9 +541,7 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attention_kernel(KvAttnArgs a)
 #pragma unroll
           for (int j = 0; j < 4; ++j) s[r][u][j] = n == 0 ? ks[j] * d[j] : __builtin_fmaf(ks[j], d[j], s[r][u][j]);
         }
-        if constexpr (NG > 4 || R > 1) __builtin_amdgcn_sched_barrier(0);
       }
-      __builtin_amdgcn_sched_barrier(0);                     // (fewer registers at once)
     }
     float lv[2][4], rv[2][4];
 #pragma unroll
@@ -577,9 +550,8 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attention_kernel(KvAttnArgs a)
       *reinterpret_cast<f32x4*>(rv[u]) = *reinterpret_cast<const f32x4*>(&mine.rv[16 * u + 4 * g4]);
     }
     load_k(n0, n1);
-    __builtin_amdgcn_sched_barrier(0);
-    g0 = page_of(base + 2 * STEP);
-    g1 = page_of(base + 2 * STEP + 16);
+    g0 = page_of(base + 64);
+    g1 = page_of(base + 80);
 
     // whole tile visible to every row of this workgroup?
     const int tmin_p = p0 + i0, tmax_p = p0 + i1;
@@ -636,6 +608,7 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attention_kernel(KvAttnArgs a)
     e0 = n0;
     e1 = n1;
   }
+
   // A lane has, per 16-row subtile, channels 2 P (4 g4 + j) .. + 2 P - 1 of each piece of its row.
   // (The copies keep the compiler from computing addresses ahead of the tile loop.)
   constexpr int W1 = 2 * P1::P, W2 = 2 * P2::P;
@@ -705,52 +678,71 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attention_kernel(KvAttnArgs a)
       if (last) reset_counter(counter);
     }
     if (!__builtin_amdgcn_readfirstlane(last)) break;
-    constexpr int DP = D / 4, RP = DP <= 64 ? 64 / DP : 1;   // 16-byte parts of a row, rows at a time
     for (int r = 0; r < R; ++r) {
       const int live = min(16, rows - r0 - 16 * r);
       if (live <= 0) break;
       wave_sync();
+      // 64 lanes over (row, 16-byte part); two passes' loads at a time, the first ahead of the factors
+      constexpr int DP = D / 4;
+      const int parts = live * DP;
+      constexpr int NP = 2;
+      f32x4 v[NP][kJoin];
+      auto load_parts = [&](int b) {
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+          const int id = min(b + 64 * k + lane, parts - 1), row = id / DP, dp = id % DP;
+#pragma unroll
+          for (int c = 0; c < kJoin; ++c)
+            v[k][c] = load_partial(rs, part_row(ch0 + min(c, n - 1) * stride, 16 * r + row) / 4 + dp);
+        }
+      };
       // factors 2^(M_c - M) of the chunks: four rows at a time, 16 lanes (chunks) per row
+      f32x2 ml[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int row = 4 * q + g4, c = c16;
+        const int64_t p = part_row(ch0 + min(c16, n - 1) * stride, 16 * r + min(4 * q + g4, live - 1));
+        ml[q] = __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, (int)((p + D) * 4), 0, kCachePolicySc1));
+      }
+      load_parts(0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int row = 4 * q + g4;
         if (4 * q >= live) break;                            // uniform
-        const int64_t p = part_row(ch0 + min(c, n - 1) * stride, 16 * r + min(row, live - 1));
-        f32x2 ml = __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, (int)((p + D) * 4), 0, kCachePolicySc1));
-        if (c >= n) ml = (f32x2){kNegInf, 0.0f};
-        const float M = max_row16(ml.x);
-        const float f = M == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ml.x - M);
-        const float L = sum_row16(ml.y * f);
-        mine.f[row][c] = f;
-        if (c == 0 && row < live) {
-          if (!done) {
-            const float out[2] = {M, L};
-            store_run<2>(rs, p + D, out);
-          } else if (a.lse) {
-            a.lse[out_row(r0 + 16 * r + row)] = L > 0.0f ? (M + __builtin_amdgcn_logf(L)) * kLn2 : kNegInf;
+        if (c16 >= n) ml[q] = (f32x2){kNegInf, 0.0f};
+        const float M = max_row16(ml[q].x);
+        const float f = M == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ml[q].x - M);
+        const float L = sum_row16(ml[q].y * f);
+        mine.f[row][c16] = f;
+        if (c16 == 0) {
+          mine.inv[row] = L > 0.0f ? 1.0f / L : 0.0f;
+          if (row < live) {
+            if (!done) {
+              const float out[2] = {M, L};
+              store_run<2>(rs, part_row(ch0, 16 * r + row) + D, out);
+            } else if (a.lse) {
+              a.lse[out_row(r0 + 16 * r + row)] = L > 0.0f ? (M + __builtin_amdgcn_logf(L)) * kLn2 : kNegInf;
+            }
           }
         }
-        if (c == 0) mine.inv[row] = L > 0.0f ? 1.0f / L : 0.0f;
       }
       wave_sync();
-      // sums: 64 lanes over (row, part)
-      for (int b = 0; b < live * DP; b += 64) {
-        const int id = min(b + lane, live * DP - 1), row = id / DP, dp = id % DP;
-        f32x4 v[kJoin];
+      for (int b = 0; b < parts; b += 64 * NP) {
+        if (b) load_parts(b);
 #pragma unroll
-        for (int c = 0; c < kJoin; ++c)
-          v[c] = load_partial(rs, part_row(ch0 + min(c, n - 1) * stride, 16 * r + row) / 4 + dp);
-        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < NP; ++k) {
+          const int id = b + 64 * k + lane, row = min(id, parts - 1) / DP, dp = id % DP;
+          f32x4 sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < kJoin; ++c) sum += v[c] * mine.f[row][c];   // f is 0 past the last
-        const float inv = mine.inv[row];
-        if (b + lane < live * DP) {
-          if (done) {
-            uint32_t* out = reinterpret_cast<uint32_t*>(a.out + out_row(r0 + 16 * r + row) * D + dp * 4);
-            out[0] = pack_bf16x2(sum.x * inv, sum.y * inv);
-            out[1] = pack_bf16x2(sum.z * inv, sum.w * inv);
-          } else {
-            store_partial(rs, part_row(ch0, 16 * r + row) / 4 + dp, sum);
+          for (int c = 0; c < kJoin; ++c) sum += v[k][c] * mine.f[row][c];   // f is 0 past the last
+          if (id < parts) {
+            if (done) {
+              const float inv = mine.inv[row];
+              uint32_t* out = reinterpret_cast<uint32_t*>(a.out + out_row(r0 + 16 * r + row) * D + dp * 4);
+              out[0] = pack_bf16x2(sum.x * inv, sum.y * inv);
+              out[1] = pack_bf16x2(sum.z * inv, sum.w * inv);
+            } else {
+              store_partial(rs, part_row(ch0, 16 * r + row) / 4 + dp, sum);
+            }
           }
         }
       }
@@ -778,7 +770,7 @@ KvAttnPlan plan_kv_attention(int64_t T, int64_t B, int64_t Hk, int64_t G, bool o
   while ((2 << p.hw_shift) <= kWaves && Hk % (2 << p.hw_shift) == 0) ++p.hw_shift;
   // One workgroup of four waves per CU (two measured slower, see above).
   const int64_t HG = Hk >> p.hw_shift;
-  const int64_t parts = QTGT / HG;
+  const int64_t parts = 256 / HG;
   p.parts = (int)(parts >= 8 ? parts / 8 * 8 : parts < 1 ? 1 : parts);
   p.grid = p.parts * HG;
   p.waves = p.parts * (kWaves >> p.hw_shift);
