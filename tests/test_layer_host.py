@@ -152,7 +152,7 @@ def test_attention_refusals():
     attn("window", window=-1)
     attn("causal", window=5, causal=0)
     need = qlq.kv_attention_workspace_bytes(4, 4, 32, 8, 128)
-    assert need > 131072
+    assert need > 262144
     attn("workspace", wb=need - 256)
     attn("workspace", ws=None)
     attn("256-byte", ws=ctypes.c_void_p(0x10010))
@@ -169,7 +169,7 @@ def test_workspace_sizes():
         for Hq, Hk in ((1, 1), (28, 4), (32, 8), (64, 1), (128, 128), (1023, 1023), (1024, 1024)):
             for D in (32, 128, 256):
                 for one in (True, False):
-                    assert 131072 < w(B, B, Hq, Hk, D, one) < (1 << 31)
+                    assert 262144 < w(B, B, Hq, Hk, D, one) < (1 << 31)
                     assert w(B, B, Hq, Hk, D, one) % 256 == 0
 
 

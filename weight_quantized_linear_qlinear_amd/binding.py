@@ -786,7 +786,7 @@ def kv_attention_workspace_bytes(T: int, B: int, Hq: int, Hk: int, D: int, one_e
     return int(lib().qlq_kv_attention_workspace_bytes(T, B, Hq, Hk, D, int(one_each)))
 
 
-_ATTENTION_COUNTER_BYTES = 131072
+_ATTENTION_COUNTER_BYTES = 262144
 _attention_workspaces: dict = {}
 
 

@@ -22,7 +22,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqlq.so")
 
 SOURCES = ["api.cpp", "quant_kernels.hip", "gemm_small.hip", "gemm_large.hip", "gemm_mfma.hip", "kv_codec.hip",
-           "rms_norm.hip", "rope_kv.hip", "kv_attention.hip"]
+           "rms_norm.hip", "rope_kv.hip", "kv_attention.hip", "kv_attention_tile.hip"]
 ARCH = os.environ.get("QLQ_OFFLOAD_ARCH", "gfx950")
 
 

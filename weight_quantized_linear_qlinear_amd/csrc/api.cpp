@@ -979,8 +979,8 @@ qlq_status qlq_kv_gather(const void* k_codes, const void* k_scales, const void* 
 
 // Attention workspace: a counter region of one fixed size for every plan (so that one call's
 // partial sums never land on another's counters), then two partial tiles per wave.  Counters: one
-// per level of joining (three), slot and head.
-constexpr size_t kAttnCounterBytes = 131072;
+// per level of joining (three), slot, head and (many rows) wave.
+constexpr size_t kAttnCounterBytes = 262144;
 constexpr int64_t kMaxAttnHeads = 1024;
 
 static bool attn_dims_ok(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D) {
@@ -1029,7 +1029,7 @@ qlq_status qlq_kv_attention(const void* q, int64_t q_stride, int64_t T, int64_t 
   const qlq::KvAttnPlan p = qlq::plan_kv_attention(T, B, Hk, Hq / Hk, q_start == nullptr);
   const size_t partial = attn_partial_bytes(p, Hk, D), need = kAttnCounterBytes + partial;
   if (p.tiles * (max_pages * page_size / 32 + 1) >= (int64_t(1) << 31) || partial >= ((size_t)1 << 31) ||
-      (size_t)p.waves * 2 * (size_t)Hk * 12 > kAttnCounterBytes || p.waves > 4096)
+      (size_t)p.counters * 12 > kAttnCounterBytes || p.waves > 4096)
     return fail(QLQ_ERR_UNSUPPORTED, "sizes too large for one call");
   if (!workspace || workspace_bytes < need)
     return fail(QLQ_ERR_INVALID_ARG, "workspace too small: need %zu bytes, got %zu", need,
@@ -1063,7 +1063,7 @@ qlq_status qlq_kv_attention(const void* q, int64_t q_stride, int64_t T, int64_t 
   a.parts = p.parts;
   a.tile_rows = p.tile_rows;
   a.hw_shift = p.hw_shift;
-  a.level_counters = (int)(p.waves * 2 * Hk);
+  a.level_counters = (int)p.counters;
   a.counters = static_cast<uint32_t*>(workspace);
   a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAttnCounterBytes);
   a.partials_bytes = (uint32_t)partial;

@@ -28,49 +28,13 @@
 // joined by the last to finish, in the order of the chunks.
 #include <type_traits>
 
-#include "qlq_device.h"
-#include "qlq_launch.h"
+#include "kv_attention.h"
 
 namespace qlq {
 
+using namespace attn;
+
 namespace {
-
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNegInf = -__builtin_inff();
-
-__device__ __forceinline__ f32x4 mfma_f16_k32(f16x8 a, f16x8 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-}
-
-__device__ __forceinline__ float f16_lo(uint32_t b) { return (float)__builtin_bit_cast(_Float16, (uint16_t)(b & 0xFFFF)); }
-__device__ __forceinline__ float f16_hi(uint32_t b) { return (float)__builtin_bit_cast(_Float16, (uint16_t)(b >> 16)); }
-
-// Two int8 codes (bytes 0, 1 or 2, 3 of w ^ 0x80808080) as fp16: 1024 + (q + 128) by its bit
-// pattern, minus 1152; exact.
-template <bool HI>
-__device__ __forceinline__ uint32_t i8x2_to_f16(uint32_t flipped) {
-  const uint32_t b = __builtin_amdgcn_perm(0x64646464u, flipped, HI ? 0x04030402u : 0x04010400u);
-  const f16x2 k = {(_Float16)1152.0f, (_Float16)1152.0f};
-  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, b) - k);
-}
-
-__device__ __forceinline__ f16x8 i8x8_to_f16(u32x2 w) {
-  const uint32_t a = w.x ^ 0x80808080u, b = w.y ^ 0x80808080u;
-  const u32x4 r = {i8x2_to_f16<false>(a), i8x2_to_f16<true>(a), i8x2_to_f16<false>(b), i8x2_to_f16<true>(b)};
-  return __builtin_bit_cast(f16x8, r);
-}
-
-template <bool HI>
-__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t w) {
-  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI));
-}
-
-// Memory that no kernel writes meanwhile, read through the scalar cache.
-typedef __attribute__((address_space(4))) const int32_t ConstInt;
 
 template <bool NT, class T>
 __device__ __forceinline__ T ld(const T* p) {
@@ -159,86 +123,13 @@ struct KScales {
   __device__ __forceinline__ float get(int i) const { return i & 1 ? f16_hi(d[i / 2]) : f16_lo(d[i / 2]); }
 };
 
-// Sequence b: its query tokens, its cached tokens, and the first of those any query can see
-// (rounded down to a tile of 32).
-struct Extent {
-  int qs, nq, L, begin;
-  __device__ __forceinline__ int units() const { return max(1, (L - begin + 31) >> 5); }   // tiles of 32 tokens
-};
-
-__device__ __forceinline__ Extent extent_of(const KvAttnArgs& a, int b) {
-  Extent e;
-  if (a.q_start) {
-    const int lo = min(max(a.q_start[b], 0), a.T), hi = min(max(a.q_start[b + 1], lo), a.T);
-    e.qs = lo;
-    e.nq = hi - lo;
-  } else {
-    e.qs = b;
-    e.nq = 1;
-  }
-  e.L = min(max(a.seq_lens[b], 0), a.max_tokens);
-  e.begin = a.window > 0 ? min(max(0, e.L - e.nq - a.window + 1), e.L) & ~31 : 0;
-  return e;
+// The first token that any query of the sequence can see (rounded down to a tile of 32), and
+// the tiles of 32 from there.
+__device__ __forceinline__ int begin_of(const KvAttnArgs& a, const Extent& e) {
+  return a.window > 0 ? min(max(0, e.L - e.nq - a.window + 1), e.L) & ~31 : 0;
 }
-
-// Cross-lane steps in the vector unit (no trip through LDS).
-template <int N>
-__device__ __forceinline__ int row_ror(int v) {               // within 16 lanes
-  return __builtin_amdgcn_mov_dpp(v, 0x120 + N, 0xf, 0xf, true);
-}
-
-template <class OP>
-__device__ __forceinline__ int row16(int v, OP op) {          // over 16 lanes, to each of them
-  v = op(v, row_ror<8>(v));
-  v = op(v, row_ror<4>(v));
-  v = op(v, row_ror<2>(v));
-  return op(v, row_ror<1>(v));
-}
-
-template <class OP>
-__device__ __forceinline__ int across16(int v, OP op) {       // over lanes l, l ^ 16, l ^ 32, l ^ 48
-  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-  v = op((int)a[0], (int)a[1]);
-  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  return op((int)b[0], (int)b[1]);
-}
-
-struct AddI {
-  __device__ __forceinline__ int operator()(int a, int b) const { return a + b; }
-};
-struct AddF {
-  __device__ __forceinline__ int operator()(int a, int b) const {
-    return __builtin_bit_cast(int, __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b));
-  }
-};
-struct MaxF {
-  __device__ __forceinline__ int operator()(int a, int b) const {
-    return __builtin_bit_cast(int, fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
-  }
-};
-
-__device__ __forceinline__ float max_across16(float v) {
-  return __builtin_bit_cast(float, across16(__builtin_bit_cast(int, v), MaxF()));
-}
-__device__ __forceinline__ float sum_across16(float v) {
-  return __builtin_bit_cast(float, across16(__builtin_bit_cast(int, v), AddF()));
-}
-__device__ __forceinline__ float max_row16(float v) {
-  return __builtin_bit_cast(float, row16(__builtin_bit_cast(int, v), MaxF()));
-}
-__device__ __forceinline__ float sum_row16(float v) {
-  return __builtin_bit_cast(float, row16(__builtin_bit_cast(int, v), AddF()));
-}
-
-__device__ __forceinline__ int wave_sum(int v) { return across16(row16(v, AddI()), AddI()); }
-__device__ __forceinline__ int wave_scan(int v) {             // inclusive
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);    // row_shr 1, 2, 4, 8
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast 15 into rows 1, 3
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast 31 into rows 2, 3
-  return v;
+__device__ __forceinline__ int units_of(const KvAttnArgs& a, const Extent& e) {
+  return max(1, (e.L - begin_of(a, e) + 31) >> 5);
 }
 
 // The work of one KV head is a line of units (32 tokens of one query tile), tile after tile;
@@ -250,7 +141,7 @@ __device__ __forceinline__ int total_units(const KvAttnArgs& a, const Extent& mi
   for (int b0 = 0; b0 < a.B; b0 += 64) {
     Extent e = mine;
     if (b0) e = b0 + lane < a.B ? extent_of(a, b0 + lane) : Extent{};
-    total += wave_sum((e.nq * a.G + TR - 1) / TR * e.units());
+    total += wave_sum((e.nq * a.G + TR - 1) / TR * units_of(a, e));
   }
   return __builtin_amdgcn_readfirstlane(total);
 }
@@ -269,7 +160,7 @@ __device__ __forceinline__ Tile tile_of(const KvAttnArgs& a, const Extent& mine,
   for (int b0 = 0; b0 < a.B; b0 += 64) {
     Extent e = mine;
     if (b0) e = b0 + lane < a.B ? extent_of(a, b0 + lane) : Extent{};
-    const int n = (e.nq * a.G + TR - 1) / TR * e.units();
+    const int n = (e.nq * a.G + TR - 1) / TR * units_of(a, e);
     const int inc = before + wave_scan(n);
     const uint64_t hit = __ballot(u < inc && u >= inc - n);
     if (hit) {
@@ -278,9 +169,8 @@ __device__ __forceinline__ Tile tile_of(const KvAttnArgs& a, const Extent& mine,
       t.e.qs = of(e.qs);
       t.e.nq = of(e.nq);
       t.e.L = of(e.L);
-      t.e.begin = of(e.begin);
       t.b = b0 + src;
-      t.units = t.e.units();
+      t.units = units_of(a, t.e);
       const int begin = of(inc - n);
       t.qt = (u - begin) / t.units;
       t.begin = begin + t.qt * t.units;
@@ -291,48 +181,17 @@ __device__ __forceinline__ Tile tile_of(const KvAttnArgs& a, const Extent& mine,
   return t;
 }
 
-// A wave's LDS: the token scales of its tile, or the factors of the chunks that it joins.
-constexpr int kJoin = 16;        // chunks joined at a time
 constexpr int kWaves = 4;
 
+// A wave's LDS: the token scales of its tile, or what joining needs.
 template <int NG>
 union WaveLds {
   struct {
     float ks[NG][32];            // K scales by group and token
     float lv[32], rv[32];        // log2 and reciprocal of the V scales
   };
-  struct {
-    float f[16][kJoin];          // by row and chunk
-    float inv[16];               // a row's reciprocal sum
-  };
+  JoinLds join;
 };
-
-// W floats (2, or a multiple of 4) to a partial row at float offset `at`.
-template <int W>
-__device__ __forceinline__ void store_run(__amdgpu_buffer_rsrc_t rs, int64_t at, const float* v) {
-  if constexpr (W == 2) {
-    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, (f32x2){v[0], v[1]}), rs, (int)(at * 4), 0, kCachePolicySc1);
-  } else {
-#pragma unroll
-    for (int e = 0; e < W; e += 4) store_partial(rs, (at + e) / 4, (f32x4){v[e], v[e + 1], v[e + 2], v[e + 3]});
-  }
-}
-
-// W values (even) times f to bf16 at p.
-template <int W>
-__device__ __forceinline__ void store_out(uint16_t* p, const float* v, float f) {
-  uint32_t d[W / 2];
-#pragma unroll
-  for (int e = 0; e < W; e += 2) d[e / 2] = pack_bf16x2(v[e] * f, v[e + 1] * f);
-  if constexpr (W == 2) {
-    *reinterpret_cast<uint32_t*>(p) = d[0];
-  } else if constexpr (W == 4) {
-    *reinterpret_cast<u32x2*>(p) = (u32x2){d[0], d[1]};
-  } else {
-#pragma unroll
-    for (int e = 0; e < W / 2; e += 4) st16(p + 2 * e, (u32x4){d[e], d[e + 1], d[e + 2], d[e + 3]});
-  }
-}
 
 template <int NG, int R>
 __global__ __launch_bounds__(kWaves * 64) void kv_attention_kernel(KvAttnArgs a) {
@@ -362,14 +221,16 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attention_kernel(KvAttnArgs a)
   const Tile it = tile_of<TR>(a, mine_e, u, lane);
   const int u_next = min(u_end, it.begin + it.units);
   // This tile's chunks: one per wave that its units reach
-  const int wf = it.begin / U, nch = (it.begin + it.units - 1) / U - wf + 1, ch = me - wf;
+  const int wf = it.begin / U;
+  const Chunks ck{wf, (it.begin + it.units - 1) / U - wf + 1, me - wf};
   const int nq = it.e.nq, L = it.e.L, r0 = it.qt * TR, rows = nq * a.G;
   const int i0 = r0 / a.G, i1 = min(nq - 1, (r0 + TR - 1) / a.G);
   const int p0 = L - nq;                                     // position of query 0
   const int tend = min(max(a.causal ? p0 + i1 + 1 : L, 0), L);
   const int tbeg = a.window > 0 ? min(max(0, p0 + i0 - a.window + 1), tend) & ~31 : 0;
-  const int c0 = max(tbeg, it.e.begin + 32 * (u - it.begin));              // a multiple of 32
-  const int c1 = min(tend, it.e.begin + 32 * (u_next - it.begin));
+  const int begin = begin_of(a, it.e);
+  const int c0 = max(tbeg, begin + 32 * (u - it.begin));              // a multiple of 32
+  const int c1 = min(tend, begin + 32 * (u_next - it.begin));
   u = u_next;
 
   int c16 = lane & 15, g4 = lane >> 4;
@@ -460,13 +321,7 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attention_kernel(KvAttnArgs a)
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto wave_sync = [] {                                      // this wave's LDS writes before its reads
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-  };
-
-    int e0 = entry_of(page_of(c0), c0), e1 = entry_of(page_of(c0 + 16), c0 + 16);   // of the tile's halves
+  int e0 = entry_of(page_of(c0), c0), e1 = entry_of(page_of(c0 + 16), c0 + 16);   // of the tile's halves
   int g0 = page_of(c0 + 32), g1 = page_of(c0 + 48);          // the next tile's pages
   load_k(e0, e1);
   load_v(e0, e1);
@@ -613,12 +468,9 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attention_kernel(KvAttnArgs a)
   // (The copies keep the compiler from computing addresses ahead of the tile loop.)
   constexpr int W1 = 2 * P1::P, W2 = 2 * P2::P;
   asm volatile("" : "+v"(c16), "+v"(g4));
-  const bool split = nch > 1;
+  const bool split = ck.count > 1;
   const __amdgpu_buffer_rsrc_t rs = partial_rsrc(a.partials, a.partials_bytes);
-  // A wave has at most two chunks of tiles that it shares: the tile that began before it (slot
-  // 2 w) and the one that goes on after it (2 w + 1).  Partial row: [D sums][M, L, -, -].
-  auto slot_of = [&](int c) { return 2 * (wf + c) + (c == 0 ? 1 : 0); };
-  auto part_row = [&](int c, int row) { return (int64_t)((slot_of(c) * hk + h) * a.tile_rows + row) * (D + 4); };
+  auto part_row = [&](int c, int row) { return (int64_t)((ck.slot(c) * hk + h) * a.tile_rows + row) * (D + 4); };
   auto out_row = [&](int grow) {                             // index of [token][query head]
     const int i = grow / a.G;
     return (int64_t)(it.e.qs + i) * a.Hq + h * a.G + (grow - i * a.G);
@@ -648,7 +500,7 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attention_kernel(KvAttnArgs a)
         }
         if (a.lse && g4 == 0) a.lse[at] = L > 0.0f ? (m[r] + __builtin_amdgcn_logf(L)) * kLn2 : kNegInf;
       } else {
-        const int64_t p = part_row(ch, row);
+        const int64_t p = part_row(ck.mine, row);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           store_run<W1>(rs, p + (4 * g4 + j) * W1, v1r[j]);
@@ -663,92 +515,8 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attention_kernel(KvAttnArgs a)
   }
   if (!split) continue;
 
-  // Join the chunks, kJoin at a time, then those groups, and so on: the last wave of a group to
-  // finish joins it (always in chunk order) into the group's first partial rows, the last group
-  // of all into the output.
-  for (int level = 0, stride = 1;; ++level, stride *= kJoin) {
-    const int ch0 = ch - ch % (stride * kJoin);
-    const int n = min(kJoin, (nch - ch0 + stride - 1) / stride);
-    const bool done = stride * kJoin >= nch;                 // one group: joins into the output
-    wait_stores_performed();
-    uint32_t* counter = a.counters + level * a.level_counters + slot_of(ch0) * hk + h;
-    int last = 0;
-    if (lane == 0) {
-      last = arrive(counter) + 1u == (uint32_t)n;
-      if (last) reset_counter(counter);
-    }
-    if (!__builtin_amdgcn_readfirstlane(last)) break;
-    for (int r = 0; r < R; ++r) {
-      const int live = min(16, rows - r0 - 16 * r);
-      if (live <= 0) break;
-      wave_sync();
-      // 64 lanes over (row, 16-byte part); two passes' loads at a time, the first ahead of the factors
-      constexpr int DP = D / 4;
-      const int parts = live * DP;
-      constexpr int NP = 2;
-      f32x4 v[NP][kJoin];
-      auto load_parts = [&](int b) {
-#pragma unroll
-        for (int k = 0; k < NP; ++k) {
-          const int id = min(b + 64 * k + lane, parts - 1), row = id / DP, dp = id % DP;
-#pragma unroll
-          for (int c = 0; c < kJoin; ++c)
-            v[k][c] = load_partial(rs, part_row(ch0 + min(c, n - 1) * stride, 16 * r + row) / 4 + dp);
-        }
-      };
-      // factors 2^(M_c - M) of the chunks: four rows at a time, 16 lanes (chunks) per row
-      f32x2 ml[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t p = part_row(ch0 + min(c16, n - 1) * stride, 16 * r + min(4 * q + g4, live - 1));
-        ml[q] = __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, (int)((p + D) * 4), 0, kCachePolicySc1));
-      }
-      load_parts(0);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int row = 4 * q + g4;
-        if (4 * q >= live) break;                            // uniform
-        if (c16 >= n) ml[q] = (f32x2){kNegInf, 0.0f};
-        const float M = max_row16(ml[q].x);
-        const float f = M == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ml[q].x - M);
-        const float L = sum_row16(ml[q].y * f);
-        mine.f[row][c16] = f;
-        if (c16 == 0) {
-          mine.inv[row] = L > 0.0f ? 1.0f / L : 0.0f;
-          if (row < live) {
-            if (!done) {
-              const float out[2] = {M, L};
-              store_run<2>(rs, part_row(ch0, 16 * r + row) + D, out);
-            } else if (a.lse) {
-              a.lse[out_row(r0 + 16 * r + row)] = L > 0.0f ? (M + __builtin_amdgcn_logf(L)) * kLn2 : kNegInf;
-            }
-          }
-        }
-      }
-      wave_sync();
-      for (int b = 0; b < parts; b += 64 * NP) {
-        if (b) load_parts(b);
-#pragma unroll
-        for (int k = 0; k < NP; ++k) {
-          const int id = b + 64 * k + lane, row = min(id, parts - 1) / DP, dp = id % DP;
-          f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < kJoin; ++c) sum += v[k][c] * mine.f[row][c];   // f is 0 past the last
-          if (id < parts) {
-            if (done) {
-              const float inv = mine.inv[row];
-              uint32_t* out = reinterpret_cast<uint32_t*>(a.out + out_row(r0 + 16 * r + row) * D + dp * 4);
-              out[0] = pack_bf16x2(sum.x * inv, sum.y * inv);
-              out[1] = pack_bf16x2(sum.z * inv, sum.w * inv);
-            } else {
-              store_partial(rs, part_row(ch0, 16 * r + row) / 4 + dp, sum);
-            }
-          }
-        }
-      }
-    }
-    if (done) break;
-  }
+  join_chunks<D>(a, rs, mine.join, lane, ck, min(TR, rows - r0), part_row, [&](int row) { return out_row(r0 + row); },
+                 [&](int level, int c) { return level * a.level_counters + ck.slot(c) * hk + h; });
   }
 }
 
@@ -761,9 +529,23 @@ hipError_t launch_ng(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t st) {
 
 }  // namespace
 
+#ifndef QR2
+#define QR2 32
+#endif
 KvAttnPlan plan_kv_attention(int64_t T, int64_t B, int64_t Hk, int64_t G, bool one_each) {
   KvAttnPlan p;
   const int64_t rows = one_each ? G : (T + B - 1) / B * G;   // query rows of an average sequence
+  if (rows > QR2) {
+    // Many rows: kv_attention_tile.hip, one workgroup of eight waves per CU.
+    p.R = 16;
+    p.parts = (int)(Hk >= 256 ? 1 : 256 / Hk);
+    p.grid = p.parts * Hk;
+    p.waves = p.parts;
+    p.tile_rows = 256;
+    p.counters = 2 * p.parts * Hk * 8;
+    p.tiles = one_each ? B * ((G + 255) / 256) : T * G / 256 + B;
+    return p;
+  }
   p.R = rows <= 16 ? 1 : 2;
   const int64_t TR = 16 * p.R;
   // Neighbouring KV heads per workgroup: a power of two that divides Hk, at most the waves.
@@ -775,11 +557,13 @@ KvAttnPlan plan_kv_attention(int64_t T, int64_t B, int64_t Hk, int64_t G, bool o
   p.grid = p.parts * HG;
   p.waves = p.parts * (kWaves >> p.hw_shift);
   p.tile_rows = (int)(one_each && G < TR ? G : TR);
+  p.counters = 2 * p.waves * Hk;
   p.tiles = one_each ? B * ((G + TR - 1) / TR) : T * G / TR + B;
   return p;
 }
 
 hipError_t launch_kv_attention(const KvAttnArgs& a, const KvAttnPlan& p, int D, hipStream_t st) {
+  if (p.R == 16) return launch_kv_attention_tile(a, p, D, st);
   switch (D / 32) {
     case 1: return launch_ng<1>(a, p, st);
     case 2: return launch_ng<2>(a, p, st);

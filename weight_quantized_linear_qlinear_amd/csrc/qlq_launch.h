@@ -131,14 +131,16 @@ struct KvAttnArgs {
   uint32_t partials_bytes;
 };
 struct KvAttnPlan {
-  int R = 1;                   // 16-row subtiles per workgroup
+  int R = 1;                   // 16-row subtiles of query rows per wave (16: per workgroup, kv_attention_tile.hip)
   int hw_shift = 0;            // log2 of the KV heads per workgroup
   int parts = 1;               // workgroups per group of heads
-  int64_t waves = 1;           // waves per head
+  int64_t waves = 1;           // parts that a head's work is cut into
+  int64_t counters = 0;        // arrival counters per level of joining
   int tile_rows = 0;           // rows of a partial
   int64_t tiles = 0, grid = 0; // query tiles at most, workgroups
 };
 KvAttnPlan plan_kv_attention(int64_t T, int64_t B, int64_t Hk, int64_t G, bool one_each);
+hipError_t launch_kv_attention_tile(const KvAttnArgs& a, const KvAttnPlan& p, int D, hipStream_t st);
 hipError_t launch_kv_attention(const KvAttnArgs& a, const KvAttnPlan& p, int D, hipStream_t st);
 
 // Raises kernel k's dynamic-LDS limit to `bytes` on the current device, once per
