@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import math
 import os
 import threading
@@ -490,13 +491,20 @@ def kv_cache(slots: int, heads: int, head_dim: int, device: torch.device | str |
 
 
 # ---------------------------------------------------------------------- between the linears
+# These calls take a few microseconds on the GPU, so what the host does before them counts: the raw
+# handle of the current stream without a Stream object (0.1 against 1.9 us), outputs by empty_like.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _enqueue(dev: torch.device, fn, *args):
     """fn(*args, the current stream of dev), with dev as the current device."""
-    if dev.index == torch.cuda.current_device():
-        status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+    index = dev.index
+    if index == torch.cuda.current_device():
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, torch.cuda.current_stream(dev).cuda_stream)
+            status = fn(*args, _raw_stream(index))
     if status != 0:
         _check(status)
 
@@ -538,7 +546,7 @@ def _norm_inputs(x, weight, residual, residual_out):
 
 def _norm_codes(x, qtype, out):
     if out is None:
-        return torch.empty(x.shape, dtype=code_dtype(qtype), device=x.device)
+        return torch.empty_like(x, dtype=code_dtype(qtype))
     if out.element_size() != 1 or out.shape != x.shape:
         raise ValueError(f"out must be 1-byte codes {list(x.shape)}")
     _on(x.device, out)
@@ -582,7 +590,7 @@ def rms_norm_quant_dynamic(x: torch.Tensor, weight: torch.Tensor, qtype: str, ep
     residual_out = _norm_inputs(x, weight, residual, residual_out)
     out = _norm_codes(x, qtype, out)
     if x_scale is None:
-        x_scale = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+        x_scale = x.new_empty(x.shape[0], dtype=torch.float32)
     elif x_scale.dtype != torch.float32 or x_scale.numel() != x.shape[0]:
         raise ValueError(f"x_scale must be fp32 [{x.shape[0]}]")
     else:
@@ -686,16 +694,15 @@ def _frequencies(inv_freq: torch.Tensor, dev: torch.device) -> int:
 
 def _cache_entries(c: QuantizedKV, H: int, D: int, dev: torch.device) -> int:
     """Slots of a cache for H heads of D channels."""
-    P = c.k_codes.shape[0]
+    kc, ks, vc, vs = c.k_codes, c.k_scales, c.v_codes, c.v_scales
+    P = kc.shape[0]
     if D % 32 != 0:
         raise ValueError("head_dim must be a multiple of 32")
-    if (c.k_codes.shape != (P, H, D) or c.v_codes.shape != (P, H, D) or c.k_scales.shape != (P, H, D // 32)
-            or c.v_scales.shape != (P, H)):
+    if kc.shape != (P, H, D) or vc.shape != kc.shape or ks.shape != (P, H, D // 32) or vs.shape != (P, H):
         raise ValueError(f"the cache must hold [slots, {H}, {D}] entries")
-    if (c.k_codes.element_size() != 1 or c.v_codes.element_size() != 1 or c.k_scales.dtype != torch.float16
-            or c.v_scales.dtype != torch.float16):
+    if kc.element_size() != 1 or vc.element_size() != 1 or ks.dtype != torch.float16 or vs.dtype != torch.float16:
         raise ValueError("the cache must hold 1-byte codes and float16 scales")
-    _on(dev, c.k_codes, c.k_scales, c.v_codes, c.v_scales)
+    _on(dev, kc, ks, vc, vs)
     return P
 
 
@@ -708,10 +715,11 @@ def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, atten
     R = _frequencies(inv_freq, x.device)
     p64 = _indices(positions, T, x.device, "positions")
     if out is None:
-        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=x.device)
-    os_ = _token_rows(out, "out")
-    if out.shape != x.shape or out.device != x.device:
-        raise ValueError(f"out must be bf16 {list(x.shape)} on {x.device}")
+        out, os_ = torch.empty_like(x, memory_format=torch.contiguous_format), H * D
+    else:
+        os_ = _token_rows(out, "out")
+        if out.shape != x.shape or out.device != x.device:
+            raise ValueError(f"out must be bf16 {list(x.shape)} on {x.device}")
     _enqueue(x.device, lib().qlq_rope, x.data_ptr(), xs, T, H, D, positions.data_ptr(), p64, inv_freq.data_ptr(), R,
              float(attention_factor), int(interleaved), out.data_ptr(), os_)
     return out
@@ -746,10 +754,11 @@ def rope_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions:
     R = _frequencies(inv_freq, dev)
     p64, s64 = _indices(positions, T, dev, "positions"), _indices(slots, T, dev, "slots")
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-    os_ = _token_rows(q_out, "q_out")
-    if q_out.shape != q.shape or q_out.device != dev:
-        raise ValueError(f"q_out must be bf16 {list(q.shape)} on {dev}")
+        q_out, os_ = torch.empty_like(q, memory_format=torch.contiguous_format), Hq * D
+    else:
+        os_ = _token_rows(q_out, "q_out")
+        if q_out.shape != q.shape or q_out.device != dev:
+            raise ValueError(f"q_out must be bf16 {list(q.shape)} on {dev}")
     _enqueue(dev, lib().qlq_rope_kv_append, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, Hq, Hk, D,
              positions.data_ptr(), p64, inv_freq.data_ptr(), R, float(attention_factor), int(interleaved),
              slots.data_ptr(), s64, P, cache.k_codes.data_ptr(), cache.k_scales.data_ptr(), cache.v_codes.data_ptr(),
@@ -770,7 +779,7 @@ def kv_gather(cache: QuantizedKV, slots: torch.Tensor, k_out: torch.Tensor | Non
     outs = []
     for t in (k_out, v_out):
         if t is None:
-            t = torch.empty((n, H, D), dtype=torch.bfloat16, device=dev)
+            t = torch.empty_like(outs[0]) if outs else torch.empty(n, H, D, dtype=torch.bfloat16, device=dev)
         elif t.dtype != torch.bfloat16 or t.shape != (n, H, D):
             raise ValueError(f"k_out and v_out must be bf16 [{n}, {H}, {D}]")
         else:
@@ -781,6 +790,7 @@ def kv_gather(cache: QuantizedKV, slots: torch.Tensor, k_out: torch.Tensor | Non
     return outs[0], outs[1]
 
 
+@functools.lru_cache(maxsize=1024)
 def kv_attention_workspace_bytes(T: int, B: int, Hq: int, Hk: int, D: int, one_each: bool = True) -> int:
     """Workspace of kv_attention for T query tokens of B sequences (one_each: without q_start)."""
     return int(lib().qlq_kv_attention_workspace_bytes(T, B, Hq, Hk, D, int(one_each)))
@@ -794,7 +804,7 @@ def _attention_workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
     """A workspace of this stream with its counters zeroed, grown on demand; inside a graph capture, one of the
     graph's own (its zero fill is recorded with it), so that graphs and streams never share one."""
     capturing = torch.cuda.is_current_stream_capturing()
-    key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
+    key = (dev.index, _raw_stream(dev.index))
     ws = None if capturing else _attention_workspaces.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
@@ -832,19 +842,17 @@ def kv_attention(q: torch.Tensor, cache: QuantizedKV, block_table: torch.Tensor,
     if q_start is not None and (q_start.dtype != torch.int32 or q_start.shape != (B + 1,)):
         raise ValueError(f"q_start must be int32 [{B + 1}]")
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     elif out.dtype != torch.bfloat16 or out.shape != q.shape:
         raise ValueError(f"out must be bf16 {list(q.shape)}")
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (T, Hq)):
         raise ValueError(f"lse must be fp32 [{T}, {Hq}]")
     _on(dev, block_table, seq_lens, q_start, out, lse, workspace)
-    L = lib()
     if workspace is None:
-        need = L.qlq_kv_attention_workspace_bytes(T, B, Hq, Hk, D, int(q_start is None))
-        workspace = _attention_workspace(dev, need)
-    _enqueue(dev, L.qlq_kv_attention, q.data_ptr(), qs, T, B, Hq, Hk, D, cache.k_codes.data_ptr(),
+        workspace = _attention_workspace(dev, kv_attention_workspace_bytes(T, B, Hq, Hk, D, q_start is None))
+    _enqueue(dev, lib().qlq_kv_attention, q.data_ptr(), qs, T, B, Hq, Hk, D, cache.k_codes.data_ptr(),
              cache.k_scales.data_ptr(), cache.v_codes.data_ptr(), cache.v_scales.data_ptr(), P,
              block_table.data_ptr(), block_table.shape[1], page_size, seq_lens.data_ptr(), _addr(q_start),
              D ** -0.5 if scale is None else float(scale), int(causal), int(window), out.data_ptr(), _addr(lse),
-             _addr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size())
+             workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out

@@ -103,6 +103,7 @@ struct RopeArgs {
   uint8_t* v_codes;
   uint16_t* v_scales;
   int vec_in, vec_out;         // 16-byte aligned rows
+  int TW;                      // tokens per workgroup (set by the launcher)
 };
 hipError_t launch_rope_kv(const RopeArgs& a, hipStream_t st);
 hipError_t launch_kv_gather(const void* kq, const void* ks, const void* vq, const void* vs, int64_t pool, int H, int D,

@@ -4,10 +4,13 @@
 //   rho = 1 / sqrt(mean_k h^2 + eps),   y = h * rho * w   (fp32),
 //   out: bf16(y)  |  sat(rne(y / input_scale))  |  s = absmax_k |y| / qmax, sat(rne(y / s)).
 //
-// The codes are taken from the fp32 y: one rounding, where a norm to bf16 followed by the
+// The codes are taken from the fp32 value: one rounding, where a norm to bf16 followed by the
 // quantizer has two (and two more passes over the rows).  Sums and the statistics are fp32.
-// The division of the codes is RcpDiv's (an fp32 quotient to within one ulp) for scales in
-// [2^-100, 2^100], the IEEE one outside.
+// y / s = (h w) g with one factor per row, g = rho / input_scale or, as s = absmax |h w| rho /
+// qmax, g = qmax / absmax |h w|: the dynamic codes do not depend on rho, so a row needs one
+// reduction (its sum of squares and its absmax together), and an element one product for its
+// code instead of a division.  rho and g are formed in fp64, once per row.  A g outside fp32's
+// normal range (scales below 2^-126 or above 2^126 of the values) divides element by element.
 //
 // Bound by HBM for many rows (2 K bytes of x, 2 K of the residual in and out, K of codes per
 // row) and by latency for few: a row is read once, kept in registers as fp32 (8 elements per
@@ -43,39 +46,44 @@ __device__ __forceinline__ float wave_absmax(float v) {
   return v;
 }
 
-__device__ __forceinline__ bool rcp_scale(float s) { return s >= 0x1p-100f && s <= 0x1p100f; }
-
-__device__ __forceinline__ uint32_t code1(float v, int fp8) {
-  return fp8 ? f32_to_e4m3_sat(v) : f32_to_i8_sat(v);
-}
-
-template <class DIV>
-__device__ __forceinline__ uint32_t code4(const float* v, int fp8, const DIV& dv) {
-  const float a = dv(v[0]), b = dv(v[1]), c = dv(v[2]), d = dv(v[3]);
-  if (fp8) return f32x4_to_e4m3x4_sat(a, b, c, d);
-  return f32_to_i8_sat(a) | (f32_to_i8_sat(b) << 8) | (f32_to_i8_sat(c) << 16) | (f32_to_i8_sat(d) << 24);
-}
-
-struct IeeeDiv {
-  float s;
-  __device__ __forceinline__ explicit IeeeDiv(float s_) : s(s_) {}
-  __device__ __forceinline__ float operator()(float x) const { return x / s; }
+// Code of v g, or of v / d g where g is not a normal number (d: what g would divide by).
+struct Coder {
+  float g, num, den;             // g = num / den
+  int fp8;
+  bool plain;
+  __device__ __forceinline__ Coder(double n, double d, int fp8_) : num((float)n), den((float)d), fp8(fp8_) {
+    const double q = n / d;
+    g = (float)q;
+    plain = q >= 0x1p-126 && q <= 0x1p126;
+  }
+  __device__ __forceinline__ float scaled(float v) const { return plain ? v * g : v / den * num; }
+  __device__ __forceinline__ uint32_t one(float v) const {
+    const float c = scaled(v);
+    return fp8 ? f32_to_e4m3_sat(c) : f32_to_i8_sat(c);
+  }
+  __device__ __forceinline__ uint32_t four(const float* v) const {
+    const float a = scaled(v[0]), b = scaled(v[1]), c = scaled(v[2]), d = scaled(v[3]);
+    if (fp8) return f32x4_to_e4m3x4_sat(a, b, c, d);
+    return f32_to_i8_sat(a) | (f32_to_i8_sat(b) << 8) | (f32_to_i8_sat(c) << 16) | (f32_to_i8_sat(d) << 24);
+  }
 };
 
-// A workgroup's sum or maximum per row of T threads (T = 64: a wave; else through `red`).
+// A row's 1 / sqrt(mean + eps) in fp64 from its fp32 sum of squares.
+__device__ __forceinline__ double rho_of(float ss, int K, float eps) { return 1.0 / sqrt((double)ss / K + (double)eps); }
+
+// Sum of v and maximum of w over a row of T threads (T = 64: a wave; else through `red`).
 template <int T, bool MAX>
-__device__ __forceinline__ float row_reduce(float v, float* red) {
-  v = MAX ? wave_absmax(v) : wave_sum(v);
+__device__ __forceinline__ void row_reduce(float& v, float& w, float (*red)[2]) {
+  v = wave_sum(v);
+  if constexpr (MAX) w = wave_absmax(w);
   if constexpr (T > 64) {
-    const int w = threadIdx.x >> 6;
+    const int i = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) red[i][0] = v, red[i][1] = w;
     __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[w] = v;
-    __syncthreads();
-    v = red[0];
+    v = red[0][0], w = red[0][1];
 #pragma unroll
-    for (int i = 1; i < T / 64; ++i) v = MAX ? fmaxf(v, red[i]) : v + red[i];
+    for (int k = 1; k < T / 64; ++k) v += red[k][0], w = fmaxf(w, red[k][1]);
   }
-  return v;
 }
 
 // T threads per row (64: four rows per workgroup of 256; 256 or 1024: one row per workgroup),
@@ -83,7 +91,7 @@ __device__ __forceinline__ float row_reduce(float v, float* red) {
 template <int OUT, int T, int NC>
 __global__ __launch_bounds__(T == 64 ? 256 : T) void rms_norm_kernel(NormArgs a) {
   constexpr int RPW = T == 64 ? 4 : 1;
-  __shared__ float red[T > 64 ? T / 64 : 1];
+  __shared__ float red[T > 64 ? T / 64 : 1][2];
   const int t = T == 64 ? (threadIdx.x & 63) : threadIdx.x;
   const int m = blockIdx.x * RPW + (T == 64 ? (threadIdx.x >> 6) : 0);
   if (m >= a.M) return;                                       // whole waves; T > 64 has no idle row
@@ -123,8 +131,6 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void rms_norm_kernel(NormArgs a)
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(h[c][e], h[c][e], ss);
   }
-  ss = row_reduce<T, false>(ss, red);
-  const float rho = 1.0f / sqrtf(ss / (float)a.K + a.eps);
   if (a.res_out) {
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
@@ -136,43 +142,39 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void rms_norm_kernel(NormArgs a)
   }
   float am = 0.0f;
 #pragma unroll
-  for (int c = 0; c < NC; ++c) {
+  for (int c = 0; c < NC; ++c) {                              // h w
     const uint32_t wd[4] = {wr[c].x, wr[c].y, wr[c].z, wr[c].w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      h[c][2 * e] = h[c][2 * e] * rho * bf16_bits_to_f32(wd[e] & 0xFFFF);
-      h[c][2 * e + 1] = h[c][2 * e + 1] * rho * bf16_bits_to_f32(wd[e] >> 16);
+      h[c][2 * e] *= bf16_bits_to_f32(wd[e] & 0xFFFF);
+      h[c][2 * e + 1] *= bf16_bits_to_f32(wd[e] >> 16);
       if constexpr (OUT == kNormDynamic)
         am = fmaxf(am, fmaxf(fabsf(h[c][2 * e]), fabsf(h[c][2 * e + 1])));
     }
   }
+  row_reduce<T, OUT == kNormDynamic>(ss, am, red);
+  const double rho = rho_of(ss, a.K, a.eps);
   if constexpr (OUT == kNormBf16) {
+    const float r = (float)rho;
     uint16_t* y = static_cast<uint16_t*>(a.y) + base;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const int i = t + c * T;
       if (i < nv)
-        st16(y + i * 8, (u32x4){pack_bf16x2(h[c][0], h[c][1]), pack_bf16x2(h[c][2], h[c][3]),
-                                pack_bf16x2(h[c][4], h[c][5]), pack_bf16x2(h[c][6], h[c][7])});
+        st16(y + i * 8, (u32x4){pack_bf16x2(h[c][0] * r, h[c][1] * r), pack_bf16x2(h[c][2] * r, h[c][3] * r),
+                                pack_bf16x2(h[c][4] * r, h[c][5] * r), pack_bf16x2(h[c][6] * r, h[c][7] * r)});
     }
   } else {
-    float s = a.input_scale;
-    if constexpr (OUT == kNormDynamic) {
-      am = row_reduce<T, true>(am, red);
-      s = am == 0.0f ? 1.0f : am / (a.fp8 ? 448.0f : 127.0f);
-      if (t == 0) a.y_scale[m] = s;
-    }
+    const double qmax = a.fp8 ? 448.0 : 127.0;
+    if (OUT == kNormDynamic && t == 0) a.y_scale[m] = am == 0.0f ? 1.0f : (float)((double)am * rho / qmax);
+    const Coder code = OUT == kNormStatic ? Coder(rho, (double)a.input_scale, a.fp8)
+                                          : Coder(qmax, am == 0.0f ? 1.0 : (double)am, a.fp8);
     uint8_t* y = static_cast<uint8_t*>(a.y) + base;
-    auto emit = [&](const auto& dv) {
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const int i = t + c * T;
-        if (i < nv)
-          *reinterpret_cast<u32x2*>(y + i * 8) = (u32x2){code4(h[c], a.fp8, dv), code4(h[c] + 4, a.fp8, dv)};
-      }
-    };
-    if (rcp_scale(s)) emit(RcpDivAny(s));
-    else emit(IeeeDiv(s));
+    for (int c = 0; c < NC; ++c) {
+      const int i = t + c * T;
+      if (i < nv) *reinterpret_cast<u32x2*>(y + i * 8) = (u32x2){code.four(h[c]), code.four(h[c] + 4)};
+    }
   }
 }
 
@@ -181,36 +183,30 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void rms_norm_kernel(NormArgs a)
 // be the inputs here too.
 template <int OUT>
 __global__ __launch_bounds__(256) void rms_norm_any_kernel(NormArgs a) {
-  __shared__ float red[4];
+  __shared__ float red[4][2];
   const int t = threadIdx.x, m = blockIdx.x;
   const int64_t base = (int64_t)m * a.K;
   auto load = [&](int k) {
     const float v = bf16_bits_to_f32(a.x[base + k]);
     return a.res ? v + bf16_bits_to_f32(a.res[base + k]) : v;
   };
-  float ss = 0.0f;
+  float ss = 0.0f, am = 0.0f;
   for (int k = t; k < a.K; k += 256) {
     const float v = load(k);
     ss = __builtin_fmaf(v, v, ss);
+    if constexpr (OUT == kNormDynamic) am = fmaxf(am, fabsf(v * bf16_bits_to_f32(a.w[k])));
   }
-  ss = row_reduce<256, false>(ss, red);
-  const float rho = 1.0f / sqrtf(ss / (float)a.K + a.eps);
-  float s = a.input_scale;
-  if constexpr (OUT == kNormDynamic) {
-    float am = 0.0f;
-    for (int k = t; k < a.K; k += 256) am = fmaxf(am, fabsf(load(k) * rho * bf16_bits_to_f32(a.w[k])));
-    am = row_reduce<256, true>(am, red);
-    s = am == 0.0f ? 1.0f : am / (a.fp8 ? 448.0f : 127.0f);
-    if (t == 0) a.y_scale[m] = s;
-  }
-  const bool rcp = OUT != kNormBf16 && rcp_scale(s);
-  const RcpDivAny dv(rcp ? s : 1.0f);
+  row_reduce<256, OUT == kNormDynamic>(ss, am, red);
+  const double rho = rho_of(ss, a.K, a.eps), qmax = a.fp8 ? 448.0 : 127.0;
+  const float r = (float)rho;
+  if (OUT == kNormDynamic && t == 0) a.y_scale[m] = am == 0.0f ? 1.0f : (float)((double)am * rho / qmax);
+  const Coder code = OUT == kNormStatic ? Coder(rho, (double)a.input_scale, a.fp8)
+                                        : Coder(qmax, am == 0.0f ? 1.0 : (double)am, a.fp8);
   for (int k = t; k < a.K; k += 256) {
-    const float v = load(k);
-    const float y = v * rho * bf16_bits_to_f32(a.w[k]);
+    const float v = load(k), hw = v * bf16_bits_to_f32(a.w[k]);
     if (a.res_out) a.res_out[base + k] = (uint16_t)(pack_bf16x2(v, v) & 0xFFFF);
-    if constexpr (OUT == kNormBf16) static_cast<uint16_t*>(a.y)[base + k] = (uint16_t)(pack_bf16x2(y, y) & 0xFFFF);
-    else static_cast<uint8_t*>(a.y)[base + k] = (uint8_t)code1(rcp ? dv(y) : y / s, a.fp8);
+    if constexpr (OUT == kNormBf16) static_cast<uint16_t*>(a.y)[base + k] = (uint16_t)(pack_bf16x2(hw * r, hw * r) & 0xFFFF);
+    else static_cast<uint8_t*>(a.y)[base + k] = (uint8_t)code.one(hw);
   }
 }
 

@@ -9,8 +9,8 @@
 // e4m3 with one per (token, head).  A rotated K is quantized from its fp32 value: one rounding
 // fewer than rotating to bf16 first.
 //
-// One workgroup per token (or per token and a share of its heads, while tokens are few): its
-// first threads compute the R/2 angles once for all heads into LDS.  A head row is D/8 lanes
+// One workgroup per TW tokens (or per token and a share of its heads, while tokens are few): its
+// threads compute the tokens' R/2 angles once for all heads into LDS.  A head row is D/8 lanes
 // of one wave, 8 channels each; the row passes through the wave's LDS so that a lane finds its
 // pair partners, and every load of a row comes before its stores, so q may be rotated in
 // place.  Bound by HBM for many tokens, by latency for few.
@@ -56,50 +56,69 @@ __device__ __forceinline__ void unpack8(u32x4 v, float* f) {
   }
 }
 
-// Angles of token t's position: cs[i] = (factor cos, factor sin), i < R / 2.
-__device__ __forceinline__ void token_angles(const RopeArgs& a, int64_t t, float2* cs) {
-  const int64_t pos = load_index(a.positions, a.pos64, t);
-  for (int i = threadIdx.x; i < a.R / 2; i += kRopeWaves * 64) {
+// Angles of the positions of tokens t0 .. t0 + n - 1: cs[k R/2 + i] = (factor cos, factor sin).
+__device__ __forceinline__ void token_angles(const RopeArgs& a, int64_t t0, int n, float2* cs) {
+  const int half = a.R / 2;
+  for (int j = threadIdx.x; j < n * half; j += kRopeWaves * 64) {
+    const int k = j / half, i = j - k * half;
+    const int64_t pos = load_index(a.positions, a.pos64, t0 + k);
     const double th = (double)pos * a.inv_freq[i];
-    const double n = rint(th * 0x1.45f306dc9c883p-3);                    // 1 / (2 pi)
-    double r = __builtin_fma(-n, 0x1.921fb54442d18p+2, th);             // 2 pi, high part
-    r = __builtin_fma(-n, 0x1.1a62633145c07p-52, r);                    // and the rest of it
+    const double q = rint(th * 0x1.45f306dc9c883p-3);                    // 1 / (2 pi)
+    double r = __builtin_fma(-q, 0x1.921fb54442d18p+2, th);             // 2 pi, high part
+    r = __builtin_fma(-q, 0x1.1a62633145c07p-52, r);                    // and the rest of it
     float s, c;
     sincosf((float)r, &s, &c);
-    cs[i] = make_float2(a.factor * c, a.factor * s);
+    cs[j] = make_float2(a.factor * c, a.factor * s);
   }
 }
 
 __global__ __launch_bounds__(kRopeWaves * 64) void rope_kv_kernel(RopeArgs a) {
-  extern __shared__ float2 cs[];                             // [R / 2]
+  extern __shared__ __align__(16) float2 cs_all[];           // [TW][R / 2]
   __shared__ __align__(16) uint16_t rows[kRopeWaves][512];   // 64 lanes x 8 channels per wave
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = blockIdx.x;
+  const int64_t t0 = (int64_t)blockIdx.x * a.TW;
+  const int ntok = (int)min((int64_t)a.TW, a.T - t0);
   const int tpr = a.D / 8, rpw = 64 / tpr;                    // lanes per row, rows per wave
   const int r = lane / tpr, c = lane % tpr;
-  const int total = a.Hq + a.Hk + a.Hv;                       // rows of the token: q, then k, then v
+  const int total = a.Hq + a.Hk + a.Hv, all = ntok * total;   // rows of a token: q, then k, then v
   const int step = gridDim.y * kRopeWaves * rpw;
   const int first = (blockIdx.y * kRopeWaves + wave) * rpw;
-  auto load = [&](int row) -> u32x4 {
-    if (row < a.Hq) return load8(a.q + t * a.q_stride + (int64_t)row * a.D + c * 8, a.vec_in);
-    if (row < a.Hq + a.Hk) return load8(a.k + t * a.k_stride + (int64_t)(row - a.Hq) * a.D + c * 8, a.vec_in);
-    return load8(a.v + t * a.v_stride + (int64_t)(row - a.Hq - a.Hk) * a.D + c * 8, a.vec_in);
-  };
   const bool lane_live = r < rpw;
-  u32x4 raw = {0u, 0u, 0u, 0u};
-  if (lane_live && first + r < total) raw = load(first + r);
-  int64_t slot = -1;
-  if (a.Hk) slot = load_index(a.slots, a.slot64, t);
-  const bool stored = slot >= 0 && slot < a.pool;
-  if (a.R) token_angles(a, t, cs);
-  __syncthreads();
-  for (int base = first; base < total; base += step) {        // uniform per wave
-    const int row = base + r;
-    const bool live = lane_live && row < total;
-    if (base != first) {
-      raw = (u32x4){0u, 0u, 0u, 0u};
-      if (live) raw = load(row);
+  // The row `at` of this lane: its token, its place in the token, its data and its cache slot.
+  struct Row {
+    u32x4 raw;
+    int64_t slot;
+    int tok, row;
+    bool live;
+  };
+  auto load = [&](int at) -> Row {
+    Row w;
+    w.live = lane_live && at < all;
+    w.tok = w.live ? at / total : 0;
+    w.row = w.live ? at - w.tok * total : 0;
+    w.raw = (u32x4){0u, 0u, 0u, 0u};
+    w.slot = -1;
+    const int64_t t = t0 + w.tok;
+    if (w.live) {
+      if (w.row < a.Hq) w.raw = load8(a.q + t * a.q_stride + (int64_t)w.row * a.D + c * 8, a.vec_in);
+      else if (w.row < a.Hq + a.Hk) w.raw = load8(a.k + t * a.k_stride + (int64_t)(w.row - a.Hq) * a.D + c * 8, a.vec_in);
+      else w.raw = load8(a.v + t * a.v_stride + (int64_t)(w.row - a.Hq - a.Hk) * a.D + c * 8, a.vec_in);
+      if (a.Hk) w.slot = load_index(a.slots, a.slot64, t);
     }
+    return w;
+  };
+  Row next = load(first + r);
+  if (a.R) token_angles(a, t0, ntok, cs_all);
+  __syncthreads();
+  for (int base = first; base < all; base += step) {          // uniform per wave
+    const Row cur = next;
+    next = load(base + step + r);                             // the next batch's rows are in flight meanwhile
+    const u32x4 raw = cur.raw;
+    const int row = cur.row;
+    const bool live = cur.live;
+    const int64_t t = t0 + cur.tok, slot = cur.slot;
+    const bool stored = slot >= 0 && slot < a.pool;
+    const float2* cs = cs_all + cur.tok * (a.R / 2);
     float f[8];
     unpack8(raw, f);
     // the wave's rows through its own LDS: written and read by this wave alone, in order
@@ -111,7 +130,29 @@ __global__ __launch_bounds__(kRopeWaves * 64) void rope_kv_kernel(RopeArgs a) {
     const bool turns = live && row < a.Hq + a.Hk && c * 8 < a.R;
     if (turns) {
       const int half = a.R / 2;
-      if (a.interleaved) {
+      if (a.R % 16 == 0) {                                    // (also keeps the 16-byte reads aligned)
+        // the chunk is whole: one run of cosines and sines, read as vectors
+        const int i0 = a.interleaved ? c * 4 : c * 8 < half ? c * 8 : c * 8 - half;
+        f32x4 w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!a.interleaved || e < 2) w[e] = *reinterpret_cast<const f32x4*>(&cs[i0 + 2 * e]);
+        if (a.interleaved) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float co = w[e / 2][2 * (e & 1)], si = w[e / 2][2 * (e & 1) + 1];
+            const float x = f[2 * e], y = f[2 * e + 1];
+            f[2 * e] = x * co - y * si;
+            f[2 * e + 1] = x * si + y * co;
+          }
+        } else {
+          float o[8];
+          unpack8(ld16(mine + (c * 8 < half ? c * 8 + half : c * 8 - half)), o);
+          const float sign = c * 8 < half ? -1.0f : 1.0f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = f[e] * w[e / 2][2 * (e & 1)] + sign * o[e] * w[e / 2][2 * (e & 1) + 1];
+        }
+      } else if (a.interleaved) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = c * 4 + e;                            // pair (2 i, 2 i + 1)
@@ -123,23 +164,13 @@ __global__ __launch_bounds__(kRopeWaves * 64) void rope_kv_kernel(RopeArgs a) {
           }
         }
       } else {
-        float o[8];
-        const int p0 = c * 8 < half ? c * 8 + half : c * 8 - half;   // partner of channel 8 c
-        if (half % 8 == 0) {
-          unpack8(ld16(mine + p0), o);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int ch = c * 8 + e;
-            o[e] = ch < a.R ? bf16_bits_to_f32(mine[ch < half ? ch + half : ch - half]) : 0.0f;
-          }
-        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int ch = c * 8 + e;
           if (ch < a.R) {
             const float2 w = cs[ch < half ? ch : ch - half];
-            f[e] = ch < half ? f[e] * w.x - o[e] * w.y : o[e] * w.y + f[e] * w.x;
+            const float o = bf16_bits_to_f32(mine[ch < half ? ch + half : ch - half]);
+            f[e] = ch < half ? f[e] * w.x - o * w.y : o * w.y + f[e] * w.x;
           }
         }
       }
@@ -159,7 +190,7 @@ __global__ __launch_bounds__(kRopeWaves * 64) void rope_kv_kernel(RopeArgs a) {
         }
       }
     }
-    if (base + rpw > a.Hq && a.Hk) {                          // wave-uniform: some K or V rows
+    if (a.Hk && __ballot(live && row >= a.Hq)) {              // wave-uniform: some K or V rows
       float am = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(f[e]));
@@ -176,10 +207,10 @@ __global__ __launch_bounds__(kRopeWaves * 64) void rope_kv_kernel(RopeArgs a) {
         const int h = is_k ? row - a.Hq : row - a.Hq - a.Hk;
         const int64_t at = slot * a.Hk + h;
         const uint32_t sb = is_k ? kv_f16_scale(am, 127.0f) : kv_f16_scale(rm, 448.0f);
-        const float s = f16_value(sb);
+        const RcpDiv dv(f16_value(sb));                       // (the codec's codes wherever the input is bf16)
         float d[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] = f[e] / s;
+        for (int e = 0; e < 8; ++e) d[e] = dv(f[e]);
         if (is_k) {
           const u32x2 w = {f32_to_i8_sat(d[0]) | (f32_to_i8_sat(d[1]) << 8) | (f32_to_i8_sat(d[2]) << 16) |
                                (f32_to_i8_sat(d[3]) << 24),
@@ -227,13 +258,17 @@ __global__ __launch_bounds__(256) void kv_gather_kernel(const uint8_t* __restric
 }  // namespace
 
 hipError_t launch_rope_kv(const RopeArgs& a, hipStream_t st) {
-  // A workgroup takes 4 waves x (64 / (D / 8)) head rows at a time.  Few tokens: one such
-  // batch per workgroup (more, shorter workgroups); many: a workgroup per token, so that the
-  // angles are computed once.
+  // A workgroup takes 4 waves x (64 / (D / 8)) head rows at a time.  Few tokens: one such batch
+  // per workgroup (more, shorter workgroups); from 2048 on two tokens per workgroup share the
+  // wait for positions and angles (2048 tokens, 32 + 2 x 8 heads of 128: 15.6 -> 13.8 us, 8191:
+  // 46.1 -> 41.3 us; four tokens: 17.3 and 41.3 us; split by batches: 18.8 and 63 us).
+  RopeArgs b = a;
   const int rpw = 64 / (a.D / 8), rows = a.Hq + a.Hk + a.Hv;
   const int batches = (rows + kRopeWaves * rpw - 1) / (kRopeWaves * rpw);
+  b.TW = a.T >= 2048 ? 2 : 1;
   const int gy = a.T < 1024 ? batches : 1;
-  rope_kv_kernel<<<dim3((unsigned)a.T, (unsigned)gy), kRopeWaves * 64, (size_t)(a.R / 2) * sizeof(float2), st>>>(a);
+  rope_kv_kernel<<<dim3((unsigned)((a.T + b.TW - 1) / b.TW), (unsigned)gy), kRopeWaves * 64,
+                   (size_t)b.TW * (a.R / 2) * sizeof(float2), st>>>(b);
   return hipGetLastError();
 }
 
