@@ -46,6 +46,29 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t w) {
 // Memory that no kernel writes meanwhile, read through the scalar cache.
 typedef __attribute__((address_space(4))) const int32_t ConstInt;
 
+// One token's K scales, NG fp16 as raw dwords (aligned to their size's largest power of two).
+template <int NG>
+struct KScales {
+  static constexpr int N = (NG + 1) / 2;
+  uint32_t d[N];
+  __device__ __forceinline__ void load(const uint16_t* p) {
+    if constexpr (NG == 8) {
+      const u32x4 v = ld16(p);
+      d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
+    } else if constexpr (NG == 4) {
+      const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+      d[0] = v.x, d[1] = v.y;
+    } else if constexpr (NG % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) d[i] = *reinterpret_cast<const uint32_t*>(p + 2 * i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) d[i] = p[2 * i] | (2 * i + 1 < NG ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+    }
+  }
+  __device__ __forceinline__ float get(int i) const { return i & 1 ? f16_hi(d[i / 2]) : f16_lo(d[i / 2]); }
+};
+
 // Sequence b: its query tokens and its cached tokens.
 struct Extent {
   int qs, nq, L;
@@ -80,6 +103,13 @@ __device__ __forceinline__ int row16(int v, OP op) {          // over 16 lanes, 
 }
 
 template <class OP>
+__device__ __forceinline__ int row8(int v, OP op) {           // over 8 lanes, where both halves of 16 hold the same
+  v = op(v, row_ror<4>(v));
+  v = op(v, row_ror<2>(v));
+  return op(v, row_ror<1>(v));
+}
+
+template <class OP>
 __device__ __forceinline__ int across16(int v, OP op) {       // over lanes l, l ^ 16, l ^ 32, l ^ 48
   const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
   v = op((int)a[0], (int)a[1]);
@@ -98,6 +128,12 @@ struct AddF {
 struct MaxF {
   __device__ __forceinline__ int operator()(int a, int b) const {
     return __builtin_bit_cast(int, fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
+  }
+};
+struct MaxU16 {                                               // both halves on their own
+  __device__ __forceinline__ int operator()(int a, int b) const {
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(int, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
   }
 };
 

@@ -100,29 +100,6 @@ __device__ __forceinline__ void pv_piece(const Raw<2 * P, NT> (&v)[8], const f16
   }
 }
 
-// One token's K scales, NG fp16 as raw dwords (aligned to their size's largest power of two).
-template <int NG>
-struct KScales {
-  static constexpr int N = (NG + 1) / 2;
-  uint32_t d[N];
-  __device__ __forceinline__ void load(const uint16_t* p) {
-    if constexpr (NG == 8) {
-      const u32x4 v = ld16(p);
-      d[0] = v.x, d[1] = v.y, d[2] = v.z, d[3] = v.w;
-    } else if constexpr (NG == 4) {
-      const u32x2 v = *reinterpret_cast<const u32x2*>(p);
-      d[0] = v.x, d[1] = v.y;
-    } else if constexpr (NG % 2 == 0) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) d[i] = *reinterpret_cast<const uint32_t*>(p + 2 * i);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i) d[i] = p[2 * i] | (2 * i + 1 < NG ? (uint32_t)p[2 * i + 1] << 16 : 0u);
-    }
-  }
-  __device__ __forceinline__ float get(int i) const { return i & 1 ? f16_hi(d[i / 2]) : f16_lo(d[i / 2]); }
-};
-
 // The first token that any query of the sequence can see (rounded down to a tile of 32), and
 // the tiles of 32 from there.
 __device__ __forceinline__ int begin_of(const KvAttnArgs& a, const Extent& e) {
@@ -529,14 +506,13 @@ hipError_t launch_ng(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t st) {
 
 }  // namespace
 
-#ifndef QR2
-#define QR2 32
-#endif
 KvAttnPlan plan_kv_attention(int64_t T, int64_t B, int64_t Hk, int64_t G, bool one_each) {
   KvAttnPlan p;
   const int64_t rows = one_each ? G : (T + B - 1) / B * G;   // query rows of an average sequence
-  if (rows > QR2) {
-    // Many rows: kv_attention_tile.hip, one workgroup of eight waves per CU.
+  // More than 32 rows: kv_attention_tile.hip, one workgroup of eight waves per CU.  (17 to 32 rows
+  // there and here, 16 sequences of 6 x 4 rows, heads of 128 over 8 KV heads: 93 and 69 us at 4000
+  // tokens each, 262 and 159 us at 16000.)
+  if (rows > 32) {
     p.R = 16;
     p.parts = (int)(Hk >= 256 ? 1 : 256 / Hk);
     p.grid = p.parts * Hk;

@@ -44,6 +44,12 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, f16x2 s) {
   return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, a) * s);
 }
 
+// Weights are 2^(x - m) of base-2 scores x, with m (the row's reference) kLift below the largest
+// score when it is set and kept until a score passes it by kSlack: they stay below 2^15, fp16's 11
+// bits reach down to 2^-21 of the largest, and o is hardly ever rescaled (following every new
+// maximum of 32 rows takes 64 products per tile nearly every time).
+constexpr float kLift = 7.0f, kSlack = 15.0f;
+
 // A query tile's tokens: those that its rows can see.
 struct Span {
   int i0, i1;                    // first and last query token
@@ -68,15 +74,32 @@ __device__ __forceinline__ int tiles_of(const KvAttnArgs& a, const Extent& e) {
   return (e.nq * a.G + kTileRows - 1) / kTileRows;
 }
 
-// Units (T tokens of one query tile) of sequence `b`, whole.
-template <int T>
-__device__ __forceinline__ int sequence_units(const KvAttnArgs& a, int b) {
-  if (b >= a.B) return 0;
-  const Extent e = extent_of(a, b);
-  int n = 0;
-  for (int qt = 0, k = tiles_of(a, e); qt < k; ++qt) n += units_of<T>(span_of<T>(a, e, qt));
-  return n;
+// Calls visit(b, qt, units) for every query tile, 64 at a time in order (a tile per lane, units 0
+// where there is none), until it returns false.
+template <int T, class Visit>
+__device__ __forceinline__ void walk_tiles(const KvAttnArgs& a, int lane, Visit visit) {
+  for (int b0 = 0; b0 < a.B; b0 += 64) {
+    const int ends = wave_scan(b0 + lane < a.B ? tiles_of(a, extent_of(a, b0 + lane)) : 0);
+    const int tiles = __builtin_amdgcn_readlane(ends, 63);
+    int i = 0, start = 0;                                    // the sequence (b0 + i) that tile f0 belongs to, its first tile
+    for (int f0 = 0; f0 < tiles; f0 += 64) {
+      int mine = i, qt = f0 + lane - start;
+      while (i < 63) {                                       // sequences that begin among these tiles
+        const int next = __builtin_amdgcn_readlane(ends, i);
+        if (next >= min(f0 + 64, tiles)) break;
+        ++i;
+        start = next;
+        if (f0 + lane >= start) mine = i, qt = f0 + lane - start;
+      }
+      const bool valid = f0 + lane < tiles;
+      const int b = valid ? b0 + mine : 0;
+      const Extent e = extent_of(a, b);
+      if (!visit(b, qt, valid ? units_of<T>(span_of<T>(a, e, qt)) : 0)) return;
+    }
+  }
 }
+
+constexpr int kAhead = 4;        // operands in flight from LDS before a product (2, 6 and 8 the same within 2 %)
 
 template <int NG>
 struct TileShape {
@@ -96,17 +119,42 @@ struct TileLds {
     JoinLds join[kTileWaves];
   };
   // by tile % 4 (written two tiles ahead):
-  float vs[4][S::T];                             // V scales, 2^-E each, 0 for a token that is not there
-  float kmul[4], kback[4];                       // on K's scales, and what undoes it on the scores
-  int e[4], gap[4];                              // E; whether a token is not there
+  float vs[4][S::T];                             // V scales, 0 for a token that is not there
+  uint32_t top[4][kTileWaves];                   // per wave's tokens: largest K scale (fp16 bits; bit 15: one is not there) and V scale
 };
 
-// Where piece p (8 tokens) of channel d lies in its row: reads (16 channels, one piece) and
-// writes (4 channels apart) then spread over the banks.
+// Where piece p (8 tokens) of channel d lies in its row: p ^ swizzle(d), so that reads (16
+// channels, one piece) spread over all banks and writes (4 channels apart) over half of them.
+// It depends on d % 32 alone, so the reads of all 32-channel blocks share their addresses.
 template <int T>
-__device__ __forceinline__ int piece(int d, int p) {
-  if constexpr (T == 64) return p ^ (((d >> 1) ^ (d >> 4)) & 7);
-  return p ^ (((d >> 2) ^ (d >> 4)) & 3);
+__device__ __forceinline__ int swizzle(int d) {
+  if constexpr (T == 64) return ((d >> 1) & 7) ^ ((d >> 4) & 1);
+  return ((d >> 2) & 3) ^ ((d >> 4) & 1);
+}
+
+// What a tile's values are scaled by, uniform for the workgroup.
+struct TileScale {
+  int e;                         // V' = V 2^-e
+  bool big;                      // K' = K 2^-7
+  bool gap;                      // a token is not there
+};
+constexpr int kNoScale = -1000;
+
+// N products that take one operand from LDS each, in exactly this order: AHEAD reads in front,
+// then a product and the read of a later one in turn (left alone, the compiler reads each operand
+// right before its product and waits for it).
+template <int N, int AHEAD, class Read, class Product>
+__device__ __forceinline__ void products(Read read, Product product) {
+  f16x8 f[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) f[i] = read(i);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    product(i, f[i % AHEAD]);
+    if (i + AHEAD < N) f[i % AHEAD] = read(i + AHEAD);
+    __builtin_amdgcn_sched_barrier(0);
+  }
 }
 
 template <int NG>
@@ -122,34 +170,33 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
   const uint32_t row_bytes = (uint32_t)hk * D;
 
   int total = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 64) total += wave_sum(sequence_units<T>(a, b0 + lane));
+  walk_tiles<T>(a, lane, [&](int, int, int n) {
+    total += wave_sum(n);
+    return true;
+  });
   total = __builtin_amdgcn_readfirstlane(total);
   const int U = max(1, (total + a.parts - 1) / a.parts), u_end = min(total, (part + 1) * U);
 
   for (int u = part * U; u < u_end;) {                       // uniform for the workgroup
-    // the sequence and the tile that unit u belongs to
-    int b = 0, at = 0;
-    for (int b0 = 0, before = 0; b0 < a.B; b0 += 64) {
-      const int n = sequence_units<T>(a, b0 + lane), inc = before + wave_scan(n);
+    // the sequence and the tile that unit u belongs to, and the tile's first unit
+    int b = 0, qt = 0, at = 0, before = 0;
+    walk_tiles<T>(a, lane, [&](int tb, int tq, int n) {
+      const int inc = before + wave_scan(n);
       const uint64_t hit = __ballot(u < inc && u >= inc - n);
       if (hit) {
         const int src = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
-        b = b0 + src;
+        b = __builtin_amdgcn_readlane(tb, src);
+        qt = __builtin_amdgcn_readlane(tq, src);
         at = __builtin_amdgcn_readlane(inc - n, src);
-        break;
       }
       before = __builtin_amdgcn_readlane(inc, 63);
-    }
+      return hit == 0;
+    });
     Extent e = extent_of(a, b);
     e.qs = __builtin_amdgcn_readfirstlane(e.qs);
     e.nq = __builtin_amdgcn_readfirstlane(e.nq);
     e.L = __builtin_amdgcn_readfirstlane(e.L);
-    int qt = 0;
-    Span sp = span_of<T>(a, e, 0);
-    while (u >= at + units_of<T>(sp)) {
-      at += units_of<T>(sp);
-      sp = span_of<T>(a, e, ++qt);
-    }
+    const Span sp = span_of<T>(a, e, qt);
     const int units = units_of<T>(sp), u_next = min(u_end, at + units);
     const Chunks ck{at / U, (at + units - 1) / U - at / U + 1, part - at / U};
     const int c0 = sp.begin + T * (u - at), c1 = min(sp.end, sp.begin + T * (u_next - at));
@@ -213,6 +260,7 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
     const int first_t = TPW * wave;                          // this wave's first token of a tile
     u32x4 kraw;
     uint32_t vraw[4], ksraw;
+    TileScale next{kNoScale, false, false};
     auto load = [&](int entry) {
       const int64_t at64 = (int64_t)max(entry, 0) * hk + h;
       kraw = ld16(a.k_codes + at64 * D + koff);
@@ -221,11 +269,19 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
 #pragma unroll
       for (int i = 0; i < 4; ++i) vraw[i] = *reinterpret_cast<const uint32_t*>(vp + (size_t)i * row_bytes);
     };
-    auto convert = [&](int n) {                              // the loaded tile, number n, into LDS buffer n % 2
+    // The loaded tile, number n, into LDS buffer n % 2.
+    auto convert = [&](int n) {
       const int buf = n & 1;
-      const float s = f16_lo(ksraw) * sm.kmul[n & 3];
+      uint32_t top = sm.top[n & 3][lane & (kTileWaves - 1)];
+      next.gap = __ballot((top & 0x8000u) != 0) != 0;
+      top = row8(top & 0x7FFF7FFFu, MaxU16());
+      top = __builtin_amdgcn_readfirstlane(top);
+      next.big = (top & 0xFFFF) > 0x6000;
+      const uint32_t vt = top >> 16;
+      if (vt) next.e = max(next.e, (vt >= 0x400 ? (int)(vt >> 10) - 14 : 8 - __builtin_clz(vt)) - 6);
+      const float s = next.big ? f16_lo(ksraw) * 0x1p-7f : f16_lo(ksraw);
       const f16x2 s2 = {(_Float16)s, (_Float16)s};
-      const f32x4 vsc = *reinterpret_cast<const f32x4*>(&sm.vs[n & 3][first_t + 4 * vgrp]);
+      f32x4 vsc = *reinterpret_cast<const f32x4*>(&sm.vs[n & 3][first_t + 4 * vgrp]);
       if (lane < NL) {
         const uint32_t kd[4] = {kraw.x, kraw.y, kraw.z, kraw.w};
         u32x4 w[2];
@@ -242,6 +298,8 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
         uint32_t r[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) r[i] = vsc[i] > 0.0f ? vraw[i] : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vsc[i] = __builtin_ldexpf(vsc[i], -next.e);
         const f16x2 v01 = {(_Float16)vsc[0], (_Float16)vsc[1]}, v23 = {(_Float16)vsc[2], (_Float16)vsc[3]};
         const uint32_t a01 = __builtin_amdgcn_perm(r[1], r[0], 0x05010400u), b01 = __builtin_amdgcn_perm(r[1], r[0], 0x07030602u);
         const uint32_t a23 = __builtin_amdgcn_perm(r[3], r[2], 0x05010400u), b23 = __builtin_amdgcn_perm(r[3], r[2], 0x07030602u);
@@ -256,41 +314,34 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
           const uint32_t hi = i & 1 ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(s23, 1.0f, true))
                                     : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(s23, 1.0f, false));
           const int d = 4 * vcb + i;
-          *reinterpret_cast<u32x2*>(&sm.v[buf][d][8 * piece<T>(d, p) + 4 * hf]) = (u32x2){mul2(lo, v01), mul2(hi, v23)};
+          *reinterpret_cast<u32x2*>(&sm.v[buf][d][8 * (p ^ swizzle<T>(d)) + 4 * hf]) = (u32x2){mul2(lo, v01), mul2(hi, v23)};
         }
       }
     };
-    // The scales of a whole tile, two tiles ahead (wave 0, a token per lane): E and K's multiplier.
-    int run_e = -1000;
-    float svr = 0.0f, kmax = 0.0f;
-    int spage = 0;
-    auto stat_page = [&](int t0) { return a.block_table[(int64_t)b * a.max_pages + (min(t0 + (lane & (T - 1)), a.max_tokens - 1) >> a.page_shift)]; };
-    auto stat_load = [&](int t0, int page) {
-      const int t = t0 + (lane & (T - 1)), en = entry_of(page, t);
-      const bool there = en >= 0 && t < c1;
-      const int64_t at64 = (int64_t)max(en, 0) * hk + h;
-      svr = f16_lo(a.v_scales[at64]);
-      kmax = 0.0f;
-#pragma unroll
-      for (int n = 0; n < NG; ++n) kmax = fmaxf(kmax, f16_lo(a.k_scales[at64 * NG + n]));
-      svr = there ? fmaxf(svr, 0x1p-24f) : 0.0f;
-      kmax = there ? kmax : 0.0f;
+    // The scales, two tiles ahead: lane l has token l % TPW of this wave's, K's block l / TPW.
+    const int srow = lane & (TPW - 1), sblock = lane / TPW % NG;
+    uint32_t svr, skr;
+    int st_t, st_page;
+    auto stat_load = [&](int t0, int page) {                 // t0: the wave's first token
+      st_t = t0;
+      st_page = page;
+      const int64_t at64 = (int64_t)max(entry_of(page, t0), 0) * hk + (int64_t)srow * hk + h;
+      svr = a.v_scales[at64];
+      skr = a.k_scales[at64 * NG + sblock];
     };
     auto stat_write = [&](int n) {
-      const float vm = max_across16(max_row16(svr)), km = max_across16(max_row16(kmax));
-      if (vm > 0.0f) run_e = max(run_e, __builtin_amdgcn_frexp_expf(vm) - 6);
-      const int gap = __ballot(svr == 0.0f) != 0;
-      if (lane < T) sm.vs[n & 3][lane] = __builtin_ldexpf(svr, -run_e);
-      if (lane == 0) {
-        sm.kmul[n & 3] = km > 512.0f ? 0x1p-7f : 1.0f;
-        sm.kback[n & 3] = km > 512.0f ? 0x1p7f : 1.0f;
-        sm.e[n & 3] = run_e;
-        sm.gap[n & 3] = gap;
-      }
+      const bool there = entry_of(st_page, st_t) >= 0 && st_t + srow < c1;
+      const uint32_t kb = there ? skr & 0x7FFF : 0u, vb = there ? max(svr & 0x7FFF, 1u) : 0u;
+      uint32_t top = across16(row16(kb | vb << 16, MaxU16()), MaxU16());
+      if (__ballot(!there)) top |= 0x8000u;
+      if (lane < TPW) sm.vs[n & 3][first_t + lane] = f16_lo(vb);
+      if (lane == 0) sm.top[n & 3][wave] = top;
     };
 
+    const int vswz = half ^ swizzle<T>(c32);                 // this lane's pieces: (4 k + 2 t) ^ vswz
     f32x16 o[NG];
     float m = kNegInf, l = 0.0f;
+    int cur_e = kNoScale;                                    // E that o was computed with
 #pragma unroll
     for (int n = 0; n < NG; ++n)
 #pragma unroll
@@ -298,73 +349,84 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
 
     __syncthreads();                                         // (LDS of the tile before is no longer read)
     const int wt = c0 + first_t;
-    int page = page_of(wt + T);
+    int page = page_of(wt + T), page2 = page_of(wt + 2 * T);
     load(entry_of(page_of(wt), wt));
-    if (wave == 0) {
-      stat_load(c0, stat_page(c0));
-      stat_write(0);
-      stat_load(c0 + T, stat_page(c0 + T));
-      stat_write(1);
-      stat_load(c0 + 2 * T, stat_page(c0 + 2 * T));
-      spage = stat_page(c0 + 3 * T);
-    }
+    stat_load(wt, page_of(wt));
+    stat_write(0);
+    stat_load(wt + T, page);
+    stat_write(1);
     __syncthreads();
     convert(0);
+    TileScale now = next;
     load(entry_of(page, wt + T));
-    page = page_of(wt + 2 * T);
+    stat_load(wt + 2 * T, page2);
+    page = page2;
+    page2 = page_of(wt + 3 * T);
     __syncthreads();
-    int cur_e = sm.e[0];
+    auto prepare = [&](int n) {                              // tile n's share of what tiles n + 1 .. n + 3 need
+      if (c0 + (n + 1) * T < c1) {
+        convert(n + 1);
+        load(entry_of(page, wt + (n + 2) * T));
+        stat_write(n + 2);
+        stat_load(wt + (n + 3) * T, page2);
+        page = page2;
+        page2 = page_of(wt + (n + 4) * T);
+      }
+    };
     for (int base = c0, n = 0; base < c1; base += T, ++n) {
       const int buf = n & 1;
       const bool skip = live_rows <= 0 || (a.causal && base > last_p) || (a.window > 0 && base + T - 1 <= first_p - a.window);
+      prepare(n);
       f32x16 s[NB];
       if (!skip) {
 #pragma unroll
-        for (int k = 0; k < NB; ++k) {
+        for (int k = 0; k < NB; ++k)
 #pragma unroll
           for (int i = 0; i < 16; ++i) s[k][i] = 0.0f;
-#pragma unroll
-          for (int c = 0; c < 2 * NG; ++c) {
-            const f16x8 kf = *reinterpret_cast<const f16x8*>(&sm.k[buf][32 * k + c32][16 * c + 8 * half]);
-            s[k] = mfma_f16_k16(kf, qf[c], s[k]);
-          }
-        }
-      }
-      if (base + T < c1) {                                   // the next tile: into the other buffer, and the one after that
-        convert(n + 1);
-        load(entry_of(page, wt + (n + 2) * T));
-        page = page_of(wt + (n + 3) * T);
-      }
-      if (wave == 0) {
-        stat_write(n + 2);
-        stat_load(base + 3 * T, spage);
-        spage = stat_page(base + 4 * T);
+        const _Float16* kp = &sm.k[buf][c32][8 * half];
+        products<2 * NG * NB, kAhead>(
+            [&](int i) { return *reinterpret_cast<const f16x8*>(kp + 32 * S::KLD * (i % NB) + 16 * (i / NB)); },
+            [&](int i, f16x8 kf) { s[i % NB] = mfma_f16_k16(kf, qf[i / NB], s[i % NB]); });
       }
       if (!skip) {
-        const bool open = !__builtin_amdgcn_readfirstlane(sm.gap[n & 3]) && (!a.causal || base + T - 1 <= first_p) &&
+        const bool open = !now.gap && (!a.causal || base + T - 1 <= first_p) &&
                           (a.window <= 0 || base > last_p - a.window);
-        const float cst = cs * sm.kback[n & 3];
-        float mx = kNegInf;
+        const float cst = now.big ? cs * 0x1p7f : cs;
+        const int t4 = base + 4 * half;
         if (!open) {
+          if (now.gap) {
 #pragma unroll
-          for (int k = 0; k < NB; ++k)
+            for (int k = 0; k < NB; ++k)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int tt = 32 * k + 8 * (i / 4) + 4 * half + (i & 3), t = base + tt;
-              const bool see = sm.vs[n & 3][tt] > 0.0f && (!a.causal || t <= qpos) && (a.window <= 0 || t > qpos - a.window);
-              s[k][i] = see ? s[k][i] : kNegInf;
-            }
+              for (int i = 0; i < 16; ++i)
+                s[k][i] = sm.vs[n & 3][32 * k + 8 * (i / 4) + 4 * half + (i & 3)] > 0.0f ? s[k][i] : kNegInf;
+          }
+          const int64_t from = (int64_t)qpos - t4;             // (may be far below and above the tile)
+        int hi = (int)max(min(from, (int64_t)T), (int64_t)-1), lo = (int)max(min(from - a.window, (int64_t)T), (int64_t)-1);
+        asm volatile("" : "+v"(hi), "+v"(lo));               // (compared as 32 bits)
+          if (a.causal) {
+#pragma unroll
+            for (int k = 0; k < NB; ++k)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) s[k][i] = 32 * k + 8 * (i / 4) + (i & 3) <= hi ? s[k][i] : kNegInf;
+          }
+          if (a.window > 0) {
+#pragma unroll
+            for (int k = 0; k < NB; ++k)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) s[k][i] = 32 * k + 8 * (i / 4) + (i & 3) > lo ? s[k][i] : kNegInf;
+          }
         }
+        float mx = kNegInf;
 #pragma unroll
         for (int k = 0; k < NB; ++k)
 #pragma unroll
           for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[k][i]);
         mx = across32(mx, false) * cst;
-        const float mn = fmaxf(m, mx);
-        const int e_new = sm.e[n & 3];
-        const float ref = mn == kNegInf ? 0.0f : mn;
-        if (__ballot(mn > m) || e_new != cur_e) {
-          const float corr = __builtin_amdgcn_exp2f(m - ref);
+        const int e_new = now.e;
+        if (__ballot(mx > m + kSlack) || e_new != cur_e) {   // (m == -inf: mx > m)
+          const float mn = fmaxf(m, mx - kLift);
+          const float corr = mn == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(m - mn);
           const float oc = __builtin_ldexpf(corr, cur_e - e_new);
           l *= corr;
 #pragma unroll
@@ -374,25 +436,28 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
           m = mn;
           cur_e = e_new;
         }
+        const float ref = m == kNegInf ? 0.0f : m;
         f16x8 w[NB][2];
 #pragma unroll
         for (int k = 0; k < NB; ++k)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float x = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k][i], cst, -ref));
-            l += x;
-            w[k][i / 8][i & 7] = (_Float16)x;
+          for (int i = 0; i < 16; i += 2) {
+            const float x0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k][i], cst, -ref));
+            const float x1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[k][i + 1], cst, -ref));
+            const f16x2 x = {(_Float16)x0, (_Float16)x1};
+            l = __builtin_amdgcn_fdot2(x, (f16x2){(_Float16)1, (_Float16)1}, l, false);
+            w[k][i / 8][i & 7] = x[0];
+            w[k][i / 8][(i & 7) + 1] = x[1];
           }
-#pragma unroll
-        for (int d = 0; d < NG; ++d)
-#pragma unroll
-          for (int k = 0; k < NB; ++k)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              const f16x8 vf = *reinterpret_cast<const f16x8*>(&sm.v[buf][32 * d + c32][8 * piece<T>(32 * d + c32, 4 * k + 2 * t + half)]);
-              o[d] = mfma_f16_k16(vf, w[k][t], o[d]);
-            }
+        const _Float16* vrow = &sm.v[buf][c32][0];
+        products<2 * NG * NB, kAhead>(
+            [&](int i) {
+              const int kt = i / NG, d = i % NG;              // 16 tokens, 32 channels
+              return *reinterpret_cast<const f16x8*>(vrow + 32 * T * d + 8 * ((2 * kt) ^ vswz));
+            },
+            [&](int i, f16x8 vf) { o[i % NG] = mfma_f16_k16(vf, w[i / NG / 2][i / NG % 2], o[i % NG]); });
       }
+      now = next;
       __syncthreads();
     }
 
