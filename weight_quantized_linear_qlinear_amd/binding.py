@@ -492,15 +492,19 @@ def kv_cache(slots: int, heads: int, head_dim: int, device: torch.device | str |
 
 # ---------------------------------------------------------------------- between the linears
 # These calls take a few microseconds on the GPU, so what the host does before them counts: the raw
-# handle of the current stream without a Stream object (0.1 against 1.9 us), outputs by empty_like.
+# handle of the current stream without a Stream object (0.1 against 1.9 us), outputs by empty_like,
+# and every check of a tensor written out once (an attribute read and compared is 0.2 us).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _enqueue(dev: torch.device, fn, *args):
     """fn(*args, the current stream of dev), with dev as the current device."""
     index = dev.index
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
@@ -527,21 +531,27 @@ def _norm_inputs(x, weight, residual, residual_out):
     if not x.is_cuda:
         raise ValueError("qlq operates on GPU tensors only")
     bf = torch.bfloat16
-    if x.dim() != 2 or x.dtype != bf:
+    shape = x.shape
+    if len(shape) != 2 or x.dtype != bf:
         raise ValueError("x must be a 2-D bf16 tensor")
-    if weight.dtype != bf or weight.dim() != 1 or weight.shape[0] != x.shape[1]:
-        raise ValueError(f"weight must be bf16 [{x.shape[1]}]")
+    if weight.dtype != bf or weight.shape != shape[1:]:
+        raise ValueError(f"weight must be bf16 [{shape[1]}]")
+    dev = x.device
+    if not x.is_contiguous() or weight.device != dev or not weight.is_contiguous():
+        _on(dev, x, weight)
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out needs a residual")
-    else:
-        if residual_out is None:
-            residual_out = torch.empty_like(x)
-        for t in (residual, residual_out):
-            if t.dtype != bf or t.shape != x.shape:
-                raise ValueError(f"residual and residual_out must be bf16 {list(x.shape)}")
-    _on(x.device, x, weight, residual, residual_out)
-    return residual_out
+        return None
+    if residual.dtype != bf or residual.shape != shape or (
+            residual_out is not None and (residual_out.dtype != bf or residual_out.shape != shape)):
+        raise ValueError(f"residual and residual_out must be bf16 {list(shape)}")
+    if residual_out is not None:
+        _on(dev, residual, residual_out)
+        return residual_out
+    if residual.device != dev or not residual.is_contiguous():
+        _on(dev, residual)
+    return torch.empty_like(x)
 
 
 def _norm_codes(x, qtype, out):
@@ -679,10 +689,12 @@ def _token_rows(t: torch.Tensor, name: str) -> int:
 
 def _indices(t: torch.Tensor, n: int, dev: torch.device, name: str) -> int:
     """1 for int64, 0 for int32 indices [n] on dev."""
-    if t.dtype not in (torch.int64, torch.int32) or t.dim() != 1 or t.shape[0] != n:
+    dtype = t.dtype
+    if (dtype != torch.int64 and dtype != torch.int32) or t.shape != (n,):
         raise ValueError(f"{name} must be int32 or int64 [{n}]")
-    _on(dev, t)
-    return int(t.dtype == torch.int64)
+    if t.device != dev or not t.is_contiguous():
+        _on(dev, t)
+    return 1 if dtype == torch.int64 else 0
 
 
 def _frequencies(inv_freq: torch.Tensor, dev: torch.device) -> int:
@@ -695,14 +707,17 @@ def _frequencies(inv_freq: torch.Tensor, dev: torch.device) -> int:
 def _cache_entries(c: QuantizedKV, H: int, D: int, dev: torch.device) -> int:
     """Slots of a cache for H heads of D channels."""
     kc, ks, vc, vs = c.k_codes, c.k_scales, c.v_codes, c.v_scales
-    P = kc.shape[0]
     if D % 32 != 0:
         raise ValueError("head_dim must be a multiple of 32")
-    if kc.shape != (P, H, D) or vc.shape != kc.shape or ks.shape != (P, H, D // 32) or vs.shape != (P, H):
+    shape = kc.shape
+    P = shape[0]
+    if shape != (P, H, D) or vc.shape != shape or ks.shape != (P, H, D // 32) or vs.shape != (P, H):
         raise ValueError(f"the cache must hold [slots, {H}, {D}] entries")
     if kc.element_size() != 1 or vc.element_size() != 1 or ks.dtype != torch.float16 or vs.dtype != torch.float16:
         raise ValueError("the cache must hold 1-byte codes and float16 scales")
-    _on(dev, kc, ks, vc, vs)
+    if not (kc.device == ks.device == vc.device == vs.device == dev and kc.is_contiguous() and ks.is_contiguous()
+            and vc.is_contiguous() and vs.is_contiguous()):
+        _on(dev, kc, ks, vc, vs)
     return P
 
 
