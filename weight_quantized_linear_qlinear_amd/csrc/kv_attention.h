@@ -209,16 +209,89 @@ struct JoinLds {
   float inv[16];                 // a row's reciprocal sum
 };
 
+// Joins n <= N chunks' partial rows, chunk_of(0) on, into the output (done) or the first one's.
+template <int D, int N, int NP, class ChunkOf, class PartRow, class OutRow>
+__device__ __forceinline__ void join_group(const KvAttnArgs& a, __amdgpu_buffer_rsrc_t rs, JoinLds& mine, int lane,
+                                           int rows, int n, bool done, ChunkOf chunk_of, PartRow part_row,
+                                           OutRow out_row) {
+  const int c16 = lane & 15, g4 = lane >> 4;
+  for (int r = 0; 16 * r < rows; ++r) {
+    const int live = min(16, rows - 16 * r);
+    wave_sync();
+    // 64 lanes over (row, 16-byte part); NP passes' loads at a time, the first ahead of the factors
+    constexpr int DP = D / 4;
+    const int parts = live * DP;
+    f32x4 v[NP][N];
+    auto load_parts = [&](int b) {
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const int id = min(b + 64 * k + lane, parts - 1), row = id / DP, dp = id % DP;
+#pragma unroll
+        for (int c = 0; c < N; ++c) v[k][c] = load_partial(rs, part_row(chunk_of(min(c, n - 1)), 16 * r + row) / 4 + dp);
+      }
+    };
+    // factors 2^(M_c - M) of the chunks: four rows at a time, 16 lanes (chunks) per row
+    f32x2 ml[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t p = part_row(chunk_of(min(c16, n - 1)), 16 * r + min(4 * q + g4, live - 1));
+      ml[q] = __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, (int)((p + D) * 4), 0, kCachePolicySc1));
+    }
+    load_parts(0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int row = 4 * q + g4;
+      if (4 * q >= live) break;                              // uniform
+      if (c16 >= n) ml[q] = (f32x2){kNegInf, 0.0f};
+      const float M = max_row16(ml[q].x);
+      const float f = M == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ml[q].x - M);
+      const float L = sum_row16(ml[q].y * f);
+      mine.f[row][c16] = f;
+      if (c16 == 0) {
+        mine.inv[row] = L > 0.0f ? 1.0f / L : 0.0f;
+        if (row < live) {
+          if (!done) {
+            const float out[2] = {M, L};
+            store_run<2>(rs, part_row(chunk_of(0), 16 * r + row) + D, out);
+          } else if (a.lse) {
+            a.lse[out_row(16 * r + row)] = L > 0.0f ? (M + __builtin_amdgcn_logf(L)) * kLn2 : kNegInf;
+          }
+        }
+      }
+    }
+    wave_sync();
+    for (int b = 0; b < parts; b += 64 * NP) {
+      if (b) load_parts(b);
+#pragma unroll
+      for (int k = 0; k < NP; ++k) {
+        const int id = b + 64 * k + lane, row = min(id, parts - 1) / DP, dp = id % DP;
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < N; ++c) sum += v[k][c] * mine.f[row][c];   // f is 0 past the last
+        if (id < parts) {
+          if (done) {
+            const float inv = mine.inv[row];
+            uint32_t* out = reinterpret_cast<uint32_t*>(a.out + out_row(16 * r + row) * D + dp * 4);
+            out[0] = pack_bf16x2(sum.x * inv, sum.y * inv);
+            out[1] = pack_bf16x2(sum.z * inv, sum.w * inv);
+          } else {
+            store_partial(rs, part_row(chunk_of(0), 16 * r + row) / 4 + dp, sum);
+          }
+        }
+      }
+    }
+  }
+}
+
 // Joins the chunks of `rows` rows of a tile, kJoin at a time, then those groups, and so on: the
 // last wave of a group to finish joins it (always in chunk order) into the group's first partial
 // rows, the last group of all into the output.  A partial row is [D sums][M, L, -, -], row
 // part_row(c, row) of the partial region; its stores were made by this wave before the call.
 // counter_of(level, c): this wave's arrival counter of the group that chunk c leads.
-template <int D, class PartRow, class OutRow, class CounterOf>
+template <int D, bool FEW, class PartRow, class OutRow, class CounterOf>
 __device__ __forceinline__ void join_chunks(const KvAttnArgs& a, __amdgpu_buffer_rsrc_t rs, JoinLds& mine, int lane,
                                             const Chunks& ck, int rows, PartRow part_row, OutRow out_row,
                                             CounterOf counter_of) {
-  const int c16 = lane & 15, g4 = lane >> 4;
   for (int level = 0, stride = 1;; ++level, stride *= kJoin) {
     const int ch0 = ck.mine - ck.mine % (stride * kJoin);
     const int n = min(kJoin, (ck.count - ch0 + stride - 1) / stride);
@@ -231,74 +304,10 @@ __device__ __forceinline__ void join_chunks(const KvAttnArgs& a, __amdgpu_buffer
       if (last) reset_counter(counter);
     }
     if (!__builtin_amdgcn_readfirstlane(last)) return;
-    for (int r = 0; 16 * r < rows; ++r) {
-      const int live = min(16, rows - 16 * r);
-      wave_sync();
-      // 64 lanes over (row, 16-byte part); two passes' loads at a time, the first ahead of the factors
-      constexpr int DP = D / 4;
-      const int parts = live * DP;
-      constexpr int NP = 2;
-      f32x4 v[NP][kJoin];
-      auto load_parts = [&](int b) {
-#pragma unroll
-        for (int k = 0; k < NP; ++k) {
-          const int id = min(b + 64 * k + lane, parts - 1), row = id / DP, dp = id % DP;
-#pragma unroll
-          for (int c = 0; c < kJoin; ++c)
-            v[k][c] = load_partial(rs, part_row(ch0 + min(c, n - 1) * stride, 16 * r + row) / 4 + dp);
-        }
-      };
-      // factors 2^(M_c - M) of the chunks: four rows at a time, 16 lanes (chunks) per row
-      f32x2 ml[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t p = part_row(ch0 + min(c16, n - 1) * stride, 16 * r + min(4 * q + g4, live - 1));
-        ml[q] = __builtin_bit_cast(f32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, (int)((p + D) * 4), 0, kCachePolicySc1));
-      }
-      load_parts(0);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int row = 4 * q + g4;
-        if (4 * q >= live) break;                            // uniform
-        if (c16 >= n) ml[q] = (f32x2){kNegInf, 0.0f};
-        const float M = max_row16(ml[q].x);
-        const float f = M == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(ml[q].x - M);
-        const float L = sum_row16(ml[q].y * f);
-        mine.f[row][c16] = f;
-        if (c16 == 0) {
-          mine.inv[row] = L > 0.0f ? 1.0f / L : 0.0f;
-          if (row < live) {
-            if (!done) {
-              const float out[2] = {M, L};
-              store_run<2>(rs, part_row(ch0, 16 * r + row) + D, out);
-            } else if (a.lse) {
-              a.lse[out_row(16 * r + row)] = L > 0.0f ? (M + __builtin_amdgcn_logf(L)) * kLn2 : kNegInf;
-            }
-          }
-        }
-      }
-      wave_sync();
-      for (int b = 0; b < parts; b += 64 * NP) {
-        if (b) load_parts(b);
-#pragma unroll
-        for (int k = 0; k < NP; ++k) {
-          const int id = b + 64 * k + lane, row = min(id, parts - 1) / DP, dp = id % DP;
-          f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int c = 0; c < kJoin; ++c) sum += v[k][c] * mine.f[row][c];   // f is 0 past the last
-          if (id < parts) {
-            if (done) {
-              const float inv = mine.inv[row];
-              uint32_t* out = reinterpret_cast<uint32_t*>(a.out + out_row(16 * r + row) * D + dp * 4);
-              out[0] = pack_bf16x2(sum.x * inv, sum.y * inv);
-              out[1] = pack_bf16x2(sum.z * inv, sum.w * inv);
-            } else {
-              store_partial(rs, part_row(ch0, 16 * r + row) / 4 + dp, sum);
-            }
-          }
-        }
-      }
-    }
+    // Two to four chunks (a prompt's query tiles, mostly) are not read as kJoin: 62 -> 49 us for a
+    // prompt of 512 tokens in 32 heads of 128.  Not for short rows (see the few-row kernel's call).
+    if (FEW && n <= 4) join_group<D, 4, 3>(a, rs, mine, lane, rows, n, done, [&](int c) { return ch0 + c * stride; }, part_row, out_row);
+    else join_group<D, kJoin, 2>(a, rs, mine, lane, rows, n, done, [&](int c) { return ch0 + c * stride; }, part_row, out_row);
     if (done) return;
   }
 }

@@ -499,7 +499,7 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
       }
     }
     if (split && live_rows > 0)
-      join_chunks<D>(a, rs, sm.join[wave], lane, ck, live_rows, part_row, out_row, [&](int level, int c) {
+      join_chunks<D, true>(a, rs, sm.join[wave], lane, ck, live_rows, part_row, out_row, [&](int level, int c) {
         return level * a.level_counters + (ck.slot(c) * hk + h) * kTileWaves + wave;
       });
   }
