@@ -994,7 +994,7 @@ static size_t attn_partial_bytes(const qlq::KvAttnPlan& p, int64_t Hk, int64_t D
 
 size_t qlq_kv_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int one_each) {
   if (!attn_dims_ok(T, B, Hq, Hk, D) || (one_each && T != B)) return 0;
-  const qlq::KvAttnPlan p = qlq::plan_kv_attention(T, B, Hk, Hq / Hk, one_each != 0);
+  const qlq::KvAttnPlan p = qlq::plan_kv_attention(T, B, Hk, Hq / Hk, D, one_each != 0);
   return (kAttnCounterBytes + attn_partial_bytes(p, Hk, D) + 255) / 256 * 256;
 }
 
@@ -1026,7 +1026,7 @@ qlq_status qlq_kv_attention(const void* q, int64_t q_stride, int64_t T, int64_t 
   if (window > 0 && !causal) return fail(QLQ_ERR_INVALID_ARG, "a window needs causal attention");
   if (!aligned(out, 16) || !aligned(seq_lens, 4) || !aligned(q_start, 4) || !aligned(lse, 4))
     return fail(QLQ_ERR_INVALID_ARG, "misaligned pointer");
-  const qlq::KvAttnPlan p = qlq::plan_kv_attention(T, B, Hk, Hq / Hk, q_start == nullptr);
+  const qlq::KvAttnPlan p = qlq::plan_kv_attention(T, B, Hk, Hq / Hk, D, q_start == nullptr);
   const size_t partial = attn_partial_bytes(p, Hk, D), need = kAttnCounterBytes + partial;
   if (p.tiles * (max_pages * page_size / 32 + 1) >= (int64_t(1) << 31) || partial >= ((size_t)1 << 31) ||
       (size_t)p.counters * 12 > kAttnCounterBytes || p.waves > 4096)

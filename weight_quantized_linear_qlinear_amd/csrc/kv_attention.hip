@@ -30,7 +30,7 @@
 // Bound by HBM: a token is 266 bytes per KV head of 128, and 512 operations per query row that
 // shares them.  Measured (MI355X): 64 sequences of 2048 to 8192 tokens, 8 KV heads
 // of 128, 125 us (699 MB, 5.6 TB/s); one of 131071 over 4 KV heads 39.9 us (139 MB; 16 us of it
-// join 256 chunks per head); 16 x 5 tokens, window 1024, 16 heads of 64 19.4 us (latency).
+// join 256 chunks per head); 16 x 5 tokens, window 1024, 16 heads of 64 18 us (latency).
 #include <type_traits>
 
 #include "kv_attention.h"
@@ -163,7 +163,11 @@ __device__ __forceinline__ Tile tile_of(const KvAttnArgs& a, const Extent& mine,
   return t;
 }
 
-constexpr int kWaves = 4;
+// Waves per workgroup (one workgroup per CU).  Heads of 32 and 64 leave registers for two waves per
+// SIMD, which their short rows need: 32 sequences of 16000 tokens, 4 heads of 64, 62 us against 74,
+// 16 x 5 tokens in a window of 1024, 16 heads of 64, 18.1 against 20.2; from 96 on eight waves are
+// slower (8 heads of 96 67 against 64, 4 of 128 42 against 39).
+constexpr int waves_of(int NG) { return NG <= 2 ? 8 : 4; }
 
 // A wave's LDS: the token scales of its tile, or what joining needs.
 template <int NG>
@@ -176,8 +180,8 @@ union WaveLds {
 };
 
 template <int NG, int R>
-__global__ __launch_bounds__(kWaves * 64) void kv_attention_kernel(KvAttnArgs a) {
-  constexpr int D = 32 * NG, TR = 16 * R;
+__global__ __launch_bounds__(waves_of(NG) * 64) void kv_attention_kernel(KvAttnArgs a) {
+  constexpr int D = 32 * NG, TR = 16 * R, kWaves = waves_of(NG);
   // Codes are read once per 16 R rows: streamed past the caches where a head's row fills whole
   // cache lines (128 bytes); shorter ones share lines between waves.
   constexpr bool NT = R == 1 && NG % 4 == 0;
@@ -507,14 +511,14 @@ __global__ __launch_bounds__(kWaves * 64) void kv_attention_kernel(KvAttnArgs a)
 
 template <int NG>
 hipError_t launch_ng(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t st) {
-  if (p.R == 1) kv_attention_kernel<NG, 1><<<(int)p.grid, kWaves * 64, 0, st>>>(a);
-  else kv_attention_kernel<NG, 2><<<(int)p.grid, kWaves * 64, 0, st>>>(a);
+  if (p.R == 1) kv_attention_kernel<NG, 1><<<(int)p.grid, waves_of(NG) * 64, 0, st>>>(a);
+  else kv_attention_kernel<NG, 2><<<(int)p.grid, waves_of(NG) * 64, 0, st>>>(a);
   return hipGetLastError();
 }
 
 }  // namespace
 
-KvAttnPlan plan_kv_attention(int64_t T, int64_t B, int64_t Hk, int64_t G, bool one_each) {
+KvAttnPlan plan_kv_attention(int64_t T, int64_t B, int64_t Hk, int64_t G, int64_t D, bool one_each) {
   KvAttnPlan p;
   const int64_t rows = one_each ? G : (T + B - 1) / B * G;   // query rows of an average sequence
   // More than 32 rows: kv_attention_tile.hip, one workgroup of eight waves per CU.  (17 to 32 rows
@@ -532,16 +536,19 @@ KvAttnPlan plan_kv_attention(int64_t T, int64_t B, int64_t Hk, int64_t G, bool o
   }
   p.R = rows <= 16 ? 1 : 2;
   const int64_t TR = 16 * p.R;
-  // Neighbouring KV heads per workgroup: a power of two that divides Hk, at most the waves.
-  while ((2 << p.hw_shift) <= kWaves && Hk % (2 << p.hw_shift) == 0) ++p.hw_shift;
-  // One workgroup of four waves per CU.  Half, one and a half, and two of them: 215, 165 and 141 us
+  // Neighbouring KV heads per workgroup: a power of two that divides Hk, at most four (eight, where
+  // there are eight waves: 70 against 75 us for 32 sequences of 4000 tokens and 16 heads of 64, but
+  // 20.4 against 18.1 for 16 x 5 tokens in a window of 1024).
+  while ((2 << p.hw_shift) <= 4 && Hk % (2 << p.hw_shift) == 0) ++p.hw_shift;
+  const int waves = waves_of((int)(D / 32));
+  // One workgroup per CU.  Half, one and a half, and two of them: 215, 165 and 141 us
   // against 126 for 64 sequences of up to 8192 tokens, and 27.0, 19.6 and 19.0 against 19.8 for
-  // 16 x 5 tokens in a window of 1024: more waves are more chunks to join.
+  // 16 x 5 tokens in a window of 1024 (four waves each): more waves are more chunks to join.
   const int64_t HG = Hk >> p.hw_shift;
   const int64_t parts = 256 / HG;
   p.parts = (int)(parts >= 8 ? parts / 8 * 8 : parts < 1 ? 1 : parts);
   p.grid = p.parts * HG;
-  p.waves = p.parts * (kWaves >> p.hw_shift);
+  p.waves = p.parts * (waves >> p.hw_shift);
   p.tile_rows = (int)(one_each && G < TR ? G : TR);
   p.counters = 2 * p.waves * Hk;
   p.tiles = one_each ? B * ((G + TR - 1) / TR) : T * G / TR + B;

@@ -140,7 +140,7 @@ struct KvAttnPlan {
   int tile_rows = 0;           // rows of a partial
   int64_t tiles = 0, grid = 0; // query tiles at most, workgroups
 };
-KvAttnPlan plan_kv_attention(int64_t T, int64_t B, int64_t Hk, int64_t G, bool one_each);
+KvAttnPlan plan_kv_attention(int64_t T, int64_t B, int64_t Hk, int64_t G, int64_t D, bool one_each);
 hipError_t launch_kv_attention_tile(const KvAttnArgs& a, const KvAttnPlan& p, int D, hipStream_t st);
 hipError_t launch_kv_attention(const KvAttnArgs& a, const KvAttnPlan& p, int D, hipStream_t st);
 
