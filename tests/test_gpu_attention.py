@@ -11,7 +11,7 @@ S = sum_t p_t |v_t|, n tokens seen, A = max_t scale sum_c |q_c k_c| and V = max 
   sums      (n / 32 + 32) u
 so |out - out64| <= 2^-8 |out64| + S (2^-11 + 2 E) + n 2^-25 V, E = u (42 A + A' + 3 (2 A + 56) + n / 32 + 40),
 and |lse - lse64| <= 2 E + u |lse|.
-Many query rows (more than 32 per KV head and sequence, on average): K and V are rounded to 11 bits after their
+Many query rows (per KV head and sequence, on average, more than 32 for heads of 96 and 128, 64 for others): K and V are rounded to 11 bits after their
 scales as well, 2^-11 of a product, so E grows by 2^-11 A (and by 2^-25 scale sum|q| below fp16's normal range,
 less than A' u for the keys here) and the output's error by 2^-11 S."""
 import math
@@ -110,7 +110,7 @@ class Problem:
         A = A1 if used.size == 0 else abs(sc) * max(
             (np.abs(q[:, h]) @ ku[:, h // (self.Hq // self.Hk)].T).max() for h in range(self.Hq))
         E = U * (42 * A + A1 + 3 * (2 * A + 56) + n / 32 + 40)
-        wide = -(-self.T // len(lens)) * (self.Hq // self.Hk) > 32
+        wide = -(-self.T // len(lens)) * (self.Hq // self.Hk) > (32 if self.D in (96, 128) else 64)
         W = 2.0 ** -11
         if wide:
             E, W = E + 2.0 ** -11 * A + U * A1, 2 * W

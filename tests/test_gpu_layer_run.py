@@ -138,10 +138,10 @@ def _prefill(lay, cache, table, lengths, seen=None):
 def test_prompts_then_tokens(qtype):
     lay, cache, table = _start(qtype)
     before = [t.clone() for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales)]
-    lengths, seen = [37, 5], {}
+    lengths, seen = [61, 5], {}
     pos, slots, lens, starts, out = _prefill(lay, cache, table, lengths, seen)
     written = _check_stages(lay, seen, cache, pos, slots, table, lens, starts.cpu().numpy(), wide=True)
-    assert written.sum() == 42 and torch.all(out[42:] == 7.0)      # rows of no sequence: as they were
+    assert written.sum() == 66 and torch.all(out[66:] == 7.0)      # rows of no sequence: as they were
     used = torch.zeros(PAGES * PAGE, dtype=torch.bool, device=dev())
     used[slots[slots >= 0]] = True
     for a, b in zip((cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales), before):
@@ -161,7 +161,7 @@ def test_captured_layer_replays_as_the_eager_one_runs():
     """Decode steps through one captured layer, its inputs changed in place; an eager twin on a second cache runs
     between the replays."""
     lay, cache, table = _start("fp8_e4m3fn")
-    lengths = [37, 5]
+    lengths = [61, 5]
     _prefill(lay, cache, table, lengths)
     twin = qlq.QuantizedKV(*(t.clone() for t in (cache.k_codes, cache.k_scales, cache.v_codes, cache.v_scales)))
     x, pos = _rows(5, 3), torch.zeros(3, dtype=torch.int64, device=dev())

@@ -169,6 +169,12 @@ __device__ __forceinline__ Tile tile_of(const KvAttnArgs& a, const Extent& mine,
 // slower (8 heads of 96 67 against 64, 4 of 128 42 against 39).
 constexpr int waves_of(int NG) { return NG <= 2 ? 8 : 4; }
 
+// Whether 17 to 32 rows go as one tile of two subtiles or as two tiles that read K and V each: 16
+// sequences of 24 rows over 4000 and 16000 tokens take 69 and 160 us against 74 and 199 for heads
+// of 128, but 112 and 231 against 75 and 138 for heads of 256 (registers), 94 and 163 against 62
+// and 149 of 192, 55 and 98 against 37 and 111 of 64 (twice the waves).
+constexpr bool pairs_rows(int NG) { return NG == 3 || NG == 4; }
+
 // A wave's LDS: the token scales of its tile, or what joining needs.
 template <int NG>
 union WaveLds {
@@ -511,8 +517,12 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv_attention_kernel(KvAttnA
 
 template <int NG>
 hipError_t launch_ng(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t st) {
-  if (p.R == 1) kv_attention_kernel<NG, 1><<<(int)p.grid, waves_of(NG) * 64, 0, st>>>(a);
-  else kv_attention_kernel<NG, 2><<<(int)p.grid, waves_of(NG) * 64, 0, st>>>(a);
+  if constexpr (pairs_rows(NG))
+    if (p.R == 2) {
+      kv_attention_kernel<NG, 2><<<(int)p.grid, waves_of(NG) * 64, 0, st>>>(a);
+      return hipGetLastError();
+    }
+  kv_attention_kernel<NG, 1><<<(int)p.grid, waves_of(NG) * 64, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -521,10 +531,13 @@ hipError_t launch_ng(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t st) {
 KvAttnPlan plan_kv_attention(int64_t T, int64_t B, int64_t Hk, int64_t G, int64_t D, bool one_each) {
   KvAttnPlan p;
   const int64_t rows = one_each ? G : (T + B - 1) / B * G;   // query rows of an average sequence
-  // More than 32 rows: kv_attention_tile.hip, one workgroup of eight waves per CU.  (17 to 32 rows
-  // there and here, 16 sequences of 6 x 4 rows, heads of 128 over 8 KV heads: 93 and 69 us at 4000
-  // tokens each, 262 and 159 us at 16000.)
-  if (rows > 32) {
+  // Many rows: kv_attention_tile.hip, one workgroup of eight waves per CU.  From where on, by 16
+  // sequences of 4000 and 16000 tokens, there and here: 24 rows of 128 over 8 KV heads 93 and 262
+  // against 69 and 159 us, 40 rows 94 and 269 against 100 and 261; 64 rows of 64 76 and 245 against
+  // 62 and 199, of 192 107 and 265 against 88 and 241, of 256 125 and 352 against 97 and 214; 96
+  // rows of 64 78 and 248 against 85 and 308, of 192 115 and 271 against 109 and 376.
+  const bool pairs = pairs_rows((int)(D / 32));
+  if (rows > (pairs ? 32 : 64)) {
     p.R = 16;
     p.parts = (int)(Hk >= 256 ? 1 : 256 / Hk);
     p.grid = p.parts * Hk;
@@ -534,7 +547,7 @@ KvAttnPlan plan_kv_attention(int64_t T, int64_t B, int64_t Hk, int64_t G, int64_
     p.tiles = one_each ? B * ((G + 255) / 256) : T * G / 256 + B;
     return p;
   }
-  p.R = rows <= 16 ? 1 : 2;
+  p.R = rows <= 16 || !pairs ? 1 : 2;
   const int64_t TR = 16 * p.R;
   // Neighbouring KV heads per workgroup: a power of two that divides Hk, at most four (eight, where
   // there are eight waves: 70 against 75 us for 32 sequences of 4000 tokens and 16 heads of 64, but
