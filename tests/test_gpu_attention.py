@@ -369,6 +369,41 @@ def test_captured_and_replayed_with_changing_lengths():
         assert torch.equal(p.run(), want_short if i % 3 == 1 else want), i      # eager between the replays
 
 
+def test_two_graphs_replayed_at_once():
+    # a token's split attention and a prompt chunk's, each captured, replayed on two streams together
+    ps = [Problem(30, (1,), (30000,), 4, 1, 64, 256), Problem(31, (150, 40), (1000, 700), 4, 2, 128, 64, each=False)]
+    want = [p.run().clone() for p in ps]
+    outs, graphs = [torch.empty_like(p.q) for p in ps], []
+    for p, o in zip(ps, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            p.run(out=o)
+        graphs.append(g)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(4):
+        for o in outs:
+            o.zero_()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for s, g in zip(streams, graphs):
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        for p, o, w in zip(ps, outs, want):
+            assert torch.equal(o, w)
+            assert torch.equal(p.run(), w)
+
+
+@pytest.mark.parametrize("heads", [(34, 1, 128), (72, 1, 64), (130, 2, 96), (128, 1, 192), (1024, 1, 32), (1024, 1024, 32),
+                                   (331, 331, 32)])
+def test_single_tokens_of_many_heads(heads):
+    # one query token with more rows than a subtile, or than the many-row kernel's tile; more heads than workgroups
+    Hq, Hk, D = heads
+    print(f"attention heads={heads}", flush=True)
+    p = Problem(Hq + Hk + D, [1] * 4, [0, 1, 65, 200], Hq, Hk, D, 16)
+    p.check(what=f"{heads}")
+
+
 def test_offsets_beyond_four_gigabytes():
     Hk, D, page = 8, 256, 256
     pool = (((1 << 32) // (Hk * D)) // page + 3) * page
