@@ -93,6 +93,31 @@ def test_norm_matches_the_oracle(MK, residual):
         _check_codes(codes(got[0]), y64, np.float64(s_in), qtype, f"static {qtype}")
 
 
+def test_codes_are_the_quotients_roundings():
+    # without a residual h is x itself; h w, its product with a factor that fp64 gives, and (dynamic) the largest
+    # |h w| are rounded once each, so a code can differ from the float64 quotient's only within 3 u of a border
+    near = 3 * U * (1 + 2.0 ** -10)
+    for (M, K), qtype in (((1200, 2048), "int8"), ((1100, 1536), "fp8_e4m3fn"), ((40, 5001), "int8"), ((9, 12000), "fp8_e4m3fn")):
+        rng = np.random.default_rng(K)
+        xb, wb = (oracle.f32_to_bf16_bits(a.astype(np.float32)) for a in (rng.standard_normal((M, K)), 1 + 0.3 * rng.standard_normal(K)))
+        y64, _ = layer.rms_norm(bits_to_f64(xb), bits_to_f64(wb), EPS)
+        qmax = 127.0 if qtype == "int8" else 448.0
+        s = np.float32(np.abs(y64).max() / qmax)
+        x, w = bf16_to_gpu(xb), bf16_to_gpu(wb)
+        static = codes(qlq.rms_norm_quant_static(x, w, float(s), qtype, EPS))
+        dynamic = codes(qlq.rms_norm_quant_dynamic(x, w, qtype, EPS)[0])
+        for got, quotient in ((static, y64 / np.float64(s)), (dynamic, y64 / (np.abs(y64).max(1, keepdims=True) / qmax))):
+            if qtype == "int8":
+                g = got.view(np.int8).astype(np.float64)
+                border = np.abs(quotient - g) - 0.5 - near * np.abs(quotient)    # beyond the half step
+            else:
+                g = oracle.e4m3fn_decode(got).astype(np.float64)
+                step = 2.0 ** np.maximum(np.floor(np.log2(np.maximum(np.abs(quotient), 2.0 ** -20))) - 3, -9)
+                border = np.abs(quotient - g) / step - 0.5 - near * np.abs(quotient) / step
+            over = (border > 2.0 ** -40) & (np.abs(quotient) <= qmax)
+            assert not over.any(), f"{M}x{K} {qtype}: {over.sum()} codes on the other side of a border"
+
+
 @pytest.mark.parametrize("MK", [(5, 2048), (1024, 1000), (3, 77), (2, 70000)])
 def test_norm_in_place_equals_out_of_place(MK):
     M, K = MK
@@ -132,10 +157,10 @@ def test_norm_at_odd_addresses(shift):
 
 
 def test_norm_extreme_static_scales():
-    # scales whose reciprocal leaves fp32's normal range take the IEEE division
+    # scales whose reciprocal leaves the range of the product form take the IEEE division
     (xb, _, wb), (x, _, w) = _inputs(9, 4, 256)
     y64, _ = layer.rms_norm(x, w, EPS)
-    for s_in in (1e-38, 3e38):
+    for s_in in (1e-38, 1e-9, 3e38):
         c = qlq.rms_norm_quant_static(bf16_to_gpu(xb), bf16_to_gpu(wb), s_in, "int8", EPS)
         _check_codes(codes(c), y64, np.float64(np.float32(s_in)), "int8", f"scale {s_in}")
 
