@@ -18,8 +18,8 @@
 // Bound by HBM for many rows (2 K bytes of x, 2 K of the residual in and out, K of codes per
 // row) and by latency for few: a row is read once, kept in registers as fp32 (8 elements per
 // 16-byte chunk, NC chunks per thread) and written once.  Measured (MI355X, kernel alone): 8192
-// rows of 4096 with a residual, bf16 out, 43.6 us (268 MB, 6.2 TB/s); 333 of 4096 to FP8 5.0 us;
-// 1000 of 2048 to INT8 5.4 us; one of 2048 to FP8 2.6 us.
+// rows of 4096 with a residual, bf16 out, 43.6 us (268 MB, 6.2 TB/s); 333 of 4096 to FP8 5.2 us;
+// 1000 of 2048 to INT8 5.8 us; one of 2048 to FP8 2.7 us.
 #include "qlq_device.h"
 #include "qlq_launch.h"
 
