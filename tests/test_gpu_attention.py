@@ -404,10 +404,11 @@ def test_single_tokens_of_many_heads(heads):
     p.check(what=f"{heads}")
 
 
-def test_offsets_beyond_four_gigabytes():
+@pytest.mark.parametrize("nqs", [(1, 1), (90, 70)])
+def test_offsets_beyond_four_gigabytes(nqs):
     Hk, D, page = 8, 256, 256
     pool = (((1 << 32) // (Hk * D)) // page + 3) * page
-    small = Problem(20, (1, 1), (500, 300), 8, Hk, D, page)
+    small = Problem(20, nqs, (500, 300), 8, Hk, D, page)
     pages = small.pool // page
     big = qlq.QuantizedKV(torch.empty((pool, Hk, D), dtype=torch.int8, device=dev()),
                           torch.empty((pool, Hk, D // 32), dtype=torch.float16, device=dev()),
@@ -418,7 +419,7 @@ def test_offsets_beyond_four_gigabytes():
                  (big.v_codes, small.cache.v_codes), (big.v_scales, small.cache.v_scales)):
         a[at:] = b
     bt = torch.where((small.bt >= 0) & (small.bt < pages), small.bt + at // page, small.bt)
-    out = qlq.kv_attention(small.q, big, bt, small.sl, page)
+    out = qlq.kv_attention(small.q, big, bt, small.sl, page, q_start=small.q0)
     assert torch.equal(out, small.run())
 
 
