@@ -19,8 +19,8 @@
 // Bound by instruction issue: per 64 tokens a wave of 128-channel heads issues 32 products (32
 // cycles each), 33 exponentials and about 200 other vector instructions, and two waves share a
 // SIMD; the matrix cores are busy 31 % of the time, LDS 25 %.  Measured (MI355X): two chunks of
-// 1500 and 804 queries over 8192 and 4394 tokens, 32 heads over 8 of 128, 313 us (235 GFLOP, 750
-// TFLOP/s); a prompt of 512 tokens on its own 49 us, half of it storing and joining partial sums.
+// 1500 and 804 queries over 8192 and 4394 tokens, 32 heads over 8 of 128, 313 to 333 us (235 GFLOP,
+// 730 TFLOP/s); a prompt of 512 tokens on its own 49 us, half of it storing and joining partial sums.
 #include "kv_attention.h"
 
 namespace qlq {
