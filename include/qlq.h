@@ -359,8 +359,10 @@ qlq_status qlq_kv_gather(const void* k_codes, const void* k_scales, const void* 
  * window needs causal).  Query head h reads KV head h / (Hq / Hk).
  *   out = softmax_t(scale q . k_t) v_t with k_t = k_code k_scale and v_t = v_code v_scale, not
  *   rounded to bf16; lse (or NULL) = log sum_t exp(scale q . k_t), fp32 [T, Hq]
- * fp32 accumulation, weights in 11 bits; with many query rows per KV head and sequence on average
- * (more than 32 for D 96 and 128, 64 for the others) also k_code k_scale and v_code v_scale.  A row that sees no token gives zeros and lse -inf;
+ * fp32 accumulation, weights rounded to fp16: 2^-11 of a weight, 2^-40 of the row's largest for
+ * those below 2^-29 of it.  With many query rows per KV head and sequence on average (more than 32
+ * for D 96 and 128, 64 for the others) k_code k_scale and v_code v_scale have 11 bits too, and small
+ * weights are off by 2^-32 of the largest.  A row that sees no token gives zeros and lse -inf;
  * rows of q outside every sequence are left as they were in out and lse.
  * q bf16 [T, Hq, D], token stride in elements (a multiple of 8); out bf16 [T, Hq, D] dense; D 32,
  * 64, 96, 128, 192 or 256; page_size a power of two, 16 .. 2^20; pool a multiple of it.  block_table int32

@@ -1,0 +1,66 @@
+"""Attention over the 8-bit cache where the softmax or its masks are at their limits.
+
+Weights far below a row's largest: w_t = 2^(x_t - m) goes to fp16 with the largest weight 2^15, so a weight is off
+by at most 2^-11 of itself or, below 2^-14, by 2^-25, i.e. by 2^-40 of the largest.  With n tokens, V = max |v| and
+S = sum_t p_t |v_t| an output is off by at most 2^-8 of itself (bf16), (2^-11 + 2 E) S and n 2^-40 V, E the
+exponent's error: scores are single products here (one channel of q is not zero), so E = u (3 (2 A + 56) + n / 32 + 40)
+with u = 2^-24 and A the largest score (test_gpu_attention.py has the terms)."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import weight_quantized_linear_qlinear_amd as qlq
+from tests.gpu_util import bf16_bits, bf16_to_gpu, bits_to_f64, dev
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+def _gpu(a, dt):
+    return torch.from_numpy(np.ascontiguousarray(a)).view(dt).to(dev())
+
+
+@pytest.mark.parametrize("octaves", [20.0, 25.2, 33.0])
+@pytest.mark.parametrize("heads", [(4, 1, 64), (4, 4, 128), (8, 2, 96), (2, 1, 192), (2, 1, 256), (3, 1, 32)])
+@pytest.mark.parametrize("BL", [(1, 32), (300, 3000)])
+def test_tail_far_below_the_largest_weight(BL, heads, octaves):
+    # One token outweighs every other by `octaves`, and half of the channels are zero in its values: there the
+    # output is the others' alone.  32 tokens are one wave's; of the long sequences (which share their pages) a
+    # wave takes hundreds and more.
+    (B, L), (Hq, Hk, D) = BL, heads
+    print(f"tail B={B} L={L} heads={heads} octaves={octaves}", flush=True)
+    rng = np.random.default_rng(L + D)
+    page = 32
+    pages = -(-L // page)
+    P, top = pages * page, L // 3
+    kc = np.zeros((P, Hk, D), np.int8)
+    kc[:, :, 1:] = rng.integers(-127, 128, size=(P, Hk, D - 1))
+    kc[top, :, 0] = 64
+    vc = rng.integers(0x30, 0x7F, size=(P, Hk, D)).astype(np.uint8)          # 0.5 .. 448
+    vc[top, :, ::2] = 0
+    ks, vs = np.full((P, Hk, D // 32), 2.0 ** -6, np.float16), np.full((P, Hk), 2.0 ** -8, np.float16)
+    q = np.zeros((Hq, D), np.float32)
+    q[:, 0] = octaves * np.log(2.0) * (1 + np.arange(Hq) / 256)
+    qb = oracle.f32_to_bf16_bits(q)
+    table = torch.arange(pages, dtype=torch.int32, device=dev()).expand(B, pages).contiguous()
+    lens = torch.full((B,), L, dtype=torch.int32, device=dev())
+    cache = qlq.QuantizedKV(_gpu(kc, torch.int8), _gpu(ks, torch.float16), _gpu(vc, torch.uint8), _gpu(vs, torch.float16))
+    lse = torch.zeros(B, Hq, device=dev())
+    out = qlq.kv_attention(bf16_to_gpu(np.broadcast_to(qb, (B, Hq, D))), cache, table, lens, page, scale=1.0, lse=lse)
+    k = kc.astype(np.float64) * 2.0 ** -6
+    v = oracle.e4m3fn_decode(vc).astype(np.float64) * 2.0 ** -8
+    q64 = bits_to_f64(qb)
+    got, got_lse = bits_to_f64(bf16_bits(out)), lse.cpu().numpy().astype(np.float64)
+    for h in range(Hq):
+        s = k[:L, h // (Hq // Hk)] @ q64[h]
+        p = np.exp(s - s.max())
+        l64 = s.max() + np.log(p.sum())
+        p /= p.sum()
+        o64 = p @ v[:L, h // (Hq // Hk)]
+        E = U * (3 * (2 * np.abs(s).max() + 56) + L / 32 + 40)
+        bound = 2.0 ** -8 * o64 + (2.0 ** -11 + 2 * E) * o64 + L * 2.0 ** -40 * np.abs(v).max()      # (v >= 0: S = o)
+        over = np.abs(got[:, h] - o64) / bound
+        assert over.max() <= 1.0, f"head {h}: {over.max():.2f} times the bound"
+        assert np.abs(got_lse[:, h] - l64).max() <= 2 * E + U * abs(l64)

@@ -6,13 +6,16 @@
 //   s_t = scale * sum_c k_scale[t,c] * (q_c . k_code[t,c])      (c: groups of 32 channels)
 //   o   = sum_t 2^(s_t log2e) v_scale_t v_code_t / sum_t 2^(s_t log2e)
 // in one pass with a running reference m and sum l.  v_scale_t is taken into the exponent:
-//   x_t = s_t log2e + log2 v_scale_t,  w_t = 2^(x_t - m) in [0, 1],  o = sum w_t v_code_t,
-//   l = sum w_t / v_scale_t,
+//   x_t = s_t log2e + log2 v_scale_t,  m = max x_t - 15,  w_t = 2^(x_t - m) in [0, 2^15],
+//   o = sum w_t v_code_t,  l = sum w_t / v_scale_t,
 // so that the weights fit fp16 whatever the scales are.  Products run on the matrix cores in
 // fp16 with fp32 accumulation: int8 and e4m3 codes are exact in fp16, q is scaled per row by a
 // power of two into [-1, 1) (exact but for channels 2^-14 and more below the row's largest,
-// whose absolute error stays under 2^-25 of it), and the weights' rounding to 11 bits is the
-// only other one (2^-11 of a weight; the output's own rounding to bf16 is 2^-8).
+// whose absolute error stays under 2^-25 of it), and the weights' rounding to fp16 is the
+// only other one: 2^-11 of a weight down to 2^-29 of the row's largest, below that 2^-40 of the
+// largest (l adds the weights before it; the output's own rounding to bf16 is 2^-8).  With the
+// largest weight 1 instead, many small ones beside a large one are lost: 31 of them 25 octaves down
+// altogether, a long tail of 131071 to 0.3 % of the output.
 //
 // Layout.  A wave takes one KV head, 16 R query rows (nq x G rows packed, so that the heads of
 // a group share every K and V load) and a run of tokens, 32 at a time, on its own; the waves of
@@ -104,6 +107,9 @@ __device__ __forceinline__ void pv_piece(const Raw<2 * P, NT> (&v)[8], const f16
     }
   }
 }
+
+// Octaves from a row's reference up to its largest weight: 2^15 is the largest power of two in fp16.
+constexpr float kLift = 15.0f;
 
 // The first token that any query of the sequence can see (rounded down to a tile of 32), and
 // the tiles of 32 from there.
@@ -430,7 +436,7 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv_attention_kernel(KvAttnA
           mx = fmaxf(mx, v);
         }
       mx = max_across16(mx);
-      const float mn = fmaxf(m[r], mx);
+      const float mn = fmaxf(m[r], mx - kLift);
       const float ref = mn == kNegInf ? 0.0f : mn;
       if (__ballot(mn > m[r])) {
         const float corr = __builtin_amdgcn_exp2f(m[r] - ref);
