@@ -362,7 +362,8 @@ qlq_status qlq_kv_gather(const void* k_codes, const void* k_scales, const void* 
  * fp32 accumulation, weights rounded to fp16: 2^-11 of a weight, 2^-40 of the row's largest for
  * those below 2^-29 of it.  With many query rows per KV head and sequence on average (more than 32
  * for D 96 and 128, 64 for the others) k_code k_scale and v_code v_scale have 11 bits too, and small
- * weights are off by 2^-32 of the largest.  A row that sees no token gives zeros and lse -inf;
+ * weights are off by 2^-32 of the largest.  A row that sees no token gives zeros and lse -inf, a
+ * NaN in a query row NaN in that row's out and lse;
  * rows of q outside every sequence are left as they were in out and lse.
  * q bf16 [T, Hq, D], token stride in elements (a multiple of 8); out bf16 [T, Hq, D] dense; D 32,
  * 64, 96, 128, 192 or 256; page_size a power of two, 16 .. 2^20; pool a multiple of it.  block_table int32

@@ -12,6 +12,7 @@ import torch
 import oracle
 import weight_quantized_linear_qlinear_amd as qlq
 from tests.gpu_util import bf16_bits, bf16_to_gpu, bits_to_f64, dev
+from tests.test_gpu_attention import Problem
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +65,22 @@ def test_tail_far_below_the_largest_weight(BL, heads, octaves):
         over = np.abs(got[:, h] - o64) / bound
         assert over.max() <= 1.0, f"head {h}: {over.max():.2f} times the bound"
         assert np.abs(got_lse[:, h] - l64).max() <= 2 * E + U * abs(l64)
+
+
+@pytest.mark.parametrize("case", [((1, 1, 1), (40, 20, 90), "few rows"), ((1, 1), (9000, 700), "few rows, joined"),
+                                  ((150, 40), (150, 300), "many rows"), ((90,), (3000,), "many rows, joined")])
+def test_a_query_with_nan_is_nan_in_its_own_row_alone(case):
+    nqs, lens, what = case
+    print(f"NaN query: {what}", flush=True)
+    for Hq, Hk, D in ((4, 2, 64), (4, 1, 128)):
+        p = Problem(sum(lens) + D, nqs, lens, Hq, Hk, D, 16, each=False)
+        lse0, lse = torch.zeros(p.T, Hq, device=dev()), torch.zeros(p.T, Hq, device=dev())
+        out0 = p.run(lse=lse0).clone()
+        hit = [(0, 1), (p.T - 1, 3)]
+        for t, h in hit:
+            p.q[t, h, 5] = float("nan")
+        out = p.run(lse=lse)
+        for t, h in hit:
+            assert bool(torch.isnan(out[t, h]).all()) and bool(torch.isnan(lse[t, h])), what
+            out[t, h], lse[t, h] = out0[t, h], lse0[t, h]
+        assert torch.equal(out, out0) and torch.equal(lse, lse0), what

@@ -248,13 +248,13 @@ __device__ __forceinline__ void join_group(const KvAttnArgs& a, __amdgpu_buffer_
       const float L = sum_row16(ml[q].y * f);
       mine.f[row][c16] = f;
       if (c16 == 0) {
-        mine.inv[row] = L > 0.0f ? 1.0f / L : 0.0f;
+        mine.inv[row] = L == 0.0f ? 0.0f : 1.0f / L;       // (NaN stays NaN)
         if (row < live) {
           if (!done) {
             const float out[2] = {M, L};
             store_run<2>(rs, part_row(chunk_of(0), 16 * r + row) + D, out);
           } else if (a.lse) {
-            a.lse[out_row(16 * r + row)] = L > 0.0f ? (M + __builtin_amdgcn_logf(L)) * kLn2 : kNegInf;
+            a.lse[out_row(16 * r + row)] = L == 0.0f ? kNegInf : (M + __builtin_amdgcn_logf(L)) * kLn2;
           }
         }
       }

@@ -489,7 +489,7 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv_attention_kernel(KvAttnA
           for (int n = 0; n < W2; ++n) v2r[j][n] = o[W1 + n][r][j];
       }
       if (!split) {
-        const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+        const float inv = L == 0.0f ? 0.0f : 1.0f / L;          // (NaN stays NaN)
         const int64_t at = out_row(r0 + row);
         uint16_t* out = a.out + at * D;
 #pragma unroll
@@ -497,7 +497,7 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv_attention_kernel(KvAttnA
           store_out<W1>(out + (4 * g4 + j) * W1, v1r[j], inv);
           if constexpr (kTwo) store_out<W2>(out + 32 * P1::P + (4 * g4 + j) * W2, v2r[j], inv);
         }
-        if (a.lse && g4 == 0) a.lse[at] = L > 0.0f ? (m[r] + __builtin_amdgcn_logf(L)) * kLn2 : kNegInf;
+        if (a.lse && g4 == 0) a.lse[at] = L == 0.0f ? kNegInf : (m[r] + __builtin_amdgcn_logf(L)) * kLn2;
       } else {
         const int64_t p = part_row(ck.mine, row);
 #pragma unroll

@@ -479,7 +479,7 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
     const float L = across32(l, true), back = __builtin_ldexpf(1.0f, cur_e);
     if (c32 < live_rows) {
       if (!split) {
-        const float inv = L > 0.0f ? back / L : 0.0f;
+        const float inv = L == 0.0f ? 0.0f : back / L;       // (NaN stays NaN)
         const int64_t row = out_row(c32);
 #pragma unroll
         for (int d = 0; d < NG; ++d)
@@ -488,7 +488,7 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
             const float v[4] = {o[d][4 * q], o[d][4 * q + 1], o[d][4 * q + 2], o[d][4 * q + 3]};
             store_out<4>(a.out + row * D + 32 * d + 8 * q + 4 * half, v, inv);
           }
-        if (a.lse && half == 0) a.lse[row] = L > 0.0f ? (m + __builtin_amdgcn_logf(L)) * kLn2 : kNegInf;
+        if (a.lse && half == 0) a.lse[row] = L == 0.0f ? kNegInf : (m + __builtin_amdgcn_logf(L)) * kLn2;
       } else {
         const int64_t row = part_row(ck.mine, c32);
 #pragma unroll
