@@ -307,8 +307,9 @@ qlq_status qlq_rms_norm(const void* x_bf16, const void* residual_bf16, const voi
  *   static:  yq = sat(round-to-nearest-even(y / input_scale))
  *   dynamic: y_scale[m] = absmax_k |y[m,k]| / qmax (1 for an all-zero row), yq by it
  * with qmax 127 (INT8) or 448 (e4m3fn).  y is the fp32 value (not rounded to bf16 first) and the
- * quotient is fp32 to within one unit in the last place.  yq [M, K] one byte per code, not
- * overlapping any input; y_scale fp32 [M] (device).  residual_out as above. */
+ * quotient is fp32 to within one unit in the last place.  A row with a NaN or an infinity has a NaN
+ * scale; a code cannot hold one and saturates.  yq [M, K] one byte per code, not overlapping any
+ * input; y_scale fp32 [M] (device).  residual_out as above. */
 qlq_status qlq_rms_norm_quant_static(const void* x_bf16, const void* residual_bf16, const void* weight_bf16, int64_t M,
                                      int64_t K, float eps, float input_scale, qlq_qtype qtype, void* yq,
                                      void* residual_out_bf16, hipStream_t stream);

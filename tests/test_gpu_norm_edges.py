@@ -1,0 +1,62 @@
+"""RMS norm at the limits of its inputs."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import weight_quantized_linear_qlinear_amd as qlq
+from oracle import layer
+from tests.gpu_util import bf16_bits, bf16_to_gpu, bits_to_f64, codes
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-6
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("MK", [(6, 64), (1030, 520), (5, 4096), (6, 20000), (7, 333)])
+def test_nan_and_infinite_rows(MK, residual):
+    # A row with a NaN or an infinity: y is what the formula gives in float64 (NaN all over, or NaN at the infinity and
+    # zero beside it); its dynamic scale is NaN, also where no element is a number; other rows do not change.
+    M, K = MK
+    print(f"norm NaN rows M={M} K={K} residual={residual}", flush=True)
+    rng = np.random.default_rng(M + K)
+    clean = [oracle.f32_to_bf16_bits(a.astype(np.float32)) for a in (rng.standard_normal((M, K)), rng.standard_normal((M, K)),
+                                                                   1 + 0.3 * rng.standard_normal(K))]
+    xb, rb, wb = (a.copy() for a in clean)
+    src = rb if residual else xb
+    src[0] = 0x7FC0                                    # NaN all over
+    src[2, K // 2] = 0x7FC0
+    src[3, K - 1] = 0x7F80                             # inf
+    bad = [0, 2, 3]
+    good = np.setdiff1d(np.arange(M), bad)
+
+    def args(x, r, w):
+        return (bf16_to_gpu(x), bf16_to_gpu(w)), dict(eps=EPS, residual=bf16_to_gpu(r) if residual else None)
+
+    (x, w), kw = args(xb, rb, wb)
+    (x0, w0), kw0 = args(*clean)
+    with np.errstate(invalid="ignore"):
+        y64, _ = layer.rms_norm(bits_to_f64(xb), bits_to_f64(wb), EPS, bits_to_f64(rb) if residual else None)
+    first = lambda got: got[0] if isinstance(got, tuple) else got
+    y, y0 = first(qlq.rms_norm(x, w, **kw)), first(qlq.rms_norm(x0, w0, **kw0))
+    got = bits_to_f64(bf16_bits(y))
+    assert np.array_equal(np.isnan(got), np.isnan(y64)) and not got[3, :K - 1].any()
+    assert torch.equal(y[good], y0[good])
+    for qtype, top in (("int8", 127.0), ("fp8_e4m3fn", 448.0)):
+        c, s = qlq.rms_norm_quant_dynamic(x, w, qtype, **kw)[:2]
+        c0, s0 = qlq.rms_norm_quant_dynamic(x0, w0, qtype, **kw0)[:2]
+        assert bool(torch.isnan(s[bad]).all()), f"{qtype}: scales {s[bad].tolist()}"
+        assert torch.equal(c[good], c0[good]) and torch.equal(s[good], s0[good])
+        z, z0 = (first(qlq.rms_norm_quant_static(a, b, 0.01, qtype, **k)) for a, b, k in ((x, w, kw), (x0, w0, kw0)))
+        assert torch.equal(z[good], z0[good])
+        # (a static scale has no place for a NaN: its codes saturate, as the activation quantizers' do)
+        v = codes(z)[[0, 2]]
+        v = v.view(np.int8).astype(np.float64) if qtype == "int8" else oracle.e4m3fn_decode(v).astype(np.float64)
+        assert np.all(np.abs(v) == top)
+    # a NaN in the weight is every row's
+    wb = clean[2].copy()
+    wb[K // 3] = 0x7FC0
+    (x, w), kw = args(clean[0], clean[1], wb)
+    assert np.array_equal(np.isnan(bits_to_f64(bf16_bits(first(qlq.rms_norm(x, w, **kw))))).any(0), np.arange(K) == K // 3)
+    assert bool(torch.isnan(qlq.rms_norm_quant_dynamic(x, w, "int8", **kw)[1]).all())

@@ -46,8 +46,11 @@ __device__ __forceinline__ double wave_sum(double v) {
   return v;
 }
 
+// The larger one; NaN if either is (a row with a NaN keeps it in its scale).
+__device__ __forceinline__ float most_of(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 __device__ __forceinline__ float wave_absmax(float v) {
-  for (int off = 32; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
+  for (int off = 32; off > 0; off >>= 1) v = most_of(v, __shfl_xor(v, off, 64));
   return v;
 }
 
@@ -94,7 +97,7 @@ __device__ __forceinline__ void row_reduce(double& v, float& w, RowPart* red) {
     __syncthreads();
     v = red[0].sum, w = red[0].most;
 #pragma unroll
-    for (int k = 1; k < T / 64; ++k) v += red[k].sum, w = fmaxf(w, red[k].most);
+    for (int k = 1; k < T / 64; ++k) v += red[k].sum, w = most_of(w, red[k].most);
   }
 }
 
@@ -161,7 +164,7 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void rms_norm_kernel(NormArgs a)
       h[c][2 * e] *= bf16_bits_to_f32(wd[e] & 0xFFFF);
       h[c][2 * e + 1] *= bf16_bits_to_f32(wd[e] >> 16);
       if constexpr (OUT == kNormDynamic)
-        am = fmaxf(am, fmaxf(fabsf(h[c][2 * e]), fabsf(h[c][2 * e + 1])));
+        am = most_of(am, most_of(fabsf(h[c][2 * e]), fabsf(h[c][2 * e + 1])));
     }
   }
   row_reduce<T, OUT == kNormDynamic>(ss, am, red);
@@ -207,7 +210,7 @@ __global__ __launch_bounds__(256) void rms_norm_any_kernel(NormArgs a) {
   for (int k = t; k < a.K; k += 256) {
     const float v = load(k);
     ss = __builtin_fma((double)v, (double)v, ss);
-    if constexpr (OUT == kNormDynamic) am = fmaxf(am, fabsf(v * bf16_bits_to_f32(a.w[k])));
+    if constexpr (OUT == kNormDynamic) am = most_of(am, fabsf(v * bf16_bits_to_f32(a.w[k])));
   }
   row_reduce<256, OUT == kNormDynamic>(ss, am, red);
   const double rho = rho_of(ss, a.K, a.eps), qmax = a.fp8 ? 448.0 : 127.0;
