@@ -370,7 +370,8 @@ qlq_status qlq_kv_gather(const void* k_codes, const void* k_scales, const void* 
  * 64, 96, 128, 192 or 256; page_size a power of two, 16 .. 2^20; pool a multiple of it.  block_table int32
  * [B, max_pages], seq_lens int32 [B], q_start int32 [B + 1], on the device: lengths are read there
  * (the host does not wait for them) and bounded by 0 .. max_pages * page_size and 0 .. T; a token
- * whose page is outside the pool is left out, never read.
+ * whose page is outside the pool is left out, never read, and entries that no query of its
+ * sequence sees (behind the last query, before the first one's window) may hold anything.
  * workspace: qlq_kv_attention_workspace_bytes(...), 256-byte aligned, zero-filled before its
  * first use and left so for the next call; it serves this operator's calls only, one stream at
  * a time. */

@@ -11,6 +11,7 @@ import torch
 
 import oracle
 import weight_quantized_linear_qlinear_amd as qlq
+from oracle.layer import slots_of
 from tests.gpu_util import bf16_bits, bf16_to_gpu, bits_to_f64, dev
 from tests.test_gpu_attention import Problem
 
@@ -49,7 +50,7 @@ def test_tail_far_below_the_largest_weight(BL, heads, octaves):
     lens = torch.full((B,), L, dtype=torch.int32, device=dev())
     cache = qlq.QuantizedKV(_gpu(kc, torch.int8), _gpu(ks, torch.float16), _gpu(vc, torch.uint8), _gpu(vs, torch.float16))
     lse = torch.zeros(B, Hq, device=dev())
-    out = qlq.kv_attention(bf16_to_gpu(np.broadcast_to(qb, (B, Hq, D))), cache, table, lens, page, scale=1.0, lse=lse)
+    out = qlq.kv_attention(bf16_to_gpu(np.tile(qb, (B, 1, 1))), cache, table, lens, page, scale=1.0, lse=lse)
     k = kc.astype(np.float64) * 2.0 ** -6
     v = oracle.e4m3fn_decode(vc).astype(np.float64) * 2.0 ** -8
     q64 = bits_to_f64(qb)
@@ -84,3 +85,23 @@ def test_a_query_with_nan_is_nan_in_its_own_row_alone(case):
             assert bool(torch.isnan(out[t, h]).all()) and bool(torch.isnan(lse[t, h])), what
             out[t, h], lse[t, h] = out0[t, h], lse0[t, h]
         assert torch.equal(out, out0) and torch.equal(lse, lse0), what
+
+
+@pytest.mark.parametrize("window", [1, 5, 40, 333])
+@pytest.mark.parametrize("nqs", [(1, 1, 1), (3, 1, 9), (150, 64, 80)])
+def test_entries_before_the_window_may_hold_anything(nqs, window):
+    # what no query can see any more (a page that its owner gave back may be another's, half written) changes nothing
+    lens = [n + e for n, e in zip(nqs, (700, 1003, 90))]
+    print(f"entries before the window nqs={nqs} window={window}", flush=True)
+    for Hq, Hk, D in ((4, 2, 64), (2, 1, 96), (4, 1, 128), (2, 1, 256)):
+        p = Problem(sum(nqs) + D + window, nqs, lens, Hq, Hk, D, 16, each=max(nqs) == 1)
+        out = p.check(window=window, what="before")
+        lse, lse2 = torch.zeros(p.T, Hq, device=dev()), torch.zeros(p.T, Hq, device=dev())
+        p.run(window=window, lse=lse)
+        for b, (n, L) in enumerate(zip(nqs, lens)):
+            gone = slots_of(p.table[b], max(0, L - n - window + 1), 16, p.pool)
+            at = torch.from_numpy(gone).to(dev())
+            p.cache.k_codes[at], p.cache.v_codes[at] = 127, 0x7F
+            p.cache.k_scales[at], p.cache.v_scales[at] = float("nan"), float("nan")
+        same = torch.equal(p.run(window=window, lse=lse2), out) and torch.equal(lse2, lse)
+        assert same, (Hq, Hk, D)

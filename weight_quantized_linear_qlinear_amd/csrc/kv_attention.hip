@@ -226,7 +226,8 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv_attention_kernel(KvAttnA
   const int i0 = r0 / a.G, i1 = min(nq - 1, (r0 + TR - 1) / a.G);
   const int p0 = L - nq;                                     // position of query 0
   const int tend = min(max(a.causal ? p0 + i1 + 1 : L, 0), L);
-  const int tbeg = a.window > 0 ? min(max(0, p0 + i0 - a.window + 1), tend) & ~31 : 0;
+  const int tmin = a.window > 0 ? min(max(0, p0 + i0 - a.window + 1), tend) : 0;      // the first token that a row sees
+  const int tbeg = tmin & ~31;
   const int begin = begin_of(a, it.e);
   const int c0 = max(tbeg, begin + 32 * (u - it.begin));              // a multiple of 32
   const int c1 = min(tend, begin + 32 * (u_next - it.begin));
@@ -352,14 +353,15 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv_attention_kernel(KvAttnA
   }
 
   for (int base = c0; base < c1; base += 32) {
-    const bool all_valid = e0 >= 0 && e1 >= 0 && base + 32 <= c1;
+    const bool all_valid = e0 >= 0 && e1 >= 0 && base >= tmin && base + 32 <= c1;
     const int n0 = entry_of(g0, base + 32), n1 = entry_of(g1, base + 48);
     const int t0 = base + 4 * g4;                            // this lane's first token (u = j = 0)
-    auto there = [&](int u, int j) { return (u ? e1 : e0) >= 0 && t0 + 16 * u + j < c1; };
+    // (tokens before every row's window are left out like those of a bad page: their entries may hold anything)
+    auto there = [&](int u, int j) { return (u ? e1 : e0) >= 0 && t0 + 16 * u + j >= tmin && t0 + 16 * u + j < c1; };
     // V scales into the exponent.  A scale of zero (an entry never written) counts as the
     // smallest one: its codes are zero too.  Tokens that are not there count as scale 1.
     if (lane < 32) {
-      const bool in = all_valid || ((lane & 16 ? e1 : e0) >= 0 && base + lane < c1);
+      const bool in = all_valid || ((lane & 16 ? e1 : e0) >= 0 && base + lane >= tmin && base + lane < c1);
       const float sv = in ? fmaxf(f16_lo(vsr), 0x1p-24f) : 1.0f;
       mine.lv[lane] = __builtin_amdgcn_logf(sv);
       mine.rv[lane] = __builtin_amdgcn_rcpf(sv);

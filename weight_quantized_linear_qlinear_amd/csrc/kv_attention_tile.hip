@@ -59,6 +59,7 @@ constexpr float kLift = 7.0f, kSlack = 15.0f;
 // A query tile's tokens: those that its rows can see.
 struct Span {
   int i0, i1;                    // first and last query token
+  int first;                     // the first token that a row sees
   int begin, end;                // tokens, begin a multiple of T
 };
 
@@ -69,7 +70,8 @@ __device__ __forceinline__ Span span_of(const KvAttnArgs& a, const Extent& e, in
   s.i1 = min(e.nq - 1, (qt * kTileRows + kTileRows - 1) / a.G);
   const int p0 = e.L - e.nq;
   s.end = min(max(a.causal ? p0 + s.i1 + 1 : e.L, 0), e.L);
-  s.begin = a.window > 0 ? min(max(0, p0 + s.i0 - a.window + 1), s.end) & ~(T - 1) : 0;
+  s.first = a.window > 0 ? min(max(0, p0 + s.i0 - a.window + 1), s.end) : 0;
+  s.begin = s.first & ~(T - 1);
   return s;
 }
 
@@ -336,7 +338,8 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
       skr = a.k_scales[at64 * NG + sblock];
     };
     auto stat_write = [&](int n) {
-      const bool there = entry_of(st_page, st_t) >= 0 && st_t + srow < c1;
+      // (tokens before every row's window are left out like those of a bad page: their entries may hold anything)
+      const bool there = entry_of(st_page, st_t) >= 0 && st_t + srow >= sp.first && st_t + srow < c1;
       const uint32_t kb = there ? skr & 0x7FFF : 0u, vb = there ? max(svr & 0x7FFF, 1u) : 0u;
       uint32_t top = across16(row16(kb | vb << 16, MaxU16()), MaxU16());
       if (__ballot(!there)) top |= 0x8000u;
