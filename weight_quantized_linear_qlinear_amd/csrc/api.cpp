@@ -1028,7 +1028,10 @@ qlq_status qlq_kv_attention(const void* q, int64_t q_stride, int64_t T, int64_t 
     return fail(QLQ_ERR_INVALID_ARG, "misaligned pointer");
   const qlq::KvAttnPlan p = qlq::plan_kv_attention(T, B, Hk, Hq / Hk, D, q_start == nullptr);
   const size_t partial = attn_partial_bytes(p, Hk, D), need = kAttnCounterBytes + partial;
-  if (p.tiles * (max_pages * page_size / 32 + 1) >= (int64_t(1) << 31) || partial >= ((size_t)1 << 31) ||
+  // The kernels count units (32 tokens of a query tile) and a sequence's query rows in 32 bits, units
+  // up to one for every wave past the last.
+  if (p.tiles * (max_pages * page_size / 32 + 1) + p.waves >= (int64_t(1) << 31) ||
+      T * (Hq / Hk) >= (int64_t(1) << 31) - 256 || partial >= ((size_t)1 << 31) ||
       (size_t)p.counters * 12 > kAttnCounterBytes || p.waves > 4096)
     return fail(QLQ_ERR_UNSUPPORTED, "sizes too large for one call");
   if (!workspace || workspace_bytes < need)
