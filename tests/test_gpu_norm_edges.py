@@ -60,3 +60,22 @@ def test_nan_and_infinite_rows(MK, residual):
     (x, w), kw = args(clean[0], clean[1], wb)
     assert np.array_equal(np.isnan(bits_to_f64(bf16_bits(first(qlq.rms_norm(x, w, **kw))))).any(0), np.arange(K) == K // 3)
     assert bool(torch.isnan(qlq.rms_norm_quant_dynamic(x, w, "int8", **kw)[1]).all())
+
+
+def test_as_many_rows_as_are_allowed():
+    # 2^24 rows: a workgroup for each would be more threads than one launch can have
+    M, K, part = 1 << 24, 3, 1 << 20
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x, r = (torch.randn(M, K, generator=g, device="cuda").bfloat16() for _ in range(2))
+    w = torch.randn(K, generator=g, device="cuda").bfloat16()
+    y, h = qlq.rms_norm(x, w, EPS, residual=r)
+    c, s, h2 = qlq.rms_norm_quant_dynamic(x, w, "int8", EPS, residual=r)
+    z = qlq.rms_norm_quant_static(x, w, 0.02, "fp8_e4m3fn", EPS)
+    same = torch.equal(h, h2)
+    for a in range(0, M, part):
+        b = slice(a, a + part)
+        y1, h1 = qlq.rms_norm(x[b], w, EPS, residual=r[b])
+        c1, s1, _ = qlq.rms_norm_quant_dynamic(x[b], w, "int8", EPS, residual=r[b])
+        same &= torch.equal(y[b], y1) and torch.equal(h[b], h1) and torch.equal(c[b], c1) and torch.equal(s[b], s1)
+        same &= torch.equal(z[b], qlq.rms_norm_quant_static(x[b], w, 0.02, "fp8_e4m3fn", EPS))
+    assert same

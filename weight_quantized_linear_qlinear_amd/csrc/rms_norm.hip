@@ -259,11 +259,23 @@ hipError_t launch_rms_norm(const void* x, const void* residual, const void* w, i
              y, y_scale, static_cast<uint16_t*>(residual_out), M, K, eps, input_scale, qtype == kFp8 ? 1 : 0};
   const bool vec = K % 8 == 0 && al(x, 16) && al(residual, 16) && al(w, 16) && al(residual_out, 16) &&
                    al(y, out == kNormBf16 ? 16 : 8);
-  switch (out) {
-    case kNormBf16: return launch_norm<kNormBf16>(a, vec, st);
-    case kNormStatic: return launch_norm<kNormStatic>(a, vec, st);
-    default: return launch_norm<kNormDynamic>(a, vec, st);
+  // A launch's threads are counted in 32 bits: at most 2^21 rows (of up to 1024 threads) at a time.
+  constexpr int kRows = 1 << 21;
+  for (int m = 0; m < M; m += kRows) {
+    NormArgs b = a;
+    const int64_t at = (int64_t)m * K;
+    b.M = M - m < kRows ? M - m : kRows;
+    b.x = a.x + at;
+    if (a.res) b.res = a.res + at;
+    if (a.res_out) b.res_out = a.res_out + at;
+    b.y = static_cast<uint8_t*>(a.y) + (out == kNormBf16 ? 2 : 1) * at;
+    if (a.y_scale) b.y_scale = a.y_scale + m;
+    const hipError_t e = out == kNormBf16   ? launch_norm<kNormBf16>(b, vec, st)
+                         : out == kNormStatic ? launch_norm<kNormStatic>(b, vec, st)
+                                              : launch_norm<kNormDynamic>(b, vec, st);
+    if (e != hipSuccess) return e;
   }
+  return hipSuccess;
 }
 
 }  // namespace qlq
