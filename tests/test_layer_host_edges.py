@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import weight_quantized_linear_qlinear_amd as qlq
+from weight_quantized_linear_qlinear_amd import binding
 
 FAKE = ctypes.c_void_p(0x10000)          # aligned, never dereferenced: refused before any launch
 
@@ -25,3 +26,20 @@ def test_attention_refuses_sizes_that_32_bits_cannot_count():
     assert _attention(B, B, 1, 1, 128, units - 1, 32, None)[0] == 2
     # a sequence's query rows (tokens x heads of the group)
     assert _attention(1 << 21, 1, 1024, 1, 32, 1, 32, FAKE)[0] == 2
+
+
+def test_attention_workspaces_of_many_streams_are_not_kept_for_ever(monkeypatch):
+    # a program that makes a stream per request: the workspaces kept are those of the latest streams
+    stream = [0]
+    monkeypatch.setattr(binding, "_raw_stream", lambda index: stream[0])
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(binding, "_attention_workspaces", {})
+    cpu = torch.device("cpu")
+    for stream[0] in range(1000):
+        ws = binding._attention_workspace(cpu, 300000)
+        assert ws.numel() == 300000 and not ws[:262144].any()
+        assert binding._attention_workspace(cpu, 290000) is ws
+        big = binding._attention_workspace(cpu, 310000)                # grown: in place of the smaller one
+        assert big.numel() == 310000 and binding._attention_workspace(cpu, 300000) is big
+    kept = binding._attention_workspaces
+    assert len(kept) <= 64 and list(kept)[-1] == (None, 999)

@@ -812,12 +812,14 @@ def kv_attention_workspace_bytes(T: int, B: int, Hq: int, Hk: int, D: int, one_e
 
 
 _ATTENTION_COUNTER_BYTES = 262144
+_ATTENTION_STREAMS = 40                  # workspaces kept: torch's 32 pooled streams, the default one, some of a user's
 _attention_workspaces: dict = {}
 
 
 def _attention_workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
     """A workspace of this stream with its counters zeroed, grown on demand; inside a graph capture, one of the
-    graph's own (its zero fill is recorded with it), so that graphs and streams never share one."""
+    graph's own (its zero fill is recorded with it), so that graphs and streams never share one.  The oldest
+    goes when there are many (its memory returns to the allocator's pool of its stream, in that stream's order)."""
     capturing = torch.cuda.is_current_stream_capturing()
     key = (dev.index, _raw_stream(dev.index))
     ws = None if capturing else _attention_workspaces.get(key)
@@ -825,7 +827,11 @@ def _attention_workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         ws[:_ATTENTION_COUNTER_BYTES].zero_()
         if not capturing:
-            _attention_workspaces[key] = ws
+            with _lock:
+                _attention_workspaces.pop(key, None)
+                while len(_attention_workspaces) >= _ATTENTION_STREAMS:
+                    del _attention_workspaces[next(iter(_attention_workspaces))]
+                _attention_workspaces[key] = ws
     return ws
 
 
