@@ -105,3 +105,22 @@ def test_entries_before_the_window_may_hold_anything(nqs, window):
             p.cache.k_scales[at], p.cache.v_scales[at] = float("nan"), float("nan")
         same = torch.equal(p.run(window=window, lse=lse2), out) and torch.equal(lse2, lse)
         assert same, (Hq, Hk, D)
+
+
+MANY = [  # query tokens of each sequence (8 heads of 32 over one KV head: a tile of 256 rows is 32 of them)
+    ("one sequence of 67 tiles", (2129,)),
+    ("65 tiles and a bit, then more", (2080, 1, 0, 37)),
+    ("64 tiles end with a sequence", (1024, 1000, 24, 0, 33, 2)),
+    ("sequences across the 64th tile", (40, 1500, 0, 700, 3, 64)),
+    ("70 sequences", tuple(9 + b % 5 for b in range(70))),
+    ("131 sequences, some empty, one long", tuple(0 if b % 7 == 3 else 12 + b % 3 for b in range(130)) + (900,))]
+
+
+@pytest.mark.parametrize("window", [0, 100])
+@pytest.mark.parametrize("case", MANY, ids=[c[0] for c in MANY])
+def test_many_query_tiles_and_sequences(case, window):
+    what, nqs = case
+    lens = [n + (b * 13) % 50 for b, n in enumerate(nqs)]
+    print(f"many tiles: {what}, window {window}", flush=True)
+    p = Problem(sum(nqs) + window, nqs, lens, 8, 1, 32, 16, each=False)
+    p.check(window=window, what=what)
