@@ -79,3 +79,49 @@ def test_as_many_rows_as_are_allowed():
         same &= torch.equal(y[b], y1) and torch.equal(h[b], h1) and torch.equal(c[b], c1) and torch.equal(s[b], s1)
         same &= torch.equal(z[b], qlq.rms_norm_quant_static(x[b], w, 0.02, "fp8_e4m3fn", EPS))
     assert same
+
+
+U = 2.0 ** -24
+
+
+@pytest.mark.parametrize("MK", [(1152, 4096), (128, 16384), (128, 65536), (128, 65544), (128, 5001)])
+def test_norm_with_a_residual_to_the_last_rounding(MK):
+    # With fp64 sums what is left are single fp32 roundings (u = 2^-24): h, h w, the row's largest |h w| (the same two),
+    # the factor (h's, halved by the root, so at most u) and the last product.  The scale is off by 4 u at most (h, h w,
+    # rho, its own), a quotient before its rounding by 4 u (static) or 5 u (dynamic), y by 6 u (rho is rounded for it).
+    # Every row holds one value, which is where a sum in fp32 would drift (16 u in 64 adds for some of these, 40 u in
+    # 256, half of that in the scale); rows from 128 on are random.
+    M, K = MK
+    print(f"norm to the last rounding M={M} K={K}", flush=True)
+    rng = np.random.default_rng(K)
+    x, r = rng.standard_normal((M, K)), 3.0 * rng.standard_normal((M, K))
+    xb, rb, wb = (oracle.f32_to_bf16_bits(a.astype(np.float32)) for a in (x, r, 1 + 0.3 * rng.standard_normal(K)))
+    xb[:128] = (0x3F80 + np.arange(128, dtype=np.uint16))[:, None]
+    rb[:128] = 0x3C01
+    x, r, w = (bits_to_f64(a) for a in (xb, rb, wb))
+    y64, h64 = layer.rms_norm(x, w, EPS, r)
+    xg, rg, wg = (bf16_to_gpu(a) for a in (xb, rb, wb))
+    near = 1 + 2.0 ** -10
+
+    def beyond(code, quotient, qtype, steps, qmax):
+        """Codes on the other side of a rounding border by more than `steps` u of the quotient."""
+        if qtype == "int8":
+            over = np.abs(quotient - code.view(np.int8)) - 0.5 - steps * U * near * np.abs(quotient)
+        else:
+            step = 2.0 ** np.maximum(np.floor(np.log2(np.maximum(np.abs(quotient), 2.0 ** -20))) - 3, -9)
+            over = (np.abs(quotient - oracle.e4m3fn_decode(code)) - steps * U * near * np.abs(quotient)) / step - 0.5
+        return int(((over > 2.0 ** -40) & (np.abs(quotient) <= qmax)).sum())
+
+    y, h = qlq.rms_norm(xg, wg, EPS, residual=rg)
+    assert np.all(np.abs(bits_to_f64(bf16_bits(y)) - y64) <= (2.0 ** -8 + 6 * U * near) * np.abs(y64))
+    assert np.all(np.abs(bits_to_f64(bf16_bits(h)) - h64) <= (2.0 ** -8 + U * near) * np.abs(h64))
+    for qtype, qmax in (("int8", 127.0), ("fp8_e4m3fn", 448.0)):
+        c, s, h2 = qlq.rms_norm_quant_dynamic(xg, wg, qtype, EPS, residual=rg)
+        s64 = np.abs(y64).max(1) / qmax
+        off = np.abs(s.cpu().numpy().astype(np.float64) / s64 - 1) / U
+        assert off.max() <= 4 * near, f"{qtype}: scale off by {off.max():.2f} u in row {off.argmax()}"
+        assert beyond(codes(c), y64 / s64[:, None], qtype, 5, qmax) == 0
+        s_in = np.float32(np.abs(y64).max() / qmax)
+        z, h3 = qlq.rms_norm_quant_static(xg, wg, float(s_in), qtype, EPS, residual=rg)
+        assert beyond(codes(z), y64 / np.float64(s_in), qtype, 4, qmax) == 0
+        assert torch.equal(h2, h) and torch.equal(h3, h)
