@@ -299,15 +299,16 @@ qlq_status qlq_kv_dequantize(const void* k_codes, const void* k_scales, const vo
  *   y = h / sqrt(mean_k(h^2) + eps) * weight   (fp32)  ->  y_bf16 = bf16(y)
  * x, residual, residual_out, y bf16 [M, K]; weight bf16 [K].  residual may be NULL (then
  * residual_out must be NULL too), residual_out may be NULL.  y and residual_out may be the
- * same buffers as x or residual (not each other).  eps > 0.  |h| below 2^60 (its square is summed in fp32). */
+ * same buffers as x or residual (not each other).  eps > 0.  Squares are summed in fp64: any
+ * h whose product with its weight is finite in fp32 will do. */
 qlq_status qlq_rms_norm(const void* x_bf16, const void* residual_bf16, const void* weight_bf16, int64_t M, int64_t K,
                         float eps, void* y_bf16, void* residual_out_bf16, hipStream_t stream);
 
 /* The same norm, written as the codes of a static or dynamic W8A8 linear's input:
  *   static:  yq = sat(round-to-nearest-even(y / input_scale))
  *   dynamic: y_scale[m] = absmax_k |y[m,k]| / qmax (1 for an all-zero row), yq by it
- * with qmax 127 (INT8) or 448 (e4m3fn).  y is the fp32 value (not rounded to bf16 first) and the
- * quotient is fp32 to within one unit in the last place.  A row with a NaN or an infinity has a NaN
+ * with qmax 127 (INT8) or 448 (e4m3fn).  y is not rounded to bf16 first; what is rounded to a
+ * code is within 5 2^-24 of the exact quotient (relative).  A row with a NaN or an infinity has a NaN
  * scale; a code cannot hold one and saturates.  yq [M, K] one byte per code, not overlapping any
  * input; y_scale fp32 [M] (device).  residual_out as above. */
 qlq_status qlq_rms_norm_quant_static(const void* x_bf16, const void* residual_bf16, const void* weight_bf16, int64_t M,

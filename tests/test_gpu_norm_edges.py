@@ -125,3 +125,19 @@ def test_norm_with_a_residual_to_the_last_rounding(MK):
         z, h3 = qlq.rms_norm_quant_static(xg, wg, float(s_in), qtype, EPS, residual=rg)
         assert beyond(codes(z), y64 / np.float64(s_in), qtype, 4, qmax) == 0
         assert torch.equal(h2, h) and torch.equal(h3, h)
+
+
+@pytest.mark.parametrize("MK", [(21, 512), (1029, 1000), (21, 20000), (21, 77)])
+def test_rows_of_every_magnitude(MK):
+    # rows from 2^-100 (eps outweighs them) to 2^120: their squares leave fp32's range, the output does not
+    M, K = MK
+    rng = np.random.default_rng(M + K)
+    gain = 2.0 ** np.linspace(-100, 120, M)[:, None]
+    xb, wb = (oracle.f32_to_bf16_bits(a.astype(np.float32)) for a in (gain * rng.standard_normal((M, K)), 1 + 0.3 * rng.standard_normal(K)))
+    y64, _ = layer.rms_norm(bits_to_f64(xb), bits_to_f64(wb), EPS)
+    x, w = bf16_to_gpu(xb), bf16_to_gpu(wb)
+    y = bits_to_f64(bf16_bits(qlq.rms_norm(x, w, EPS)))
+    assert np.all(np.abs(y - y64) <= (2.0 ** -8 + 8 * U) * np.abs(y64))
+    s = qlq.rms_norm_quant_dynamic(x, w, "int8", EPS)[1].cpu().numpy().astype(np.float64)
+    s64 = np.abs(y64).max(1) / 127.0
+    assert np.all(np.abs(s - s64) <= 4 * U * s64)
