@@ -98,13 +98,14 @@ def test_entries_before_the_window_may_hold_anything(nqs, window):
         out = p.check(window=window, what="before")
         lse, lse2 = torch.zeros(p.T, Hq, device=dev()), torch.zeros(p.T, Hq, device=dev())
         p.run(window=window, lse=lse)
-        for b, (n, L) in enumerate(zip(nqs, lens)):
-            gone = slots_of(p.table[b], max(0, L - n - window + 1), 16, p.pool)
-            at = torch.from_numpy(gone).to(dev())
-            p.cache.k_codes[at], p.cache.v_codes[at] = 127, 0x7F
-            p.cache.k_scales[at], p.cache.v_scales[at] = float("nan"), float("nan")
-        same = torch.equal(p.run(window=window, lse=lse2), out) and torch.equal(lse2, lse)
-        assert same, (Hq, Hk, D)
+        for scale in (float("nan"), float("inf")):
+            for b, (n, L) in enumerate(zip(nqs, lens)):
+                gone = slots_of(p.table[b], max(0, L - n - window + 1), 16, p.pool)
+                at = torch.from_numpy(gone).to(dev())
+                p.cache.k_codes[at], p.cache.v_codes[at] = 127, 0x7F
+                p.cache.k_scales[at], p.cache.v_scales[at] = scale, scale
+            same = torch.equal(p.run(window=window, lse=lse2), out) and torch.equal(lse2, lse)
+            assert same, (Hq, Hk, D, scale)
 
 
 MANY = [  # query tokens of each sequence (8 heads of 32 over one KV head: a tile of 256 rows is 32 of them)
