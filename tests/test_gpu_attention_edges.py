@@ -125,3 +125,41 @@ def test_many_query_tiles_and_sequences(case, window):
     print(f"many tiles: {what}, window {window}", flush=True)
     p = Problem(sum(nqs) + window, nqs, lens, 8, 1, 32, 16, each=False)
     p.check(window=window, what=what)
+
+
+@pytest.mark.parametrize("nqs", [(1, 1, 1), (90, 40)])
+def test_lengths_and_tables_that_the_graph_itself_changes(nqs):
+    # a captured step that first advances the lengths and swaps in the next step's block table, both on the device
+    lens = [n + e for n, e in zip(nqs, (200, 900, 37))]
+    p = Problem(sum(nqs), nqs, [L + 8 for L in lens], 4, 1, 128, 16, each=max(nqs) == 1)
+    other = Problem(sum(nqs) + 1, nqs, [L + 8 for L in lens], 4, 1, 128, 16, each=max(nqs) == 1)
+    first = torch.tensor(lens, dtype=torch.int32, device=dev())
+    pages = p.pool // 16                               # two tables over one pool: the second one's pages behind
+    assert other.pool == p.pool and other.bt.shape == p.bt.shape
+    c = [torch.cat(t) for t in zip(*((q.cache.k_codes, q.cache.k_scales, q.cache.v_codes, q.cache.v_scales) for q in (p, other)))]
+    cache = qlq.QuantizedKV(*c)
+    own = (other.bt >= 0) & (other.bt < pages)
+    tables = [torch.where((p.bt >= 0) & (p.bt < pages), p.bt, -1), torch.where(own, other.bt + pages, -1)]
+    both, step = torch.stack(tables), torch.zeros(1, dtype=torch.int64, device=dev())
+    sl, bt = first.clone(), tables[0].clone()
+    out, lse = torch.empty_like(p.q), torch.empty(p.T, 4, device=dev())
+
+    def body():
+        step.add_(1)
+        sl.add_(1)
+        bt.copy_(both[step % 2][0])
+        qlq.kv_attention(p.q, cache, bt, sl, 16, q_start=p.q0, out=out, lse=lse)
+
+    body()                                             # (set-up outside the capture)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        body()
+    step.zero_()
+    sl.copy_(first)
+    for n in range(1, 9):
+        want_lse = torch.empty_like(lse)
+        want = qlq.kv_attention(p.q, cache, tables[n % 2], first + n, 16, q_start=p.q0, lse=want_lse)
+        out.zero_()
+        g.replay()
+        same = torch.equal(out, want) and torch.equal(lse, want_lse)
+        assert same, n
