@@ -216,322 +216,323 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv_attention_kernel(KvAttnA
   const int total = total_units<TR>(a, mine_e, lane);
   const int U = max(1, (total + a.parts * TS - 1) / (a.parts * TS)), u_end = min(total, (me + 1) * U);
   for (int u = me * U; u < u_end;) {
-  const Tile it = tile_of<TR>(a, mine_e, u, lane);
-  if (it.units == 0) break;                                  // (only if lengths change meanwhile or overflow the sum)
-  const int u_next = min(u_end, it.begin + it.units);
-  // This tile's chunks: one per wave that its units reach
-  const int wf = it.begin / U;
-  const Chunks ck{wf, (it.begin + it.units - 1) / U - wf + 1, me - wf};
-  const int nq = it.e.nq, L = it.e.L, r0 = it.qt * TR, rows = nq * a.G;
-  const int i0 = r0 / a.G, i1 = min(nq - 1, (r0 + TR - 1) / a.G);
-  const int p0 = L - nq;                                     // position of query 0
-  const int tend = min(max(a.causal ? p0 + i1 + 1 : L, 0), L);
-  const int tmin = a.window > 0 ? min(max(0, p0 + i0 - a.window + 1), tend) : 0;      // the first token that a row sees
-  const int tbeg = tmin & ~31;
-  const int begin = begin_of(a, it.e);
-  const int c0 = max(tbeg, begin + 32 * (u - it.begin));              // a multiple of 32
-  const int c1 = min(tend, begin + 32 * (u_next - it.begin));
-  u = u_next;
+    const Tile it = tile_of<TR>(a, mine_e, u, lane);
+    if (it.units == 0) break;                                  // (only if lengths change meanwhile or overflow the sum)
+    const int u_next = min(u_end, it.begin + it.units);
+    // This tile's chunks: one per wave that its units reach
+    const int wf = it.begin / U;
+    const Chunks ck{wf, (it.begin + it.units - 1) / U - wf + 1, me - wf};
+    const int nq = it.e.nq, L = it.e.L, r0 = it.qt * TR, rows = nq * a.G;
+    const int i0 = r0 / a.G, i1 = min(nq - 1, (r0 + TR - 1) / a.G);
+    const int p0 = L - nq;                                     // position of query 0
+    const int tend = min(max(a.causal ? p0 + i1 + 1 : L, 0), L);
+    const int tmin = a.window > 0 ? min(max(0, p0 + i0 - a.window + 1), tend) : 0;      // the first token that a row sees
+    const int tbeg = tmin & ~31;
+    const int begin = begin_of(a, it.e);
+    const int c0 = max(tbeg, begin + 32 * (u - it.begin));              // a multiple of 32
+    const int c1 = min(tend, begin + 32 * (u_next - it.begin));
+    u = u_next;
 
-  int c16 = lane & 15, g4 = lane >> 4;
-  asm volatile("" : "+v"(c16), "+v"(g4));                    // (nothing computed from them outlives a tile)
-  // Channels of a group that lane group g4 holds of K and q: 8 g4 on, or (two groups loaded at
-  // once, 16 bytes per lane, and their halves swapped between the wave's halves) kq on.
-  const int kq = ((g4 & 1) << 4) | ((g4 >> 1) << 3);
+    int c16 = lane & 15, g4 = lane >> 4;
+    asm volatile("" : "+v"(c16), "+v"(g4));                    // (nothing computed from them outlives a tile)
+    // Channels of a group that lane group g4 holds of K and q: 8 g4 on, or (two groups loaded at
+    // once, 16 bytes per lane, and their halves swapped between the wave's halves) kq on.
+    const int kq = ((g4 & 1) << 4) | ((g4 >> 1) << 3);
 
-  // q's rows (packed: query token, then head of the group); their first use is further down.
-  u32x4 qraw[R][NG];
-  int qpos[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const int row = r0 + 16 * r + c16;
-    const bool live = row < rows;
-    const int i = live ? row / a.G : i0, g = live ? row - i * a.G : 0;
-    qpos[r] = live ? p0 + i : -1;
-    const uint16_t* qp = a.q + (int64_t)(it.e.qs + i) * a.q_stride + (int64_t)(h * a.G + g) * D + (NG % 2 == 0 ? kq : 8 * g4);
-#pragma unroll
-    for (int n = 0; n < NG; ++n) qraw[r][n] = ld16(qp + 32 * n);
-  }
-
-  f32x4 o[2 * NG][R];
-  float m[R], l[R];
-#pragma unroll
-  for (int n = 0; n < 2 * NG; ++n)
-#pragma unroll
-    for (int r = 0; r < R; ++r) o[n][r] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int r = 0; r < R; ++r) m[r] = kNegInf, l[r] = 0.0f;
-
-  const int hk = a.Hk, page_mask = (1 << a.page_shift) - 1;
-  typedef Pieces<NG> P1;
-  typedef Pieces<(P1::Rest > 0 ? P1::Rest : 1)> P2;          // NG <= 8, no 7: at most two pieces
-  constexpr int RB1 = 2 * P1::P, RB2 = 2 * P2::P;
-  constexpr bool kTwo = P1::Rest > 0;
-  static_assert(!kTwo || P2::Rest == 0, "two pieces at most");
-
-  // Tiles start at multiples of 32 tokens and pages hold 16 or more, so each half of a tile lies
-  // in one page: its first entry is uniform, and all addresses are a uniform base plus an offset
-  // that a lane keeps.  -1: the page is outside the pool (its tokens are left out).
-  const ConstInt* table = (const ConstInt*)(uintptr_t)(a.block_table + (int64_t)it.b * a.max_pages);
-  auto page_of = [&](int t) { return table[min(t, a.max_tokens - 1) >> a.page_shift]; };
-  auto entry_of = [&](int page, int t) {
-    return page >= 0 && page < a.pages ? (page << a.page_shift) + (t & page_mask) : -1;
-  };
-  const uint32_t row_bytes = (uint32_t)hk * D;               // from one token to the next
-  const uint32_t koff = c16 * row_bytes + (NG % 2 == 0 ? 16 : 8) * g4;
-  const uint32_t voff1 = 4 * g4 * row_bytes + RB1 * c16, voff2 = 4 * g4 * row_bytes + 32 * P1::P + RB2 * c16;
-
-  // Pipeline: while a tile is computed, the next one's K, scales and V are in flight (K and the
-  // scales from the moment the scores are done, V from the moment the values are), and the pages
-  // of the one after that.  Loads come back in the order of their issue, so what is wanted first
-  // is asked for first, and none of them is behind a branch (past the last tile they read the
-  // pool's first entries).  A second buffer changed nothing (1 % slower): the loads are bound by
-  // bandwidth, not by their latency.
-  constexpr int KI = NG % 2 == 0 ? NG / 2 : NG;
-  typedef typename std::conditional<NG % 2 == 0, u32x4, u32x2>::type KRaw;
-  KRaw kr[2][KI];
-  KScales<NG> ksr;
-  uint32_t vsr;
-  Raw<RB1, NT> v1[8];
-  Raw<RB2, NT> v2[8];
-  auto load_k = [&](int e0, int e1) {                        // and the scales: one token per lane
-    const int64_t at = ((int64_t)(max(lane & 16 ? e1 : e0, 0) + c16)) * hk + h;
-    ksr.load(a.k_scales + at * NG);
-    vsr = a.v_scales[at];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const uint8_t* p = a.k_codes + ((int64_t)max(u ? e1 : e0, 0) * hk + h) * D;
-#pragma unroll
-      for (int n = 0; n < KI; ++n) {
-        if constexpr (NG % 2 == 0) kr[u][n] = ld<NT>(reinterpret_cast<const u32x4*>(p + 64 * n + koff));
-        else kr[u][n] = *reinterpret_cast<const u32x2*>(p + 32 * n + koff);
-      }
+    // q's rows (packed: query token, then head of the group); their first use is further down.
+    u32x4 qraw[R][NG];
+    int qpos[R];
+  #pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int row = r0 + 16 * r + c16;
+      const bool live = row < rows;
+      const int i = live ? row / a.G : i0, g = live ? row - i * a.G : 0;
+      qpos[r] = live ? p0 + i : -1;
+      const uint16_t* qp = a.q + (int64_t)(it.e.qs + i) * a.q_stride + (int64_t)(h * a.G + g) * D + (NG % 2 == 0 ? kq : 8 * g4);
+  #pragma unroll
+      for (int n = 0; n < NG; ++n) qraw[r][n] = ld16(qp + 32 * n);
     }
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  auto load_v = [&](int e0, int e1) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const uint8_t* p = a.v_codes + ((int64_t)max(u ? e1 : e0, 0) * hk + h) * D;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v1[4 * u + j].load(p + (size_t)j * row_bytes + voff1);
-        if constexpr (kTwo) v2[4 * u + j].load(p + (size_t)j * row_bytes + voff2);
+
+    f32x4 o[2 * NG][R];
+    float m[R], l[R];
+  #pragma unroll
+    for (int n = 0; n < 2 * NG; ++n)
+  #pragma unroll
+      for (int r = 0; r < R; ++r) o[n][r] = (f32x4){0.f, 0.f, 0.f, 0.f};
+  #pragma unroll
+    for (int r = 0; r < R; ++r) m[r] = kNegInf, l[r] = 0.0f;
+
+    const int hk = a.Hk, page_mask = (1 << a.page_shift) - 1;
+    typedef Pieces<NG> P1;
+    typedef Pieces<(P1::Rest > 0 ? P1::Rest : 1)> P2;          // NG <= 8, no 7: at most two pieces
+    constexpr int RB1 = 2 * P1::P, RB2 = 2 * P2::P;
+    constexpr bool kTwo = P1::Rest > 0;
+    static_assert(!kTwo || P2::Rest == 0, "two pieces at most");
+
+    // Tiles start at multiples of 32 tokens and pages hold 16 or more, so each half of a tile lies
+    // in one page: its first entry is uniform, and all addresses are a uniform base plus an offset
+    // that a lane keeps.  -1: the page is outside the pool (its tokens are left out).
+    const ConstInt* table = (const ConstInt*)(uintptr_t)(a.block_table + (int64_t)it.b * a.max_pages);
+    auto page_of = [&](int t) { return table[min(t, a.max_tokens - 1) >> a.page_shift]; };
+    auto entry_of = [&](int page, int t) {
+      return page >= 0 && page < a.pages ? (page << a.page_shift) + (t & page_mask) : -1;
+    };
+    const uint32_t row_bytes = (uint32_t)hk * D;               // from one token to the next
+    const uint32_t koff = c16 * row_bytes + (NG % 2 == 0 ? 16 : 8) * g4;
+    const uint32_t voff1 = 4 * g4 * row_bytes + RB1 * c16, voff2 = 4 * g4 * row_bytes + 32 * P1::P + RB2 * c16;
+
+    // Pipeline: while a tile is computed, the next one's K, scales and V are in flight (K and the
+    // scales from the moment the scores are done, V from the moment the values are), and the pages
+    // of the one after that.  Loads come back in the order of their issue, so what is wanted first
+    // is asked for first, and none of them is behind a branch (past the last tile they read the
+    // pool's first entries).  A second buffer changed nothing (1 % slower): the loads are bound by
+    // bandwidth, not by their latency.
+    constexpr int KI = NG % 2 == 0 ? NG / 2 : NG;
+    typedef typename std::conditional<NG % 2 == 0, u32x4, u32x2>::type KRaw;
+    KRaw kr[2][KI];
+    KScales<NG> ksr;
+    uint32_t vsr;
+    Raw<RB1, NT> v1[8];
+    Raw<RB2, NT> v2[8];
+    auto load_k = [&](int e0, int e1) {                        // and the scales: one token per lane
+      const int64_t at = ((int64_t)(max(lane & 16 ? e1 : e0, 0) + c16)) * hk + h;
+      ksr.load(a.k_scales + at * NG);
+      vsr = a.v_scales[at];
+  #pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint8_t* p = a.k_codes + ((int64_t)max(u ? e1 : e0, 0) * hk + h) * D;
+  #pragma unroll
+        for (int n = 0; n < KI; ++n) {
+          if constexpr (NG % 2 == 0) kr[u][n] = ld<NT>(reinterpret_cast<const u32x4*>(p + 64 * n + koff));
+          else kr[u][n] = *reinterpret_cast<const u32x2*>(p + 32 * n + koff);
+        }
       }
-    }
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  int e0 = entry_of(page_of(c0), c0), e1 = entry_of(page_of(c0 + 16), c0 + 16);   // of the tile's halves
-  int g0 = page_of(c0 + 32), g1 = page_of(c0 + 48);          // the next tile's pages
-  load_k(e0, e1);
-  load_v(e0, e1);
-
-  // q: per query row a power of two into [-1, 1), fp16; rows past the last are zero.
-  f16x8 qf[R][NG];
-  float cs[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const bool live = r0 + 16 * r + c16 < rows;
-    float f[NG][8], am = 0.0f;
-#pragma unroll
-    for (int n = 0; n < NG; ++n) {
-      const uint32_t d[4] = {qraw[r][n].x, qraw[r][n].y, qraw[r][n].z, qraw[r][n].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        f[n][2 * e] = live ? bf16_bits_to_f32(d[e] & 0xFFFF) : 0.0f;
-        f[n][2 * e + 1] = live ? bf16_bits_to_f32(d[e] >> 16) : 0.0f;
-        am = fmaxf(am, fmaxf(fabsf(f[n][2 * e]), fabsf(f[n][2 * e + 1])));
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto load_v = [&](int e0, int e1) {
+  #pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint8_t* p = a.v_codes + ((int64_t)max(u ? e1 : e0, 0) * hk + h) * D;
+  #pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v1[4 * u + j].load(p + (size_t)j * row_bytes + voff1);
+          if constexpr (kTwo) v2[4 * u + j].load(p + (size_t)j * row_bytes + voff2);
+        }
       }
-    }
-    am = max_across16(am);
-    const int ex = am > 0.0f ? __builtin_amdgcn_frexp_expf(am) : 0;   // am < 2^ex
-#pragma unroll
-    for (int n = 0; n < NG; ++n)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) qf[r][n][e] = (_Float16)__builtin_ldexpf(f[n][e], -ex);
-    cs[r] = __builtin_ldexpf(a.scale * kLog2e, ex);
-  }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    int e0 = entry_of(page_of(c0), c0), e1 = entry_of(page_of(c0 + 16), c0 + 16);   // of the tile's halves
+    int g0 = page_of(c0 + 32), g1 = page_of(c0 + 48);          // the next tile's pages
+    load_k(e0, e1);
+    load_v(e0, e1);
 
-  // Tokens before every row's window, in its first tile: no row sees them (so `open` is false there and
-  // their scores are masked), and their values are cleared, for an entry that no query sees may hold
-  // anything.  (17.5 against 17.2 us without it for 16 x 5 tokens in a window of 1024; as a condition of
-  // each tile in the loop below 18.1, and 1 % where there is no window.)
-  if (c0 < tmin) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (c0 + 4 * g4 + 16 * (i >> 2) + (i & 3) < tmin) {
-        v1[i].clear();
-        if constexpr (kTwo) v2[i].clear();
-      }
-  }
-
-  for (int base = c0; base < c1; base += 32) {
-    const bool all_valid = e0 >= 0 && e1 >= 0 && base + 32 <= c1;
-    const int n0 = entry_of(g0, base + 32), n1 = entry_of(g1, base + 48);
-    const int t0 = base + 4 * g4;                            // this lane's first token (u = j = 0)
-    auto there = [&](int u, int j) { return (u ? e1 : e0) >= 0 && t0 + 16 * u + j < c1; };
-    // V scales into the exponent.  A scale of zero (an entry never written) counts as the
-    // smallest one: its codes are zero too.  Tokens that are not there count as scale 1.
-    if (lane < 32) {
-      const bool in = all_valid || ((lane & 16 ? e1 : e0) >= 0 && base + lane < c1);
-      const float sv = in ? fmaxf(f16_lo(vsr), 0x1p-24f) : 1.0f;
-      mine.lv[lane] = __builtin_amdgcn_logf(sv);
-      mine.rv[lane] = __builtin_amdgcn_rcpf(sv);
-#pragma unroll
-      for (int n = 0; n < NG; ++n) mine.ks[n][lane] = ksr.get(n);
-    }
-    wave_sync();
-
-    // S^T: tokens 16 u + 4 g4 + j, query c16
-    float s[R][2][4];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-#pragma unroll
+    // q: per query row a power of two into [-1, 1), fp16; rows past the last are zero.
+    f16x8 qf[R][NG];
+    float cs[R];
+  #pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool live = r0 + 16 * r + c16 < rows;
+      float f[NG][8], am = 0.0f;
+  #pragma unroll
       for (int n = 0; n < NG; ++n) {
-        u32x2 kw;
-        if constexpr (NG % 2 == 0) {
-          if (n % 2 == 0) {
-            const auto lo = __builtin_amdgcn_permlane32_swap(kr[u][n / 2].x, kr[u][n / 2].z, false, false);
-            const auto hi = __builtin_amdgcn_permlane32_swap(kr[u][n / 2].y, kr[u][n / 2].w, false, false);
-            kr[u][n / 2] = (u32x4){lo[0], hi[0], lo[1], hi[1]};
-            kw = (u32x2){lo[0], hi[0]};
-          } else {
-            kw = (u32x2){kr[u][n / 2].z, kr[u][n / 2].w};
-          }
-        } else {
-          kw = (u32x2){kr[u][n].x, kr[u][n].y};
-        }
-        const f16x8 kf = i8x8_to_f16(kw);
-        const f32x4 ks = *reinterpret_cast<const f32x4*>(&mine.ks[n][16 * u + 4 * g4]);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const f32x4 d = mfma_f16_k32(kf, qf[r][n], (f32x4){0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s[r][u][j] = n == 0 ? ks[j] * d[j] : __builtin_fmaf(ks[j], d[j], s[r][u][j]);
+        const uint32_t d[4] = {qraw[r][n].x, qraw[r][n].y, qraw[r][n].z, qraw[r][n].w};
+  #pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          f[n][2 * e] = live ? bf16_bits_to_f32(d[e] & 0xFFFF) : 0.0f;
+          f[n][2 * e + 1] = live ? bf16_bits_to_f32(d[e] >> 16) : 0.0f;
+          am = fmaxf(am, fmaxf(fabsf(f[n][2 * e]), fabsf(f[n][2 * e + 1])));
         }
       }
+      am = max_across16(am);
+      const int ex = am > 0.0f ? __builtin_amdgcn_frexp_expf(am) : 0;   // am < 2^ex
+  #pragma unroll
+      for (int n = 0; n < NG; ++n)
+  #pragma unroll
+        for (int e = 0; e < 8; ++e) qf[r][n][e] = (_Float16)__builtin_ldexpf(f[n][e], -ex);
+      cs[r] = __builtin_ldexpf(a.scale * kLog2e, ex);
     }
-    float lv[2][4], rv[2][4];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      *reinterpret_cast<f32x4*>(lv[u]) = *reinterpret_cast<const f32x4*>(&mine.lv[16 * u + 4 * g4]);
-      *reinterpret_cast<f32x4*>(rv[u]) = *reinterpret_cast<const f32x4*>(&mine.rv[16 * u + 4 * g4]);
-    }
-    load_k(n0, n1);
-    g0 = page_of(base + 64);
-    g1 = page_of(base + 80);
 
-    // whole tile visible to every row of this workgroup?
-    const int tmin_p = p0 + i0, tmax_p = p0 + i1;
-    const bool open = all_valid && (!a.causal || base + 31 <= tmin_p) && (a.window <= 0 || base > tmax_p - a.window);
-    if (!all_valid) {
-#pragma unroll
+    // Tokens before every row's window, in its first tile: no row sees them (so `open` is false there and
+    // their scores are masked), and their values are cleared, for an entry that no query sees may hold
+    // anything.  (17.5 against 17.2 us without it for 16 x 5 tokens in a window of 1024; as a condition of
+    // each tile in the loop below 18.1, and 1 % where there is no window.)
+    if (c0 < tmin) {
+  #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (!there(i >> 2, i & 3)) {
+        if (c0 + 4 * g4 + 16 * (i >> 2) + (i & 3) < tmin) {
           v1[i].clear();
           if constexpr (kTwo) v2[i].clear();
         }
     }
-    f16x8 w[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float mx = kNegInf;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float v = __builtin_fmaf(s[r][u][j], cs[r], lv[u][j]);
-          if (!open) {
-            const int t = t0 + 16 * u + j;
-            const bool see = there(u, j) && (!a.causal || t <= qpos[r]) && (a.window <= 0 || t > qpos[r] - a.window);
-            v = see ? v : kNegInf;
+
+    for (int base = c0; base < c1; base += 32) {
+      const bool all_valid = e0 >= 0 && e1 >= 0 && base + 32 <= c1;
+      const int n0 = entry_of(g0, base + 32), n1 = entry_of(g1, base + 48);
+      const int t0 = base + 4 * g4;                            // this lane's first token (u = j = 0)
+      auto there = [&](int u, int j) { return (u ? e1 : e0) >= 0 && t0 + 16 * u + j < c1; };
+      // V scales into the exponent.  A scale of zero (an entry never written) counts as the
+      // smallest one: its codes are zero too.  Tokens that are not there count as scale 1.
+      if (lane < 32) {
+        const bool in = all_valid || ((lane & 16 ? e1 : e0) >= 0 && base + lane < c1);
+        const float sv = in ? fmaxf(f16_lo(vsr), 0x1p-24f) : 1.0f;
+        mine.lv[lane] = __builtin_amdgcn_logf(sv);
+        mine.rv[lane] = __builtin_amdgcn_rcpf(sv);
+  #pragma unroll
+        for (int n = 0; n < NG; ++n) mine.ks[n][lane] = ksr.get(n);
+      }
+      wave_sync();
+
+      // S^T: tokens 16 u + 4 g4 + j, query c16
+      float s[R][2][4];
+  #pragma unroll
+      for (int u = 0; u < 2; ++u) {
+  #pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          u32x2 kw;
+          if constexpr (NG % 2 == 0) {
+            if (n % 2 == 0) {
+              const auto lo = __builtin_amdgcn_permlane32_swap(kr[u][n / 2].x, kr[u][n / 2].z, false, false);
+              const auto hi = __builtin_amdgcn_permlane32_swap(kr[u][n / 2].y, kr[u][n / 2].w, false, false);
+              kr[u][n / 2] = (u32x4){lo[0], hi[0], lo[1], hi[1]};
+              kw = (u32x2){lo[0], hi[0]};
+            } else {
+              kw = (u32x2){kr[u][n / 2].z, kr[u][n / 2].w};
+            }
+          } else {
+            kw = (u32x2){kr[u][n].x, kr[u][n].y};
           }
-          s[r][u][j] = v;
-          mx = fmaxf(mx, v);
+          const f16x8 kf = i8x8_to_f16(kw);
+          const f32x4 ks = *reinterpret_cast<const f32x4*>(&mine.ks[n][16 * u + 4 * g4]);
+  #pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const f32x4 d = mfma_f16_k32(kf, qf[r][n], (f32x4){0.f, 0.f, 0.f, 0.f});
+  #pragma unroll
+            for (int j = 0; j < 4; ++j) s[r][u][j] = n == 0 ? ks[j] * d[j] : __builtin_fmaf(ks[j], d[j], s[r][u][j]);
+          }
         }
-      mx = max_across16(mx);
-      const float mn = fmaxf(m[r], mx - kLift);
-      const float ref = mn == kNegInf ? 0.0f : mn;
-      if (__ballot(mn > m[r])) {
-        const float corr = __builtin_amdgcn_exp2f(m[r] - ref);
-        l[r] *= corr;
-#pragma unroll
-        for (int n = 0; n < 2 * NG; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) o[n][r][j] *= corr;
-        m[r] = mn;
       }
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float e = __builtin_amdgcn_exp2f(s[r][u][j] - ref);
-          l[r] = __builtin_fmaf(e, rv[u][j], l[r]);
-          w[r][4 * u + j] = (_Float16)e;
-        }
-    }
-    pv_piece<P1::P, R, NT>(v1, w, o);
-    if constexpr (kTwo) pv_piece<P2::P, R, NT>(v2, w, o + 2 * P1::P);
-    load_v(n0, n1);
-    e0 = n0;
-    e1 = n1;
-  }
+      float lv[2][4], rv[2][4];
+  #pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        *reinterpret_cast<f32x4*>(lv[u]) = *reinterpret_cast<const f32x4*>(&mine.lv[16 * u + 4 * g4]);
+        *reinterpret_cast<f32x4*>(rv[u]) = *reinterpret_cast<const f32x4*>(&mine.rv[16 * u + 4 * g4]);
+      }
+      load_k(n0, n1);
+      g0 = page_of(base + 64);
+      g1 = page_of(base + 80);
 
-  // A lane has, per 16-row subtile, channels 2 P (4 g4 + j) .. + 2 P - 1 of each piece of its row.
-  // (The copies keep the compiler from computing addresses ahead of the tile loop.)
-  constexpr int W1 = 2 * P1::P, W2 = 2 * P2::P;
-  asm volatile("" : "+v"(c16), "+v"(g4));
-  const bool split = ck.count > 1;
-  const __amdgpu_buffer_rsrc_t rs = partial_rsrc(a.partials, a.partials_bytes);
-  auto part_row = [&](int c, int row) { return (int64_t)((ck.slot(c) * hk + h) * a.tile_rows + row) * (D + 4); };
-  auto out_row = [&](int grow) {                             // index of [token][query head]
-    const int i = grow / a.G;
-    return (int64_t)(it.e.qs + i) * a.Hq + h * a.G + (grow - i * a.G);
-  };
-#pragma unroll
-  for (int r = 0; r < R; ++r) {
-    const float L = sum_across16(l[r]);                      // over the lane groups of a query
-    const int row = 16 * r + c16;
-    if (r0 + row < rows) {
-      float v1r[4][W1], v2r[4][W2];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-#pragma unroll
-        for (int n = 0; n < W1; ++n) v1r[j][n] = o[n][r][j];
-        if constexpr (kTwo)
-#pragma unroll
-          for (int n = 0; n < W2; ++n) v2r[j][n] = o[W1 + n][r][j];
+      // whole tile visible to every row of this workgroup?
+      const int tmin_p = p0 + i0, tmax_p = p0 + i1;
+      const bool open = all_valid && (!a.causal || base + 31 <= tmin_p) && (a.window <= 0 || base > tmax_p - a.window);
+      if (!all_valid) {
+  #pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (!there(i >> 2, i & 3)) {
+            v1[i].clear();
+            if constexpr (kTwo) v2[i].clear();
+          }
       }
-      if (!split) {
-        const float inv = L == 0.0f ? 0.0f : 1.0f / L;          // (NaN stays NaN)
-        const int64_t at = out_row(r0 + row);
-        uint16_t* out = a.out + at * D;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          store_out<W1>(out + (4 * g4 + j) * W1, v1r[j], inv);
-          if constexpr (kTwo) store_out<W2>(out + 32 * P1::P + (4 * g4 + j) * W2, v2r[j], inv);
+      f16x8 w[R];
+  #pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float mx = kNegInf;
+  #pragma unroll
+        for (int u = 0; u < 2; ++u)
+  #pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float v = __builtin_fmaf(s[r][u][j], cs[r], lv[u][j]);
+            if (!open) {
+              const int t = t0 + 16 * u + j;
+              const bool see = there(u, j) && (!a.causal || t <= qpos[r]) && (a.window <= 0 || t > qpos[r] - a.window);
+              v = see ? v : kNegInf;
+            }
+            s[r][u][j] = v;
+            mx = fmaxf(mx, v);
+          }
+        mx = max_across16(mx);
+        const float mn = fmaxf(m[r], mx - kLift);
+        const float ref = mn == kNegInf ? 0.0f : mn;
+        if (__ballot(mn > m[r])) {
+          const float corr = __builtin_amdgcn_exp2f(m[r] - ref);
+          l[r] *= corr;
+  #pragma unroll
+          for (int n = 0; n < 2 * NG; ++n)
+  #pragma unroll
+            for (int j = 0; j < 4; ++j) o[n][r][j] *= corr;
+          m[r] = mn;
         }
-        if (a.lse && g4 == 0) a.lse[at] = L == 0.0f ? kNegInf : (m[r] + __builtin_amdgcn_logf(L)) * kLn2;
-      } else {
-        const int64_t p = part_row(ck.mine, row);
-#pragma unroll
+  #pragma unroll
+        for (int u = 0; u < 2; ++u)
+  #pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float e = __builtin_amdgcn_exp2f(s[r][u][j] - ref);
+            l[r] = __builtin_fmaf(e, rv[u][j], l[r]);
+            w[r][4 * u + j] = (_Float16)e;
+          }
+      }
+      pv_piece<P1::P, R, NT>(v1, w, o);
+      if constexpr (kTwo) pv_piece<P2::P, R, NT>(v2, w, o + 2 * P1::P);
+      load_v(n0, n1);
+      e0 = n0;
+      e1 = n1;
+    }
+
+    // A lane has, per 16-row subtile, channels 2 P (4 g4 + j) .. + 2 P - 1 of each piece of its row.
+    // (The copies keep the compiler from computing addresses ahead of the tile loop.)
+    constexpr int W1 = 2 * P1::P, W2 = 2 * P2::P;
+    asm volatile("" : "+v"(c16), "+v"(g4));
+    const bool split = ck.count > 1;
+    const __amdgpu_buffer_rsrc_t rs = partial_rsrc(a.partials, a.partials_bytes);
+    auto part_row = [&](int c, int row) { return (int64_t)((ck.slot(c) * hk + h) * a.tile_rows + row) * (D + 4); };
+    auto out_row = [&](int grow) {                             // index of [token][query head]
+      const int i = grow / a.G;
+      return (int64_t)(it.e.qs + i) * a.Hq + h * a.G + (grow - i * a.G);
+    };
+  #pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float L = sum_across16(l[r]);                      // over the lane groups of a query
+      const int row = 16 * r + c16;
+      if (r0 + row < rows) {
+        float v1r[4][W1], v2r[4][W2];
+  #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          store_run<W1>(rs, p + (4 * g4 + j) * W1, v1r[j]);
-          if constexpr (kTwo) store_run<W2>(rs, p + 32 * P1::P + (4 * g4 + j) * W2, v2r[j]);
+  #pragma unroll
+          for (int n = 0; n < W1; ++n) v1r[j][n] = o[n][r][j];
+          if constexpr (kTwo)
+  #pragma unroll
+            for (int n = 0; n < W2; ++n) v2r[j][n] = o[W1 + n][r][j];
         }
-        if (g4 == 0) {
-          const float ml[2] = {m[r], L};
-          store_run<2>(rs, p + D, ml);
+        if (!split) {
+          const float inv = L == 0.0f ? 0.0f : 1.0f / L;          // (NaN stays NaN)
+          const int64_t at = out_row(r0 + row);
+          uint16_t* out = a.out + at * D;
+  #pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            store_out<W1>(out + (4 * g4 + j) * W1, v1r[j], inv);
+            if constexpr (kTwo) store_out<W2>(out + 32 * P1::P + (4 * g4 + j) * W2, v2r[j], inv);
+          }
+          if (a.lse && g4 == 0) a.lse[at] = L == 0.0f ? kNegInf : (m[r] + __builtin_amdgcn_logf(L)) * kLn2;
+        } else {
+          const int64_t p = part_row(ck.mine, row);
+  #pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            store_run<W1>(rs, p + (4 * g4 + j) * W1, v1r[j]);
+            if constexpr (kTwo) store_run<W2>(rs, p + 32 * P1::P + (4 * g4 + j) * W2, v2r[j]);
+          }
+          if (g4 == 0) {
+            const float ml[2] = {m[r], L};
+            store_run<2>(rs, p + D, ml);
+          }
         }
       }
     }
-  }
-  if (!split) continue;
+    if (!split) continue;
 
-  // (four chunks at a time from heads of 128 on: 72 -> 63 us for 32 x 8 rows of 256 over 8000 tokens;
-  // heads of 64 lost 3 %)
-  join_chunks<D, (NG >= 4)>(a, rs, mine.join, lane, ck, min(TR, rows - r0), part_row, [&](int row) { return out_row(r0 + row); },
-                 [&](int level, int c) { return level * a.level_counters + ck.slot(c) * hk + h; });
+    // (four chunks at a time from heads of 128 on: 72 -> 63 us for 32 x 8 rows of 256 over 8000 tokens;
+    // heads of 64 lost 3 %)
+    join_chunks<D, (NG >= 4)>(a, rs, mine.join, lane, ck, min(TR, rows - r0), part_row,
+                              [&](int row) { return out_row(r0 + row); },
+                              [&](int level, int c) { return level * a.level_counters + ck.slot(c) * hk + h; });
   }
 }
 

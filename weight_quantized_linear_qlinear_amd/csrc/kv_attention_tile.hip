@@ -411,8 +411,8 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
                 s[k][i] = sm.vs[n & 3][32 * k + 8 * (i / 4) + 4 * half + (i & 3)] > 0.0f ? s[k][i] : kNegInf;
           }
           const int64_t from = (int64_t)qpos - t4;             // (may be far below and above the tile)
-        int hi = (int)max(min(from, (int64_t)T), (int64_t)-1), lo = (int)max(min(from - a.window, (int64_t)T), (int64_t)-1);
-        asm volatile("" : "+v"(hi), "+v"(lo));               // (compared as 32 bits)
+          int hi = (int)max(min(from, (int64_t)T), (int64_t)-1), lo = (int)max(min(from - a.window, (int64_t)T), (int64_t)-1);
+          asm volatile("" : "+v"(hi), "+v"(lo));             // (compared as 32 bits)
           if (a.causal) {
 #pragma unroll
             for (int k = 0; k < NB; ++k)
