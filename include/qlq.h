@@ -373,9 +373,11 @@ qlq_status qlq_kv_gather(const void* k_codes, const void* k_scales, const void* 
  * (the host does not wait for them) and bounded by 0 .. max_pages * page_size and 0 .. T; a token
  * whose page is outside the pool is left out, never read, and entries that no query of its
  * sequence sees (behind the last query, before the first one's window) may hold anything.
- * workspace: qlq_kv_attention_workspace_bytes(...), 256-byte aligned, zero-filled before its
- * first use and left so for the next call; it serves this operator's calls only, one stream at
- * a time. */
+ * One kernel is chosen for the whole call, by the average of query rows per KV head and sequence: a
+ * prompt's tokens and single tokens of other sequences are faster in a call each (up to 4 times).
+ * workspace: qlq_kv_attention_workspace_bytes(...), 256-byte aligned, its first 262144 bytes
+ * (counters) zero-filled before its first use and left so for the next call; it serves this
+ * operator's calls only, one stream at a time. */
 qlq_status qlq_kv_attention(const void* q_bf16, int64_t q_stride, int64_t T, int64_t B, int64_t Hq, int64_t Hk,
                             int64_t D, const void* k_codes, const void* k_scales, const void* v_codes,
                             const void* v_scales, int64_t pool, const int32_t* block_table, int64_t max_pages,

@@ -32,8 +32,8 @@
 //
 // Bound by HBM: a token is 266 bytes per KV head of 128, and 512 operations per query row that
 // shares them.  Measured (MI355X): 64 sequences of 2048 to 8192 tokens, 8 KV heads
-// of 128, 125 us (699 MB, 5.6 TB/s); one of 131071 over 4 KV heads 39.9 us (139 MB; 16 us of it
-// join 256 chunks per head); 16 x 5 tokens, window 1024, 16 heads of 64 18 us (latency).
+// of 128, 126 us (699 MB, 5.6 TB/s); one of 131071 over 4 KV heads 40 us (139 MB; 16 us of it
+// join 256 chunks per head); 16 x 5 tokens, window 1024, 16 heads of 64 17.5 us (latency).
 #include <type_traits>
 
 #include "kv_attention.h"
@@ -557,6 +557,10 @@ KvAttnPlan plan_kv_attention(int64_t T, int64_t B, int64_t Hk, int64_t G, int64_
   // against 69 and 159 us, 40 rows 94 and 269 against 100 and 261; 64 rows of 64 76 and 245 against
   // 62 and 199, of 192 107 and 265 against 88 and 241, of 256 125 and 352 against 97 and 214; 96
   // rows of 64 78 and 248 against 85 and 308, of 192 115 and 271 against 109 and 376.
+  // One kernel takes the whole call, so a prompt beside single tokens is slow on either side of that
+  // average (32 heads over 8 of 128, tokens over up to 4096): a prompt of 512 with 63 of them 289 us
+  // where the two calls take 74 + 49, with 127 227 (133 + 49), with 255 298 (248 + 49); one of 2048 with
+  // 255 of them 1400 (251 + 120).
   const bool pairs = pairs_rows((int)(D / 32));
   if (rows > (pairs ? 32 : 64)) {
     p.R = 16;

@@ -17,8 +17,8 @@
 // that V' of that scale keeps 2^6 .. 2^15 and smaller ones their 11 bits down to 2^-20 of it.
 //
 // Bound by instruction issue: per 64 tokens a wave of 128-channel heads issues 32 products (32
-// cycles each), 33 exponentials and about 200 other vector instructions, and two waves share a
-// SIMD; the matrix cores are busy 31 % of the time, LDS 25 %.  Measured (MI355X): two chunks of
+// cycles each), 33 exponentials and about 280 other vector instructions (counted), and two waves
+// share a SIMD; the matrix cores are busy 31 % of the time, LDS 25 %.  Measured (MI355X): two chunks of
 // 1500 and 804 queries over 8192 and 4394 tokens, 32 heads over 8 of 128, 313 to 333 us (235 GFLOP,
 // 730 TFLOP/s); a prompt of 512 tokens on its own 49 us, half of it storing and joining partial sums.
 #include "kv_attention.h"

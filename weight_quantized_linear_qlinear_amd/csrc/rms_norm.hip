@@ -18,8 +18,10 @@
 // Bound by HBM for many rows (2 K bytes of x, 2 K of the residual in and out, K of codes per
 // row) and by latency for few: a row is read once, kept in registers as fp32 (8 elements per
 // 16-byte chunk, NC chunks per thread) and written once.  Measured (MI355X, kernel alone): 8192
-// rows of 4096 with a residual, bf16 out, 43.6 us (268 MB, 6.2 TB/s); 333 of 4096 to FP8 5.2 us;
-// 1000 of 2048 to INT8 5.8 us; one of 2048 to FP8 2.7 us.
+// rows of 4096 with a residual, bf16 out, 43.9 us (268 MB, 6.1 TB/s); 333 of 4096 to FP8 5.2 us;
+// 1000 of 2048 to INT8 5.8 us; one of 2048 to FP8 2.7 us.  Rows that are no whole 16-byte chunks
+// take the kernel below that reads elements, twice: 8192 of 4095 111 us (bf16) and 123 us (FP8, where
+// 4096 columns take 44), 333 of 5001 15 and 17 us (5000 columns 6.6 and 7.1).
 #include "qlq_device.h"
 #include "qlq_launch.h"
 

@@ -263,7 +263,11 @@ hipError_t launch_rope_kv(const RopeArgs& a, hipStream_t st) {
   // A workgroup takes 4 waves x (64 / (D / 8)) head rows at a time.  Few tokens: one such batch
   // per workgroup (more, shorter workgroups); from 2048 on two tokens per workgroup share the
   // wait for positions and angles (2048 tokens, 32 + 2 x 8 heads of 128: 15.6 -> 13.8 us, 8191:
-  // 46.1 -> 41.3 us; four tokens: 17.3 and 41.3 us; split by batches: 18.8 and 63 us).
+  // 46.1 -> 41.3 us; four tokens: 17.3 and 41.3 us; split by batches: 18.8 and 63 us).  Between, one
+  // against two tokens, inputs in cache: 32 + 2 x 8 heads of 128, 1200 tokens 9.5 and 10.8 us, 1600
+  // 11.9 and 12.3, 2047 12.9 and 12.6, 3000 17.6 and 18.0; 28 + 2 x 4, 8.2 and 8.9, 10.4 and 10.1,
+  // 11.4 and 10.6, 15.5 and 14.6; 16 + 2 x 16 heads of 64 6.9 and 7.2, 8.5 and 8.2, 9.4 and 8.5, 12.7
+  // and 11.6: they cross between 1400 and 2047 tokens, by the heads.
   RopeArgs b = a;
   const int rpw = 64 / (a.D / 8), rows = a.Hq + a.Hk + a.Hv;
   const int batches = (rows + kRopeWaves * rpw - 1) / (kRopeWaves * rpw);
