@@ -11,7 +11,7 @@ import torch
 
 import oracle
 import weight_quantized_linear_qlinear_amd as qlq
-from oracle.layer import slots_of
+from oracle.layer import kv_attention, slots_of
 from tests.gpu_util import bf16_bits, bf16_to_gpu, bits_to_f64, dev
 from tests.test_gpu_attention import Problem
 
@@ -163,3 +163,38 @@ def test_lengths_and_tables_that_the_graph_itself_changes(nqs):
         g.replay()
         same = torch.equal(out, want) and torch.equal(lse, want_lse)
         assert same, n
+
+
+@pytest.mark.parametrize("heads", [(4, 1, 32), (4, 2, 64), (4, 1, 128), (8, 2, 256)])
+@pytest.mark.parametrize("huge", [2.0 ** 14, 2.0 ** 24])
+def test_prompt_rows_that_do_not_see_a_huge_value(heads, huge):
+    # One token's values are 2^14 or 2^24 times the others'.  Rows before it do not see it, and their bound does not
+    # know it: 2^-8 of the output and (2 2^-11 + 2 E) S as for any prompt (test_gpu_attention.py), and what fp16's
+    # smallest step (2^-24) leaves of a value at the outlier's scaling (its own scale at 2^5 or more, a code at 2^-8):
+    # half a step is 2^-30 of the outlier's scale, once per token.
+    Hq, Hk, D = heads
+    nqs, lens = (100, 70), (260, 70)
+    p = Problem(D, nqs, lens, Hq, Hk, D, 16, each=False)
+    kc, ks, vc, vs = p.host
+    at = [slots_of(p.table[b], lens[b], 16, p.pool) for b in range(2)]
+    for b, s in enumerate(at):                         # queries 0 .. 59 of each sequence come before it
+        t = lens[b] - nqs[b] + 60
+        vs[s[t]] = oracle.fp16_encode(np.minimum(oracle.fp16_decode(vs[s[t]]) * huge, 65504.0).astype(np.float32))
+    p.cache = qlq.QuantizedKV(_gpu(kc, torch.int8), _gpu(ks.view(np.int16), torch.float16), _gpu(vc, torch.uint8),
+                              _gpu(vs.view(np.int16), torch.float16))
+    got = bits_to_f64(bf16_bits(p.run()))
+    k, v = p.values()
+    q = bits_to_f64(p.qb)
+    o64, _, _, S = kv_attention(q, k, v, p.table, lens, 16, p.starts)
+    for b, s in enumerate(at):
+        ku, scales = np.abs(k[s]), oracle.fp16_decode(vs[s]).astype(np.float64)
+        A = D ** -0.5 * max((np.abs(q[:, h]) @ ku[:, h // (Hq // Hk)].T).max() for h in range(Hq))
+        A1 = D ** -0.5 * np.abs(q).max() * ku.sum(-1).max()
+        E = U * (42 * A + A1 + 3 * (2 * A + 56) + lens[b] / 32 + 40) + 2.0 ** -11 * A + U * A1
+        rows = slice(p.starts[b], p.starts[b] + 60)
+        unseen = lens[b] - nqs[b] + 60
+        V = np.abs(v[s[:unseen]]).max()
+        bound = 2.0 ** -8 * np.abs(o64[rows]) + S[rows] * (2 * 2.0 ** -11 + 2 * E) + lens[b] * 2.0 ** -32 * V
+        bound += 2.0 ** -30 * scales.max()
+        over = np.abs(got[rows] - o64[rows]) / bound
+        assert over.max() <= 1.0, f"sequence {b}: {over.max():.2f} times the bound"

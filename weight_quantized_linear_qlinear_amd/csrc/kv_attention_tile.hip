@@ -14,7 +14,7 @@
 // Roundings to fp16's 11 bits: K', V' and the weights (kv_attention.hip has the weights' alone;
 // there the products with the scales are fp32).  Range: K' overflows only for scales above 512,
 // a tile with such a scale is computed in 2^-7 of it; E follows the largest V scale so far, so
-// that V' of that scale keeps 2^6 .. 2^15 and smaller ones their 11 bits down to 2^-20 of it.
+// that this scale is at 2^5 .. 2^6 and V' below 2^15; fp16's smallest step is then 2^-29 of it.
 //
 // Bound by instruction issue: per 64 tokens a wave of 128-channel heads issues 32 products (32
 // cycles each), 33 exponentials and about 280 other vector instructions (counted), and two waves
@@ -147,6 +147,12 @@ struct TileScale {
   bool gap;                      // a token is not there
 };
 constexpr int kNoScale = -1000;
+
+// V's codes go to fp16 as 2^-8 of themselves (exact: 2^-17 is the smallest) and their scales as 2^(8 - E), so
+// that a scale keeps its 11 bits down to 2^-27 of the largest.  (2^-19 with both as they are: beside a
+// scale 2^24 times as large, which earlier rows of its query tile do not even see, 5 bits were left.)
+constexpr int kCodeShift = 8;
+constexpr float kCode = 0x1p-8f;
 
 // N products that take one operand from LDS each, in exactly this order: AHEAD reads in front,
 // then a product and the read of a later one in turn (left alone, the compiler reads each operand
@@ -307,7 +313,7 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
 #pragma unroll
         for (int i = 0; i < 4; ++i) r[i] = vsc[i] > 0.0f ? vraw[i] : 0u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) vsc[i] = __builtin_ldexpf(vsc[i], -next.e);
+        for (int i = 0; i < 4; ++i) vsc[i] = __builtin_ldexpf(vsc[i], kCodeShift - next.e);
         const f16x2 v01 = {(_Float16)vsc[0], (_Float16)vsc[1]}, v23 = {(_Float16)vsc[2], (_Float16)vsc[3]};
         const uint32_t a01 = __builtin_amdgcn_perm(r[1], r[0], 0x05010400u), b01 = __builtin_amdgcn_perm(r[1], r[0], 0x07030602u);
         const uint32_t a23 = __builtin_amdgcn_perm(r[3], r[2], 0x05010400u), b23 = __builtin_amdgcn_perm(r[3], r[2], 0x07030602u);
@@ -317,10 +323,10 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t s01 = i < 2 ? a01 : b01, s23 = i < 2 ? a23 : b23;
-          const uint32_t lo = i & 1 ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(s01, 1.0f, true))
-                                    : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(s01, 1.0f, false));
-          const uint32_t hi = i & 1 ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(s23, 1.0f, true))
-                                    : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(s23, 1.0f, false));
+          const uint32_t lo = i & 1 ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(s01, kCode, true))
+                                    : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(s01, kCode, false));
+          const uint32_t hi = i & 1 ? __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(s23, kCode, true))
+                                    : __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(s23, kCode, false));
           const int d = 4 * vcb + i;
           *reinterpret_cast<u32x2*>(&sm.v[buf][d][8 * (p ^ swizzle<T>(d)) + 4 * hf]) = (u32x2){mul2(lo, v01), mul2(hi, v23)};
         }
