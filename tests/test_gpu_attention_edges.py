@@ -198,3 +198,43 @@ def test_prompt_rows_that_do_not_see_a_huge_value(heads, huge):
         bound += 2.0 ** -30 * scales.max()
         over = np.abs(got[rows] - o64[rows]) / bound
         assert over.max() <= 1.0, f"sequence {b}: {over.max():.2f} times the bound"
+
+
+@pytest.mark.parametrize("heads", [(4, 1, 32), (4, 2, 64), (4, 1, 128), (8, 2, 256)])
+def test_prompt_rows_that_do_not_see_a_huge_key(heads):
+    # One token's keys have scales of 3000; the others' are small (2^-6).  A query is the key of its own token, scaled
+    # to a score of 8.  Rows before the huge one do not see it; in their bound A and A' are those of the keys they see,
+    # and a key beside the huge one is off by fp16's smallest half step at 2^-7 of it: 2^-18, times scale sum |q| in a
+    # score.
+    Hq, Hk, D = heads
+    nqs, lens = (100, 70), (260, 70)
+    p = Problem(D + 1, nqs, lens, Hq, Hk, D, 16, each=False)
+    kc, ks, vc, vs = p.host
+    at = [slots_of(p.table[b], lens[b], 16, p.pool) for b in range(2)]
+    for s in at:
+        ks[s] = oracle.fp16_encode((oracle.fp16_decode(ks[s]) * 2.0 ** -6).astype(np.float32))
+    k, v = p.values()
+    q = np.concatenate([np.repeat(k[s[lens[b] - nqs[b]:]], Hq // Hk, axis=1) for b, s in enumerate(at)])
+    q *= 8 * D ** 0.5 / (q * q).sum(-1, keepdims=True)
+    p.qb = oracle.f32_to_bf16_bits(q.astype(np.float32))
+    p.q = bf16_to_gpu(p.qb)
+    for b, s in enumerate(at):                         # queries 0 .. 59 of each sequence come before it
+        ks[s[lens[b] - nqs[b] + 60]] = oracle.fp16_encode(np.float32(3000.0))
+    p.cache = qlq.QuantizedKV(_gpu(kc, torch.int8), _gpu(ks.view(np.int16), torch.float16), _gpu(vc, torch.uint8),
+                              _gpu(vs.view(np.int16), torch.float16))
+    lse = torch.zeros(p.T, Hq, device=dev())
+    got = bits_to_f64(bf16_bits(p.run(lse=lse)))
+    q, (k, v) = bits_to_f64(p.qb), p.values()
+    o64, l64, _, S = kv_attention(q, k, v, p.table, lens, 16, p.starts)
+    for b, s in enumerate(at):
+        unseen = lens[b] - nqs[b] + 60
+        ku, vu, rows = np.abs(k[s[:unseen]]), np.abs(v[s[:unseen]]), slice(p.starts[b], p.starts[b] + 60)
+        qa = np.abs(q[rows])
+        A = D ** -0.5 * max((qa[:, h] @ ku[:, h // (Hq // Hk)].T).max() for h in range(Hq))
+        A1 = D ** -0.5 * qa.max() * ku.sum(-1).max()
+        E = U * (42 * A + A1 + 3 * (2 * A + 56) + lens[b] / 32 + 40) + 2.0 ** -11 * A + U * A1
+        E += 2.0 ** -18 * D ** -0.5 * qa.sum(-1).max()
+        off = np.abs(lse.cpu().numpy()[rows] - l64[rows]) / (2 * E + U * np.abs(l64[rows]))
+        bound = 2.0 ** -8 * np.abs(o64[rows]) + S[rows] * (2 * 2.0 ** -11 + 2 * E) + lens[b] * 2.0 ** -32 * vu.max()
+        over = np.abs(got[rows] - o64[rows]) / bound
+        assert max(over.max(), off.max()) <= 1.0, f"sequence {b}: output {over.max():.2f}, lse {off.max():.2f} times the bound"

@@ -24,11 +24,11 @@ __device__ __forceinline__ float f16_lo(uint32_t b) { return (float)__builtin_bi
 __device__ __forceinline__ float f16_hi(uint32_t b) { return (float)__builtin_bit_cast(_Float16, (uint16_t)(b >> 16)); }
 
 // Two int8 codes (bytes 0, 1 or 2, 3 of w ^ 0x80808080) as fp16: 1024 + (q + 128) by its bit
-// pattern, minus 1152; exact.
+// pattern, minus 1152; exact.  With the upper byte of 8 and minus 9, 2^-7 of the codes.
 template <bool HI>
-__device__ __forceinline__ uint32_t i8x2_to_f16(uint32_t flipped) {
-  const uint32_t b = __builtin_amdgcn_perm(0x64646464u, flipped, HI ? 0x04030402u : 0x04010400u);
-  const f16x2 k = {(_Float16)1152.0f, (_Float16)1152.0f};
+__device__ __forceinline__ uint32_t i8x2_to_f16(uint32_t flipped, uint32_t upper = 0x64646464u, float zero = 1152.0f) {
+  const uint32_t b = __builtin_amdgcn_perm(upper, flipped, HI ? 0x04030402u : 0x04010400u);
+  const f16x2 k = {(_Float16)zero, (_Float16)zero};
   return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, b) - k);
 }
 

@@ -293,8 +293,9 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
       next.big = (top & 0xFFFF) > 0x6000;
       const uint32_t vt = top >> 16;
       if (vt) next.e = max(next.e, (vt >= 0x400 ? (int)(vt >> 10) - 14 : 8 - __builtin_clz(vt)) - 6);
-      const float s = next.big ? f16_lo(ksraw) * 0x1p-7f : f16_lo(ksraw);
-      const f16x2 s2 = {(_Float16)s, (_Float16)s};
+      const f16x2 s2 = __builtin_bit_cast(f16x2, (ksraw & 0xFFFF) | ksraw << 16);
+      const uint32_t upper = next.big ? 0x48484848u : 0x64646464u;        // (the codes take the 2^-7: a small scale
+      const float zero = next.big ? 9.0f : 1152.0f;                       // beside a big one keeps its bits)
       f32x4 vsc = *reinterpret_cast<const f32x4*>(&sm.vs[n & 3][first_t + 4 * vgrp]);
       if (lane < NL) {
         const uint32_t kd[4] = {kraw.x, kraw.y, kraw.z, kraw.w};
@@ -302,8 +303,8 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t f = kd[i] ^ 0x80808080u;
-          w[i / 2][2 * (i & 1)] = mul2(i8x2_to_f16<false>(f), s2);
-          w[i / 2][2 * (i & 1) + 1] = mul2(i8x2_to_f16<true>(f), s2);
+          w[i / 2][2 * (i & 1)] = mul2(i8x2_to_f16<false>(f, upper, zero), s2);
+          w[i / 2][2 * (i & 1) + 1] = mul2(i8x2_to_f16<true>(f, upper, zero), s2);
         }
         _Float16* kp = &sm.k[buf][first_t + krow][16 * kchunk];
         st16(kp, w[0]);
