@@ -843,10 +843,11 @@ def kv_attention(q: torch.Tensor, cache: QuantizedKV, block_table: torch.Tensor,
 
     block_table int32 [B, pages] holds each sequence's page numbers (token t is cache entry
     block_table[b][t // page_size] * page_size + t % page_size; page_size a power of two from 16), seq_lens int32
-    [B] its cached tokens.  Without q_start, row b of q is the last token of sequence b; with q_start int32 [B + 1], rows q_start[b] ..
-    q_start[b+1]-1 are its last tokens.  A query sees the tokens up to its own (causal), and no more than `window`
-    of them if that is not 0.  scale defaults to D^-0.5; lse fp32 [T, Hq], if given, receives log sum exp of the
-    scaled scores.  Rows that see nothing give zeros (lse -inf); rows of no sequence are left as they were.
+    [B] its cached tokens.  Without q_start, row b of q is the last token of sequence b; with q_start int32 [B + 1],
+    rows q_start[b] .. q_start[b+1]-1 are its last tokens.  A query sees the tokens up to its own (causal), and no
+    more than `window` of them if that is not 0.  scale defaults to D^-0.5; lse fp32 [T, Hq], if given, receives log
+    sum exp of the scaled scores.  Rows that see nothing give zeros (lse -inf); rows of no sequence are left as they
+    were.
     The lengths stay on the device: nothing here waits for them.  One kernel is chosen for all rows by their average
     per sequence, so prompts and single tokens are faster in a call each.
 
