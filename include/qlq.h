@@ -389,6 +389,63 @@ qlq_status qlq_kv_attention(const void* q_bf16, int64_t q_stride, int64_t T, int
  * call needs none, or for sizes that the call refuses. */
 size_t qlq_kv_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int one_each);
 
+/* Norms of query and key heads with rotary positions of one axis or several, in one kernel: per head
+ * row x of q [T, Hq, D] and k [T, Hk, D] (bf16, token strides in elements)
+ *   y_c = x_c weight_c / sqrt(mean_c(x_c^2) + eps)     q_weight, k_weight bf16 [D]; NULL: y = x
+ * and the rotation of y as in qlq_rope, with theta = positions[axes[i]][t] * inv_freq[i]: positions
+ * [n_axes, T] (images and video: time, rows, columns), axes int32 [rotary_dim / 2] on the device, entries
+ * outside 0 .. n_axes - 1 count as the nearest of them (NULL for one axis; n_axes at most 16).  One
+ * rounding, at the end.  q_out may be q and k_out k (same strides), no other buffers may overlap.
+ * Hk = 0: q alone (k, k_out, k_weight are not looked at).  eps is looked at where there is a weight.
+ * D a multiple of 8, at most 512; the rest as for qlq_rope. */
+qlq_status qlq_norm_rope(const void* q_bf16, int64_t q_stride, const void* k_bf16, int64_t k_stride, int64_t T,
+                         int64_t Hq, int64_t Hk, int64_t D, const void* q_weight, const void* k_weight, float eps,
+                         const void* positions, int positions_64, const int32_t* axes, int64_t n_axes,
+                         const double* inv_freq, int64_t rotary_dim, float factor, int interleaved, void* q_out_bf16,
+                         int64_t q_out_stride, void* k_out_bf16, int64_t k_out_stride, hipStream_t stream);
+
+/* The 4-bit cache: K and V both as OCP e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign) with an IEEE
+ * binary16 scale per (t, h, group g of channels 32g .. 32g+31):
+ *   scale = fp16(fp32(absmax / 6)): 1 for an all-zero group, 2^-24 where a positive absmax would round
+ *           to 0, at most 65504, NaN for a group with a NaN or an infinity
+ *   code  = e2m1(x / scale): nearest, ties to even, saturating at 6
+ * k_codes, v_codes [pool, H, D/2] bytes, k_scales, v_scales [pool, H, D/32].  A row's bytes: its groups in
+ * runs of P = 8, 4, 2 or 1, the largest that fits each time; byte c P + g of a run (c = 0 .. 15) is
+ * channels 2c (low nibble) and 2c + 1 of the run's group g.  Per (t, h) D + D/8 bytes: 0.28 of bf16.
+ *
+ * qlq_norm_rope of q and k (Hk >= 1) and appending the rotated k and v to slots[t] of a cache of 8 bits
+ * (qlq_kv_append's entries) or of 4, in one kernel.  K is quantized from its unrounded value: in fp32 for
+ * 8 bits, in fp64 for 4.  Slots as in qlq_kv_append; D a multiple of 32, at most 512; code buffers 16-byte
+ * aligned.  bits other than 4 and 8: QLQ_ERR_UNSUPPORTED. */
+qlq_status qlq_norm_rope_kv_append(const void* q_bf16, int64_t q_stride, const void* k_bf16, int64_t k_stride,
+                                   const void* v_bf16, int64_t v_stride, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
+                                   const void* q_weight, const void* k_weight, float eps, const void* positions,
+                                   int positions_64, const int32_t* axes, int64_t n_axes, const double* inv_freq,
+                                   int64_t rotary_dim, float factor, int interleaved, const void* slots, int slots_64,
+                                   int64_t pool, int bits, void* k_codes, void* k_scales, void* v_codes,
+                                   void* v_scales, void* q_out_bf16, int64_t q_out_stride, hipStream_t stream);
+
+/* qlq_kv_append and qlq_kv_gather for the 4-bit cache (gather: D at most 512, bf16(fp32(code) * fp32(scale))). */
+qlq_status qlq_kv4_append(const void* k_bf16, int64_t k_stride, const void* v_bf16, int64_t v_stride, int64_t T,
+                          int64_t H, int64_t D, const void* slots, int slots_64, int64_t pool, void* k_codes,
+                          void* k_scales, void* v_codes, void* v_scales, hipStream_t stream);
+qlq_status qlq_kv4_gather(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                          int64_t pool, int64_t H, int64_t D, const void* slots, int slots_64, int64_t n, void* k_bf16,
+                          void* v_bf16, hipStream_t stream);
+
+/* qlq_kv_attention over the 4-bit cache: the same arguments, masks, rules and workspace (of
+ * qlq_kv4_attention_workspace_bytes; one buffer may serve both operators' calls on one stream).  Code and
+ * scale buffers 16-byte aligned.  k_t = k_code k_scale and v_t = v_code v_scale are not rounded with few rows;
+ * weights times V scales are rounded to fp16: 2^-11, 2^-40 of the row's largest below 2^-29 of it.  With many
+ * rows (as in qlq_kv_attention) K, V and the weights are rounded to 11 bits each. */
+qlq_status qlq_kv4_attention(const void* q_bf16, int64_t q_stride, int64_t T, int64_t B, int64_t Hq, int64_t Hk,
+                             int64_t D, const void* k_codes, const void* k_scales, const void* v_codes,
+                             const void* v_scales, int64_t pool, const int32_t* block_table, int64_t max_pages,
+                             int64_t page_size, const int32_t* seq_lens, const int32_t* q_start, float scale,
+                             int causal, int64_t window, void* out_bf16, float* lse, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream);
+size_t qlq_kv4_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int one_each);
+
 /* ------------------------------------------------------------- test hooks */
 
 /* The launch plan a GEMM call takes for these sizes when x is 16-byte aligned (what

@@ -116,3 +116,63 @@ def kv_dequantize(k_codes, k_scales, v_codes, v_scales):
 def kv_bytes_per_token_head(D: int) -> int:
     """Storage of one (token, head) entry: K codes + K fp16 scales + V codes + one V fp16 scale."""
     return D + 2 * (D // K_GROUP) + D + 2
+
+
+# The 4-bit entries: K and V both e2m1 in groups of 32 channels with fp16 scales.
+#
+# The pages quantize their cache to 8 bits; this form carries their K rule (a float16 scale per 32 channels,
+# absmax over the largest code) to the 4-bit floating format that the MI355X converts by itself (OCP e2m1: no
+# infinities, no NaN).  Readings: the scale is fp16(fp32(absmax / 6)), with the range rules of the 8-bit codec; a group
+# with a NaN or an infinity has a NaN scale, since a code cannot hold one.
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def kv4_order(D: int) -> np.ndarray:
+    """The channel of nibble i of a row (nibble i is the low half of byte i / 2 for even i): runs of 8, 4, 2 or 1 groups,
+    the largest that fits each time; in a run of P groups byte c P + g is channels 2 c and 2 c + 1 of group g."""
+    out, first = [], 0
+    while first < D // 32:
+        P = next(p for p in (8, 4, 2, 1) if p <= D // 32 - first)
+        out += [32 * (first + g) + 2 * c + e for c in range(16) for g in range(P) for e in range(2)]
+        first += P
+    return np.array(out)
+
+
+def e2m1_encode(x, s) -> np.ndarray:
+    """Codes (0 .. 15, bit 3 the sign) of x / s: nearest, ties to the even code, saturating; x, s float64."""
+    a = np.abs(x)
+    c = np.zeros(np.broadcast(x, s).shape, np.uint8)
+    for i in range(7):
+        border = (E2M1[i] + E2M1[i + 1]) / 2 * s           # (exact: s has 11 bits)
+        c += (a > border) if i % 2 == 0 else (a >= border)
+    return c | np.where(np.signbit(x), 8, 0).astype(np.uint8)
+
+
+def kv4_quantize_values(x: np.ndarray):
+    """Values [..., D] (float64) -> (bytes [..., D/2], scales fp16 bits [..., D/32])."""
+    x = np.asarray(x, np.float64)
+    D = x.shape[-1]
+    g = x.reshape(*x.shape[:-1], D // 32, 32)
+    am = np.abs(g).max(-1)                                 # (NaN where the group has one)
+    with np.errstate(invalid="ignore", over="ignore"):
+        s = fp16_encode(np.minimum((am / 6.0).astype(np.float32), np.float32(FP16_MAX)))
+    s = np.where(am == 0, np.uint16(0x3C00), np.where((am > 0) & (s == 0), np.uint16(1), s))
+    s = np.where(np.isfinite(am), s, np.uint16(0x7E00)).astype(np.uint16)
+    with np.errstate(invalid="ignore"):
+        c = e2m1_encode(g, fp16_decode(s)[..., None]).reshape(x.shape)[..., kv4_order(D)]
+    return (c[..., 0::2] | (c[..., 1::2] << 4)).astype(np.uint8), s
+
+
+def kv4_values(codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
+    """The values (float64) that bytes [..., D/2] and scales (fp16 bits) [..., D/32] stand for."""
+    D = 2 * codes.shape[-1]
+    n = np.stack((codes & 15, codes >> 4), -1).reshape(*codes.shape[:-1], D)
+    v = np.empty(n.shape, np.float64)
+    v[..., kv4_order(D)] = np.where(n & 8, -1.0, 1.0) * E2M1[n & 7]
+    with np.errstate(invalid="ignore"):
+        return (v.reshape(*codes.shape[:-1], D // 32, 32) * fp16_decode(scales)[..., None]).reshape(v.shape)
+
+
+def kv4_bytes_per_token_head(D: int) -> int:
+    """Storage of one 4-bit (token, head) entry: codes and fp16 scales of K and V."""
+    return 2 * (D // 2 + 2 * (D // 32))

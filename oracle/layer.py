@@ -19,11 +19,23 @@ def rms_norm(x, weight, eps, residual=None):
     return h * rho * np.asarray(weight, np.float64), h
 
 
-def rope(x, positions, inv_freq, factor=1.0, interleaved=False):
-    """Rotary positions on the first 2 * len(inv_freq) channels of x [T, H, D], unrounded."""
+def norm_heads(x, weight, eps):
+    """RMS norm of every head row of x [T, H, D] (weight None: x), unrounded."""
+    x = np.asarray(x, np.float64)
+    if weight is None:
+        return x
+    rho = 1.0 / np.sqrt((x * x).mean(axis=-1, keepdims=True) + np.float64(np.float32(eps)))
+    return x * rho * np.asarray(weight, np.float64)
+
+
+def rope(x, positions, inv_freq, factor=1.0, interleaved=False, axes=None):
+    """Rotary positions on the first 2 * len(inv_freq) channels of x [T, H, D], unrounded; with axes,
+    frequency i takes its position from row axes[i] of positions [n, T]."""
     x = np.asarray(x, np.float64)
     n = len(inv_freq)
-    ang = np.asarray(positions, np.float64)[:, None] * np.asarray(inv_freq, np.float64)[None, :]
+    positions = np.asarray(positions, np.float64)
+    at = positions[:, None] if axes is None else positions[np.asarray(axes)].T
+    ang = at * np.asarray(inv_freq, np.float64)[None, :]
     c, s = factor * np.cos(ang)[:, None, :], factor * np.sin(ang)[:, None, :]
     ia = np.arange(n) * 2 if interleaved else np.arange(n)
     ib = ia + 1 if interleaved else ia + n

@@ -87,6 +87,16 @@ _SIGNATURES = {
                                     _c.c_void_p]),
     "qlq_kv_attention_workspace_bytes": (_c.c_size_t, [_c.c_int64, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int64,
                                                        _c.c_int]),
+    "qlq_norm_rope": (_c.c_int, [_c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int64,
+                                 _c.c_int64, _c.c_void_p, _c.c_void_p, _c.c_float, _c.c_void_p, _c.c_int, _c.c_void_p,
+                                 _c.c_int64, _c.c_void_p, _c.c_int64, _c.c_float, _c.c_int, _c.c_void_p, _c.c_int64,
+                                 _c.c_void_p, _c.c_int64, _c.c_void_p]),
+    "qlq_norm_rope_kv_append": (_c.c_int, [_c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_int64,
+                                           _c.c_int64, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_void_p,
+                                           _c.c_float, _c.c_void_p, _c.c_int, _c.c_void_p, _c.c_int64, _c.c_void_p,
+                                           _c.c_int64, _c.c_float, _c.c_int, _c.c_void_p, _c.c_int, _c.c_int64,
+                                           _c.c_int, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p, _c.c_void_p,
+                                           _c.c_int64, _c.c_void_p]),
     "qlq_linear": (_c.c_int, [_c.c_int, _c.c_void_p, _c.c_int64, _c.c_int64, _c.c_int64, _c.c_void_p, _c.c_void_p,
                               _c.c_int64, _c.c_int, _c.c_float, _c.c_void_p, _c.c_int64, _c.c_void_p, _c.c_void_p,
                               _c.c_size_t, _c.c_void_p]),
@@ -97,6 +107,9 @@ _SIGNATURES = {
     "qlq_last_error": (_c.c_char_p, []),
     "qlq_version": (_c.c_char_p, []),
 }
+
+for _name in ("append", "gather", "attention", "attention_workspace_bytes"):
+    _SIGNATURES["qlq_kv4_" + _name] = _SIGNATURES["qlq_kv_" + _name]
 
 _lib = None
 _lock = threading.Lock()
@@ -450,13 +463,29 @@ class QuantizedKV:
     v_scales: torch.Tensor    # float16 [T, H]
 
 
+@dataclasses.dataclass
+class QuantizedKV4:
+    """4-bit cache entries (e2m1 codes, two per byte in the order of include/qlq.h) for [T, H, D] keys and values."""
+    k_codes: torch.Tensor     # uint8 [T, H, D / 2]
+    k_scales: torch.Tensor    # float16 [T, H, D / 32]
+    v_codes: torch.Tensor     # uint8 [T, H, D / 2]
+    v_scales: torch.Tensor    # float16 [T, H, D / 32]
+
+
+def _eight_bits(c):
+    if not isinstance(c, QuantizedKV):
+        raise ValueError("this call takes 8-bit entries (QuantizedKV)")
+
+
 def kv_quantize(k: torch.Tensor, v: torch.Tensor, out: QuantizedKV | None = None) -> QuantizedKV:
     """Quantize bf16 K and V [T, H, D] (D % 32 == 0) into cache entries."""
     _require_gpu(k, v)
     if k.dim() != 3 or k.shape != v.shape or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
         raise ValueError("k and v must be bf16 [T, H, D] of the same shape")
     T, H, D = k.shape
-    if out is None:
+    if out is not None:
+        _eight_bits(out)
+    else:
         out = QuantizedKV(torch.empty((T, H, D), dtype=torch.int8, device=k.device),
                           torch.empty((T, H, max(D // 32, 1)), dtype=torch.float16, device=k.device),
                           torch.empty((T, H, D), dtype=torch.uint8, device=k.device),
@@ -468,6 +497,7 @@ def kv_quantize(k: torch.Tensor, v: torch.Tensor, out: QuantizedKV | None = None
 
 def kv_dequantize(q: QuantizedKV, k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None):
     """Cache entries -> bf16 (K, V) [T, H, D]."""
+    _eight_bits(q)
     _require_gpu(q.k_codes, q.k_scales, q.v_codes, q.v_scales)
     T, H, D = q.k_codes.shape
     if k_out is None:
@@ -479,11 +509,17 @@ def kv_dequantize(q: QuantizedKV, k_out: torch.Tensor | None = None, v_out: torc
     return k_out, v_out
 
 
-def kv_cache(slots: int, heads: int, head_dim: int, device: torch.device | str | None = None) -> QuantizedKV:
-    """An empty cache of `slots` token entries (codes zero, scales one) for kv_append and kv_attention."""
+def kv_cache(slots: int, heads: int, head_dim: int, device: torch.device | str | None = None, bits: int = 8):
+    """An empty cache of `slots` token entries (codes zero, scales one) for kv_append and kv_attention, of 8 bits
+    (QuantizedKV) or of 4 (QuantizedKV4: 144 bytes per token and head of 128 instead of 266)."""
     if slots < 1 or heads < 1 or head_dim < 32 or head_dim % 32 != 0:
         raise ValueError("slots and heads must be >= 1 and head_dim a multiple of 32")
+    if bits not in (4, 8):
+        raise ValueError("a cache has 4 or 8 bits")
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    if bits == 4:
+        return QuantizedKV4(*(f((slots, heads, head_dim // n), dtype=t, device=dev) for f, n, t in
+                              ((torch.zeros, 2, torch.uint8), (torch.ones, 32, torch.float16)) * 2))
     return QuantizedKV(torch.zeros((slots, heads, head_dim), dtype=torch.int8, device=dev),
                        torch.ones((slots, heads, head_dim // 32), dtype=torch.float16, device=dev),
                        torch.zeros((slots, heads, head_dim), dtype=torch.uint8, device=dev),
@@ -704,14 +740,18 @@ def _frequencies(inv_freq: torch.Tensor, dev: torch.device) -> int:
     return 2 * inv_freq.shape[0]
 
 
-def _cache_entries(c: QuantizedKV, H: int, D: int, dev: torch.device) -> int:
-    """Slots of a cache for H heads of D channels."""
+def _cache_entries(c, H: int, D: int, dev: torch.device) -> int:
+    """Slots of a cache (8 or 4 bits) for H heads of D channels."""
     kc, ks, vc, vs = c.k_codes, c.k_scales, c.v_codes, c.v_scales
     if D % 32 != 0:
         raise ValueError("head_dim must be a multiple of 32")
     shape = kc.shape
     P = shape[0]
-    if shape != (P, H, D) or vc.shape != shape or ks.shape != (P, H, D // 32) or vs.shape != (P, H):
+    if isinstance(c, QuantizedKV4):
+        groups = (P, H, D // 32)
+        if shape != (P, H, D // 2) or vc.shape != shape or ks.shape != groups or vs.shape != groups:
+            raise ValueError(f"the cache must hold [slots, {H}, {D}] entries of 4 bits")
+    elif shape != (P, H, D) or vc.shape != shape or ks.shape != (P, H, D // 32) or vs.shape != (P, H):
         raise ValueError(f"the cache must hold [slots, {H}, {D}] entries")
     if kc.element_size() != 1 or vc.element_size() != 1 or ks.dtype != torch.float16 or vs.dtype != torch.float16:
         raise ValueError("the cache must hold 1-byte codes and float16 scales")
@@ -721,44 +761,124 @@ def _cache_entries(c: QuantizedKV, H: int, D: int, dev: torch.device) -> int:
     return P
 
 
+def rope_axes(sections, layout: str = "blocks", device: torch.device | str | None = None) -> torch.Tensor:
+    """Which axis each rotary frequency takes its position from: int32 [sum(sections)] on the GPU, for `axes=` of
+    the rotary calls, axis a having sections[a] of the frequencies.  layout "blocks": axis 0's first, then axis
+    1's, ...; "cyclic": dealt in turn (0, 1, 2, 0, 1, ...), an axis whose share is used up being passed over.
+    (An image tower whose axes repeat the same frequencies takes "blocks" and an inv_freq that repeats them.)"""
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= 16 or min(left) < 0 or sum(left) < 1:
+        raise ValueError("sections must be 1 to 16 counts >= 0, not all 0")
+    if layout == "blocks":
+        out = [a for a, n in enumerate(left) for _ in range(n)]
+    elif layout == "cyclic":
+        out = [a for i in range(max(left)) for a, n in enumerate(left) if i < n]
+    else:
+        raise ValueError('layout must be "blocks" or "cyclic"')
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    return torch.tensor(out, dtype=torch.int32, device=dev)
+
+
+def _positions(positions: torch.Tensor, axes: torch.Tensor | None, T: int, R: int, dev: torch.device):
+    """(1 for int64 positions, address of axes, number of axes) of positions [T], or [n, T] with axes."""
+    if axes is None:
+        return _indices(positions, T, dev, "positions"), None, 1
+    if axes.dtype != torch.int32 or axes.shape != (R // 2,):
+        raise ValueError(f"axes must be int32 [{R // 2}] (rope_axes)")
+    dtype, shape = positions.dtype, positions.shape
+    if (dtype != torch.int64 and dtype != torch.int32) or len(shape) != 2 or shape[1] != T or shape[0] < 1:
+        raise ValueError(f"positions must be int32 or int64 [axes, {T}]")
+    _on(dev, axes, positions)
+    return int(dtype == torch.int64), axes.data_ptr(), shape[0]
+
+
+def _head_weight(w: torch.Tensor | None, D: int, dev: torch.device, name: str):
+    if w is None:
+        return None
+    if w.dtype != torch.bfloat16 or w.shape != (D,):
+        raise ValueError(f"{name} must be bf16 [{D}]")
+    if w.device != dev or not w.is_contiguous():
+        _on(dev, w)
+    return w.data_ptr()
+
+
+def _rotated(x: torch.Tensor, out: torch.Tensor | None, name: str):
+    """The output for rotated rows x, and its token stride."""
+    if out is None:
+        return torch.empty_like(x, memory_format=torch.contiguous_format), x.shape[1] * x.shape[2]
+    stride = _token_rows(out, name)
+    if out.shape != x.shape or out.device != x.device:
+        raise ValueError(f"{name} must be bf16 {list(x.shape)} on {x.device}")
+    return out, stride
+
+
 def rope(x: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor, attention_factor: float = 1.0,
-         interleaved: bool = False, out: torch.Tensor | None = None) -> torch.Tensor:
+         interleaved: bool = False, out: torch.Tensor | None = None, axes: torch.Tensor | None = None) -> torch.Tensor:
     """Rotary positions on the first 2 * len(inv_freq) channels of x [T, H, D] bf16 (pairs (i, i + R/2), or (2i,
-    2i+1) interleaved); the token stride of x is free.  out may be x."""
+    2i+1) interleaved); the token stride of x is free.  out may be x.  With axes (rope_axes), positions are [n, T]
+    and frequency i turns with positions[axes[i]]."""
     xs = _token_rows(x, "x")
     T, H, D = x.shape
     R = _frequencies(inv_freq, x.device)
-    p64 = _indices(positions, T, x.device, "positions")
-    if out is None:
-        out, os_ = torch.empty_like(x, memory_format=torch.contiguous_format), H * D
+    p64, ax, n = _positions(positions, axes, T, R, x.device)
+    out, os_ = _rotated(x, out, "out")
+    if axes is None:
+        _enqueue(x.device, lib().qlq_rope, x.data_ptr(), xs, T, H, D, positions.data_ptr(), p64, inv_freq.data_ptr(), R,
+                 float(attention_factor), int(interleaved), out.data_ptr(), os_)
     else:
-        os_ = _token_rows(out, "out")
-        if out.shape != x.shape or out.device != x.device:
-            raise ValueError(f"out must be bf16 {list(x.shape)} on {x.device}")
-    _enqueue(x.device, lib().qlq_rope, x.data_ptr(), xs, T, H, D, positions.data_ptr(), p64, inv_freq.data_ptr(), R,
-             float(attention_factor), int(interleaved), out.data_ptr(), os_)
+        _enqueue(x.device, lib().qlq_norm_rope, x.data_ptr(), xs, None, 0, T, H, 0, D, None, None, 0.0,
+                 positions.data_ptr(), p64, ax, n, inv_freq.data_ptr(), R, float(attention_factor), int(interleaved),
+                 out.data_ptr(), os_, None, 0)
     return out
 
 
-def kv_append(k: torch.Tensor, v: torch.Tensor, cache: QuantizedKV, slots: torch.Tensor) -> QuantizedKV:
-    """Quantize k, v [T, H, D] bf16 (as kv_quantize; token strides free) into cache entries slots [T].  A slot
-    outside the cache (padding: -1) is not written; slots must not repeat.  Returns the cache."""
+def norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor | None, k_weight: torch.Tensor | None,
+              positions: torch.Tensor, inv_freq: torch.Tensor, eps: float = 1e-6, attention_factor: float = 1.0,
+              interleaved: bool = False, axes: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+              k_out: torch.Tensor | None = None):
+    """RMS norm of every head of q [T, Hq, D] and k [T, Hk, D] bf16 (weights bf16 [D]; None: no norm of that one) and
+    rotary positions, in one kernel with one rounding: (q, k).  Positions, axes and strides as for rope; q_out may be
+    q, k_out k."""
+    qs, ks = _token_rows(q, "q"), _token_rows(k, "k")
+    T, Hq, D = q.shape
+    dev = q.device
+    if k.shape[0] != T or k.shape[2] != D or k.device != dev:
+        raise ValueError("k must be [T, Hk, D] with q's T, D and device")
+    wq, wk = _head_weight(q_weight, D, dev, "q_weight"), _head_weight(k_weight, D, dev, "k_weight")
+    R = _frequencies(inv_freq, dev)
+    p64, ax, n = _positions(positions, axes, T, R, dev)
+    q_out, qos = _rotated(q, q_out, "q_out")
+    k_out, kos = _rotated(k, k_out, "k_out")
+    _enqueue(dev, lib().qlq_norm_rope, q.data_ptr(), qs, k.data_ptr(), ks, T, Hq, k.shape[1], D, wq, wk, eps,
+             positions.data_ptr(), p64, ax, n, inv_freq.data_ptr(), R, float(attention_factor), int(interleaved),
+             q_out.data_ptr(), qos, k_out.data_ptr(), kos)
+    return q_out, k_out
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, cache, slots: torch.Tensor):
+    """Quantize k, v [T, H, D] bf16 (token strides free) into entries slots [T] of a cache of 8 bits (as
+    kv_quantize) or 4.  A slot outside the cache (padding: -1) is not written; slots must not repeat.  Returns the
+    cache."""
     ks, vs = _token_rows(k, "k"), _token_rows(v, "v")
     if k.shape != v.shape or k.device != v.device:
         raise ValueError("k and v must have the same shape and device")
     T, H, D = k.shape
     P = _cache_entries(cache, H, D, k.device)
     s64 = _indices(slots, T, k.device, "slots")
-    _enqueue(k.device, lib().qlq_kv_append, k.data_ptr(), ks, v.data_ptr(), vs, T, H, D, slots.data_ptr(), s64, P,
+    fn = lib().qlq_kv4_append if isinstance(cache, QuantizedKV4) else lib().qlq_kv_append
+    _enqueue(k.device, fn, k.data_ptr(), ks, v.data_ptr(), vs, T, H, D, slots.data_ptr(), s64, P,
              cache.k_codes.data_ptr(), cache.k_scales.data_ptr(), cache.v_codes.data_ptr(), cache.v_scales.data_ptr())
     return cache
 
 
 def rope_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, inv_freq: torch.Tensor,
-                   cache: QuantizedKV, slots: torch.Tensor, attention_factor: float = 1.0, interleaved: bool = False,
-                   q_out: torch.Tensor | None = None) -> torch.Tensor:
+                   cache, slots: torch.Tensor, attention_factor: float = 1.0, interleaved: bool = False,
+                   q_out: torch.Tensor | None = None, axes: torch.Tensor | None = None) -> torch.Tensor:
     """rope of q [T, Hq, D] and k [T, Hk, D], and kv_append of the rotated k and of v, in one kernel.  q, k and v
     may be views of one projection's output.  Returns the rotated q (q_out may be q)."""
+    if axes is not None or isinstance(cache, QuantizedKV4):
+        return norm_rope_kv_append(q, k, v, None, None, positions, inv_freq, cache, slots,
+                                   attention_factor=attention_factor, interleaved=interleaved, axes=axes, q_out=q_out)
     qs, ks, vs = _token_rows(q, "q"), _token_rows(k, "k"), _token_rows(v, "v")
     T, Hq, D = q.shape
     dev = q.device
@@ -768,12 +888,7 @@ def rope_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions:
     P = _cache_entries(cache, Hk, D, dev)
     R = _frequencies(inv_freq, dev)
     p64, s64 = _indices(positions, T, dev, "positions"), _indices(slots, T, dev, "slots")
-    if q_out is None:
-        q_out, os_ = torch.empty_like(q, memory_format=torch.contiguous_format), Hq * D
-    else:
-        os_ = _token_rows(q_out, "q_out")
-        if q_out.shape != q.shape or q_out.device != dev:
-            raise ValueError(f"q_out must be bf16 {list(q.shape)} on {dev}")
+    q_out, os_ = _rotated(q, q_out, "q_out")
     _enqueue(dev, lib().qlq_rope_kv_append, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, Hq, Hk, D,
              positions.data_ptr(), p64, inv_freq.data_ptr(), R, float(attention_factor), int(interleaved),
              slots.data_ptr(), s64, P, cache.k_codes.data_ptr(), cache.k_scales.data_ptr(), cache.v_codes.data_ptr(),
@@ -781,13 +896,43 @@ def rope_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions:
     return q_out
 
 
-def kv_gather(cache: QuantizedKV, slots: torch.Tensor, k_out: torch.Tensor | None = None,
+def norm_rope_kv_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_weight: torch.Tensor | None,
+                        k_weight: torch.Tensor | None, positions: torch.Tensor, inv_freq: torch.Tensor, cache,
+                        slots: torch.Tensor, eps: float = 1e-6, attention_factor: float = 1.0,
+                        interleaved: bool = False, axes: torch.Tensor | None = None,
+                        q_out: torch.Tensor | None = None) -> torch.Tensor:
+    """norm_rope of q and k, and kv_append of that k and of v into a cache of 8 or 4 bits, in one kernel (k is
+    quantized from its unrounded value).  Returns the rotated q (q_out may be q)."""
+    qs, ks, vs = _token_rows(q, "q"), _token_rows(k, "k"), _token_rows(v, "v")
+    T, Hq, D = q.shape
+    dev = q.device
+    if k.shape != v.shape or k.shape[0] != T or k.shape[2] != D or k.device != dev or v.device != dev:
+        raise ValueError("k and v must be [T, Hk, D] with q's T, D and device")
+    Hk = k.shape[1]
+    P = _cache_entries(cache, Hk, D, dev)
+    wq, wk = _head_weight(q_weight, D, dev, "q_weight"), _head_weight(k_weight, D, dev, "k_weight")
+    R = _frequencies(inv_freq, dev)
+    p64, ax, n = _positions(positions, axes, T, R, dev)
+    s64 = _indices(slots, T, dev, "slots")
+    q_out, os_ = _rotated(q, q_out, "q_out")
+    _enqueue(dev, lib().qlq_norm_rope_kv_append, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, T, Hq, Hk, D,
+             wq, wk, eps, positions.data_ptr(), p64, ax, n, inv_freq.data_ptr(), R, float(attention_factor),
+             int(interleaved), slots.data_ptr(), s64, P, 4 if isinstance(cache, QuantizedKV4) else 8,
+             cache.k_codes.data_ptr(), cache.k_scales.data_ptr(), cache.v_codes.data_ptr(), cache.v_scales.data_ptr(),
+             q_out.data_ptr(), os_)
+    return q_out
+
+
+def kv_gather(cache, slots: torch.Tensor, k_out: torch.Tensor | None = None,
               v_out: torch.Tensor | None = None):
-    """Cache entries slots [n] as dense bf16 (K, V) [n, H, D]; zeros for a slot outside the cache."""
+    """Entries slots [n] of a cache of 8 or 4 bits as dense bf16 (K, V) [n, H, D]; zeros for a slot outside it."""
     dev = cache.k_codes.device
     if not cache.k_codes.is_cuda:
         raise ValueError("qlq operates on GPU tensors only")
     _, H, D = cache.k_codes.shape
+    four = isinstance(cache, QuantizedKV4)
+    if four:
+        D *= 2
     P = _cache_entries(cache, H, D, dev)
     n = slots.shape[0] if slots.dim() == 1 else -1
     s64 = _indices(slots, n, dev, "slots")
@@ -800,15 +945,19 @@ def kv_gather(cache: QuantizedKV, slots: torch.Tensor, k_out: torch.Tensor | Non
         else:
             _on(dev, t)
         outs.append(t)
-    _enqueue(dev, lib().qlq_kv_gather, cache.k_codes.data_ptr(), cache.k_scales.data_ptr(), cache.v_codes.data_ptr(),
+    _enqueue(dev, lib().qlq_kv4_gather if four else lib().qlq_kv_gather, cache.k_codes.data_ptr(), cache.k_scales.data_ptr(), cache.v_codes.data_ptr(),
              cache.v_scales.data_ptr(), P, H, D, slots.data_ptr(), s64, n, outs[0].data_ptr(), outs[1].data_ptr())
     return outs[0], outs[1]
 
 
 @functools.lru_cache(maxsize=1024)
-def kv_attention_workspace_bytes(T: int, B: int, Hq: int, Hk: int, D: int, one_each: bool = True) -> int:
-    """Workspace of kv_attention for T query tokens of B sequences (one_each: without q_start)."""
-    return int(lib().qlq_kv_attention_workspace_bytes(T, B, Hq, Hk, D, int(one_each)))
+def kv_attention_workspace_bytes(T: int, B: int, Hq: int, Hk: int, D: int, one_each: bool = True, bits: int = 8) -> int:
+    """Workspace of kv_attention for T query tokens of B sequences (one_each: without q_start) over a cache of 8
+    bits or 4."""
+    if bits not in (4, 8):
+        raise ValueError("a cache has 4 or 8 bits")
+    fn = lib().qlq_kv4_attention_workspace_bytes if bits == 4 else lib().qlq_kv_attention_workspace_bytes
+    return int(fn(T, B, Hq, Hk, D, int(one_each)))
 
 
 _ATTENTION_COUNTER_BYTES = 262144
@@ -835,11 +984,11 @@ def _attention_workspace(dev: torch.device, nbytes: int) -> torch.Tensor:
     return ws
 
 
-def kv_attention(q: torch.Tensor, cache: QuantizedKV, block_table: torch.Tensor, seq_lens: torch.Tensor,
+def kv_attention(q: torch.Tensor, cache, block_table: torch.Tensor, seq_lens: torch.Tensor,
                  page_size: int, q_start: torch.Tensor | None = None, scale: float | None = None, causal: bool = True,
                  window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
                  workspace: torch.Tensor | None = None) -> torch.Tensor:
-    """Attention of q [T, Hq, D] bf16 over a paged cache (kv_append): out bf16 [T, Hq, D].
+    """Attention of q [T, Hq, D] bf16 over a paged cache of 8 or 4 bits (kv_append): out bf16 [T, Hq, D].
 
     block_table int32 [B, pages] holds each sequence's page numbers (token t is cache entry
     block_table[b][t // page_size] * page_size + t % page_size; page_size a power of two from 16), seq_lens int32
@@ -851,8 +1000,8 @@ def kv_attention(q: torch.Tensor, cache: QuantizedKV, block_table: torch.Tensor,
     The lengths stay on the device: nothing here waits for them.  One kernel is chosen for all rows by their average
     per sequence, so prompts and single tokens are faster in a call each.
 
-    workspace: uint8, zeros before its first use, of kv_attention_workspace_bytes(T, B, Hq, Hk, D, q_start is None)
-    bytes or more, for this function's calls on one stream at a time.  Without it, one is kept per stream; in a graph
+    workspace: uint8, zeros before its first use, of kv_attention_workspace_bytes(T, B, Hq, Hk, D, q_start is None,
+    bits) bytes or more, for this function's calls on one stream at a time.  Without it, one is kept per stream; in a graph
     capture every call gets its own and records its zero fill (2 us), which one workspace for all of a graph's
     calls saves."""
     qs = _token_rows(q, "q")
@@ -862,6 +1011,7 @@ def kv_attention(q: torch.Tensor, cache: QuantizedKV, block_table: torch.Tensor,
         raise ValueError("the cache must hold [slots, heads, head_dim] entries")
     Hk = cache.k_codes.shape[1]
     P = _cache_entries(cache, Hk, D, dev)
+    four = isinstance(cache, QuantizedKV4)
     if block_table.dim() != 2 or block_table.dtype != torch.int32:
         raise ValueError("block_table must be int32 [B, pages]")
     B = block_table.shape[0]
@@ -877,8 +1027,8 @@ def kv_attention(q: torch.Tensor, cache: QuantizedKV, block_table: torch.Tensor,
         raise ValueError(f"lse must be fp32 [{T}, {Hq}]")
     _on(dev, block_table, seq_lens, q_start, out, lse, workspace)
     if workspace is None:
-        workspace = _attention_workspace(dev, kv_attention_workspace_bytes(T, B, Hq, Hk, D, q_start is None))
-    _enqueue(dev, lib().qlq_kv_attention, q.data_ptr(), qs, T, B, Hq, Hk, D, cache.k_codes.data_ptr(),
+        workspace = _attention_workspace(dev, kv_attention_workspace_bytes(T, B, Hq, Hk, D, q_start is None, 4 if four else 8))
+    _enqueue(dev, lib().qlq_kv4_attention if four else lib().qlq_kv_attention, q.data_ptr(), qs, T, B, Hq, Hk, D, cache.k_codes.data_ptr(),
              cache.k_scales.data_ptr(), cache.v_codes.data_ptr(), cache.v_scales.data_ptr(), P,
              block_table.data_ptr(), block_table.shape[1], page_size, seq_lens.data_ptr(), _addr(q_start),
              D ** -0.5 if scale is None else float(scale), int(causal), int(window), out.data_ptr(), _addr(lse),

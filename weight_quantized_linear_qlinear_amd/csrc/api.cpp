@@ -977,6 +977,150 @@ qlq_status qlq_kv_gather(const void* k_codes, const void* k_scales, const void* 
                     "kv_gather");
 }
 
+// Norm weights, axes and outputs of a norm_rope call into a.
+static qlq_status norm_rope_args(qlq::NormRopeArgs& a, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                 int64_t T, int64_t Hq, int64_t Hk, int64_t D, const void* q_weight,
+                                 const void* k_weight, float eps, const void* positions, int positions_64,
+                                 const int32_t* axes, int64_t n_axes, const double* inv_freq, int64_t rotary_dim,
+                                 float factor, int interleaved, void* q_out, int64_t q_out_stride) {
+  if (qlq_status st = check_rotary(positions, inv_freq, rotary_dim, D, factor)) return st;
+  if (n_axes < 1 || n_axes > 16) return fail(QLQ_ERR_INVALID_ARG, "n_axes must be 1 .. 16");
+  if (n_axes > 1 && !axes) return fail(QLQ_ERR_INVALID_ARG, "several axes need the axis of each frequency");
+  if ((q_weight || k_weight) && (!std::isfinite(eps) || !(eps > 0.0f)))
+    return fail(QLQ_ERR_INVALID_ARG, "eps must be finite and > 0");
+  if (qlq_status st = check_stride(q_stride, T, Hq, D, "q")) return st;
+  if (qlq_status st = check_stride(k_stride, T, Hk, D, "k")) return st;
+  if (qlq_status st = check_stride(q_out_stride, T, Hq, D, "q_out")) return st;
+  if (q && q == q_out && q_stride != q_out_stride && T > 1)
+    return fail(QLQ_ERR_INVALID_ARG, "rotating in place needs equal strides");
+  if (!aligned(q, 2) || !aligned(k, 2) || !aligned(q_out, 2) || !aligned(q_weight, 2) || !aligned(k_weight, 2) ||
+      !aligned(positions, positions_64 ? 8 : 4) || !aligned(axes, 4))
+    return fail(QLQ_ERR_INVALID_ARG, "misaligned pointer");
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.q_out_stride = q_out_stride;
+  a.wq = static_cast<const uint16_t*>(q_weight);
+  a.wk = static_cast<const uint16_t*>(k_weight);
+  a.eps = eps;
+  a.positions = positions;
+  a.pos64 = positions_64 ? 1 : 0;
+  a.axes = n_axes > 1 ? axes : nullptr;
+  a.A = (int)n_axes;
+  a.inv_freq = inv_freq;
+  a.factor = factor;
+  a.R = (int)rotary_dim;
+  a.interleaved = interleaved ? 1 : 0;
+  a.T = (int)T;
+  a.Hq = (int)Hq;
+  a.Hk = (int)Hk;
+  a.D = (int)D;
+  a.vec_in = rows16(q, q_stride, D) && rows16(k, k_stride, D);
+  a.vec_out = rows16(q_out, q_out_stride, D);
+  a.vec_w = aligned(q_weight, 16) && aligned(k_weight, 16);
+  return QLQ_OK;
+}
+
+qlq_status qlq_norm_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, int64_t T, int64_t Hq,
+                         int64_t Hk, int64_t D, const void* q_weight, const void* k_weight, float eps,
+                         const void* positions, int positions_64, const int32_t* axes, int64_t n_axes,
+                         const double* inv_freq, int64_t rotary_dim, float factor, int interleaved, void* q_out,
+                         int64_t q_out_stride, void* k_out, int64_t k_out_stride, hipStream_t stream) {
+  if (!q || !q_out || (Hk > 0 && (!k || !k_out))) return fail(QLQ_ERR_INVALID_ARG, "null pointer");
+  if (Hq < 1) return fail(QLQ_ERR_INVALID_ARG, "T, heads and D must be >= 1");
+  if (qlq_status st = check_heads(T, Hq, Hk, D, 8)) return st;
+  if (Hk == 0) k = k_out = nullptr, k_weight = nullptr;
+  qlq::NormRopeArgs a{};
+  if (qlq_status st = norm_rope_args(a, q, q_stride, k, k_stride, T, Hq, Hk, D, q_weight, k_weight, eps, positions,
+                                     positions_64, axes, n_axes, inv_freq, rotary_dim, factor, interleaved, q_out,
+                                     q_out_stride))
+    return st;
+  if (qlq_status st = check_stride(k_out_stride, T, Hk, D, "k_out")) return st;
+  if (k && k == k_out && k_stride != k_out_stride && T > 1)
+    return fail(QLQ_ERR_INVALID_ARG, "rotating in place needs equal strides");
+  if (!aligned(k_out, 2)) return fail(QLQ_ERR_INVALID_ARG, "misaligned pointer");
+  a.k_out = static_cast<uint16_t*>(k_out);
+  a.k_out_stride = k_out_stride;
+  a.vec_out = a.vec_out && rows16(k_out, k_out_stride, D);
+  return hip_status(qlq::launch_norm_rope(a, 0, stream), "norm_rope");
+}
+
+static void cache_args(qlq::NormRopeArgs& a, const void* v, int64_t v_stride, int64_t D, const void* slots,
+                       int slots_64, int64_t pool, void* k_codes, void* k_scales, void* v_codes, void* v_scales) {
+  a.v = static_cast<const uint16_t*>(v);
+  a.v_stride = v_stride;
+  a.slots = slots;
+  a.slot64 = slots_64 ? 1 : 0;
+  a.pool = pool;
+  a.k_codes = static_cast<uint8_t*>(k_codes);
+  a.k_scales = static_cast<uint16_t*>(k_scales);
+  a.v_codes = static_cast<uint8_t*>(v_codes);
+  a.v_scales = static_cast<uint16_t*>(v_scales);
+  a.vec_in = a.vec_in && rows16(v, v_stride, D);
+}
+
+static qlq_status check_bits(int bits) {
+  return bits == 4 || bits == 8 ? QLQ_OK : fail(QLQ_ERR_UNSUPPORTED, "a cache has 4 or 8 bits, not %d", bits);
+}
+
+qlq_status qlq_norm_rope_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                   int64_t v_stride, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
+                                   const void* q_weight, const void* k_weight, float eps, const void* positions,
+                                   int positions_64, const int32_t* axes, int64_t n_axes, const double* inv_freq,
+                                   int64_t rotary_dim, float factor, int interleaved, const void* slots, int slots_64,
+                                   int64_t pool, int bits, void* k_codes, void* k_scales, void* v_codes,
+                                   void* v_scales, void* q_out, int64_t q_out_stride, hipStream_t stream) {
+  if (!q || !k || !v || !q_out) return fail(QLQ_ERR_INVALID_ARG, "null pointer");
+  if (Hq < 1 || Hk < 1) return fail(QLQ_ERR_INVALID_ARG, "T, heads and D must be >= 1");
+  if (qlq_status st = check_bits(bits)) return st;
+  if (qlq_status st = check_heads(T, Hq, Hk, D, 32)) return st;
+  qlq::NormRopeArgs a{};
+  if (qlq_status st = norm_rope_args(a, q, q_stride, k, k_stride, T, Hq, Hk, D, q_weight, k_weight, eps, positions,
+                                     positions_64, axes, n_axes, inv_freq, rotary_dim, factor, interleaved, q_out,
+                                     q_out_stride))
+    return st;
+  if (qlq_status st = check_stride(v_stride, T, Hk, D, "v")) return st;
+  if (qlq_status st = check_cache(k_codes, k_scales, v_codes, v_scales, slots, slots_64, pool)) return st;
+  if (!aligned(v, 2)) return fail(QLQ_ERR_INVALID_ARG, "misaligned pointer");
+  cache_args(a, v, v_stride, D, slots, slots_64, pool, k_codes, k_scales, v_codes, v_scales);
+  return hip_status(qlq::launch_norm_rope(a, bits, stream), "norm_rope_kv_append");
+}
+
+qlq_status qlq_kv4_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t T, int64_t H,
+                          int64_t D, const void* slots, int slots_64, int64_t pool, void* k_codes, void* k_scales,
+                          void* v_codes, void* v_scales, hipStream_t stream) {
+  if (!k || !v) return fail(QLQ_ERR_INVALID_ARG, "null pointer");
+  if (qlq_status st = check_heads(T, 0, H, D, 32)) return st;
+  if (qlq_status st = check_stride(k_stride, T, H, D, "k")) return st;
+  if (qlq_status st = check_stride(v_stride, T, H, D, "v")) return st;
+  if (qlq_status st = check_cache(k_codes, k_scales, v_codes, v_scales, slots, slots_64, pool)) return st;
+  if (!aligned(k, 2) || !aligned(v, 2)) return fail(QLQ_ERR_INVALID_ARG, "misaligned pointer");
+  qlq::NormRopeArgs a{};
+  a.k = static_cast<const uint16_t*>(k);
+  a.k_stride = k_stride;
+  a.T = (int)T;
+  a.Hk = (int)H;
+  a.D = (int)D;
+  a.A = 1;
+  a.vec_in = rows16(k, k_stride, D);
+  cache_args(a, v, v_stride, D, slots, slots_64, pool, k_codes, k_scales, v_codes, v_scales);
+  return hip_status(qlq::launch_norm_rope(a, 4, stream), "kv4_append");
+}
+
+qlq_status qlq_kv4_gather(const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                          int64_t pool, int64_t H, int64_t D, const void* slots, int slots_64, int64_t n, void* k_bf16,
+                          void* v_bf16, hipStream_t stream) {
+  if (!k_bf16 || !v_bf16) return fail(QLQ_ERR_INVALID_ARG, "null pointer");
+  if (qlq_status st = check_heads(n, 0, H, D, 32)) return st;
+  if (qlq_status st = check_cache(k_codes, k_scales, v_codes, v_scales, slots, slots_64, pool)) return st;
+  if (!aligned(k_bf16, 16) || !aligned(v_bf16, 16)) return fail(QLQ_ERR_INVALID_ARG, "outputs must be 16-byte aligned");
+  return hip_status(qlq::launch_kv4_gather(k_codes, k_scales, v_codes, v_scales, pool, (int)H, (int)D, slots,
+                                           slots_64 ? 1 : 0, n, k_bf16, v_bf16, stream),
+                    "kv4_gather");
+}
+
 // Attention workspace: a counter region of one fixed size for every plan (so that one call's
 // partial sums never land on another's counters), then two partial tiles per wave.  Counters: one
 // per level of joining (three), slot, head and (many rows) wave.
@@ -992,17 +1136,30 @@ static size_t attn_partial_bytes(const qlq::KvAttnPlan& p, int64_t Hk, int64_t D
   return (size_t)p.waves * 2 * (size_t)Hk * (size_t)p.tile_rows * (size_t)(D + 4) * 4;
 }
 
-size_t qlq_kv_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int one_each) {
+static qlq::KvAttnPlan plan_attention(int bits, int64_t T, int64_t B, int64_t Hk, int64_t G, int64_t D, bool one_each) {
+  return bits == 4 ? qlq::plan_kv4_attention(T, B, Hk, G, D, one_each) : qlq::plan_kv_attention(T, B, Hk, G, D, one_each);
+}
+
+static size_t attn_workspace_bytes(int bits, int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int one_each) {
   if (!attn_dims_ok(T, B, Hq, Hk, D) || (one_each && T != B)) return 0;
-  const qlq::KvAttnPlan p = qlq::plan_kv_attention(T, B, Hk, Hq / Hk, D, one_each != 0);
+  const qlq::KvAttnPlan p = plan_attention(bits, T, B, Hk, Hq / Hk, D, one_each != 0);
   return (kAttnCounterBytes + attn_partial_bytes(p, Hk, D) + 255) / 256 * 256;
 }
 
-qlq_status qlq_kv_attention(const void* q, int64_t q_stride, int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D,
-                            const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
-                            int64_t pool, const int32_t* block_table, int64_t max_pages, int64_t page_size,
-                            const int32_t* seq_lens, const int32_t* q_start, float scale, int causal, int64_t window,
-                            void* out, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+size_t qlq_kv_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int one_each) {
+  return attn_workspace_bytes(8, T, B, Hq, Hk, D, one_each);
+}
+
+size_t qlq_kv4_attention_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D, int one_each) {
+  return attn_workspace_bytes(4, T, B, Hq, Hk, D, one_each);
+}
+
+static qlq_status run_attention(int bits, const void* q, int64_t q_stride, int64_t T, int64_t B, int64_t Hq, int64_t Hk,
+                                int64_t D, const void* k_codes, const void* k_scales, const void* v_codes,
+                                const void* v_scales, int64_t pool, const int32_t* block_table, int64_t max_pages,
+                                int64_t page_size, const int32_t* seq_lens, const int32_t* q_start, float scale,
+                                int causal, int64_t window, void* out, float* lse, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream) {
   if (!q || !out || !block_table || !seq_lens) return fail(QLQ_ERR_INVALID_ARG, "null pointer");
   if (T < 1 || B < 1 || Hq < 1 || Hk < 1 || max_pages < 1) return fail(QLQ_ERR_INVALID_ARG, "sizes must be >= 1");
   if (Hq % Hk != 0) return fail(QLQ_ERR_INVALID_ARG, "query heads (%lld) must be a multiple of KV heads (%lld)",
@@ -1017,7 +1174,7 @@ qlq_status qlq_kv_attention(const void* q, int64_t q_stride, int64_t T, int64_t 
   if (page_size < 16 || page_size > (1 << 20) || (page_size & (page_size - 1)) != 0)
     return fail(QLQ_ERR_INVALID_ARG, "page_size must be a power of two, 16 .. 2^20");
   if (qlq_status st = check_cache(k_codes, k_scales, v_codes, v_scales, block_table, 0, pool)) return st;
-  if (!aligned(k_scales, 16)) return fail(QLQ_ERR_INVALID_ARG, "cache scales must be 16-byte aligned");
+  if (!aligned(k_scales, 16) || (bits == 4 && !aligned(v_scales, 16))) return fail(QLQ_ERR_INVALID_ARG, "cache scales must be 16-byte aligned");
   if (pool % page_size != 0) return fail(QLQ_ERR_INVALID_ARG, "the cache's slots must be a multiple of page_size");
   if (max_pages * page_size >= (int64_t(1) << 31) - 65536)
     return fail(QLQ_ERR_INVALID_ARG, "max_pages * page_size must be below 2^31 - 65536");
@@ -1026,7 +1183,7 @@ qlq_status qlq_kv_attention(const void* q, int64_t q_stride, int64_t T, int64_t 
   if (window > 0 && !causal) return fail(QLQ_ERR_INVALID_ARG, "a window needs causal attention");
   if (!aligned(out, 16) || !aligned(seq_lens, 4) || !aligned(q_start, 4) || !aligned(lse, 4))
     return fail(QLQ_ERR_INVALID_ARG, "misaligned pointer");
-  const qlq::KvAttnPlan p = qlq::plan_kv_attention(T, B, Hk, Hq / Hk, D, q_start == nullptr);
+  const qlq::KvAttnPlan p = plan_attention(bits, T, B, Hk, Hq / Hk, D, q_start == nullptr);
   const size_t partial = attn_partial_bytes(p, Hk, D), need = kAttnCounterBytes + partial;
   // The kernels count units (32 tokens of a query tile) and a sequence's query rows in 32 bits, units
   // up to one for every wave past the last.
@@ -1070,7 +1227,28 @@ qlq_status qlq_kv_attention(const void* q, int64_t q_stride, int64_t T, int64_t 
   a.counters = static_cast<uint32_t*>(workspace);
   a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAttnCounterBytes);
   a.partials_bytes = (uint32_t)partial;
-  return hip_status(qlq::launch_kv_attention(a, p, (int)D, stream), "kv_attention");
+  return bits == 4 ? hip_status(qlq::launch_kv4_attention(a, p, (int)D, stream), "kv4_attention")
+                   : hip_status(qlq::launch_kv_attention(a, p, (int)D, stream), "kv_attention");
+}
+
+qlq_status qlq_kv_attention(const void* q, int64_t q_stride, int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D,
+                            const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                            int64_t pool, const int32_t* block_table, int64_t max_pages, int64_t page_size,
+                            const int32_t* seq_lens, const int32_t* q_start, float scale, int causal, int64_t window,
+                            void* out, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return run_attention(8, q, q_stride, T, B, Hq, Hk, D, k_codes, k_scales, v_codes, v_scales, pool, block_table,
+                       max_pages, page_size, seq_lens, q_start, scale, causal, window, out, lse, workspace,
+                       workspace_bytes, stream);
+}
+
+qlq_status qlq_kv4_attention(const void* q, int64_t q_stride, int64_t T, int64_t B, int64_t Hq, int64_t Hk, int64_t D,
+                             const void* k_codes, const void* k_scales, const void* v_codes, const void* v_scales,
+                             int64_t pool, const int32_t* block_table, int64_t max_pages, int64_t page_size,
+                             const int32_t* seq_lens, const int32_t* q_start, float scale, int causal, int64_t window,
+                             void* out, float* lse, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  return run_attention(4, q, q_stride, T, B, Hq, Hk, D, k_codes, k_scales, v_codes, v_scales, pool, block_table,
+                       max_pages, page_size, seq_lens, q_start, scale, causal, window, out, lse, workspace,
+                       workspace_bytes, stream);
 }
 
 // ------------------------------------------------------------------ test hooks

@@ -1,0 +1,434 @@
+// Attention over the paged 4-bit KV cache (K and V e2m1 with an fp16 scale per 32 channels, rows in
+// the order of kv_rows.h), for few query rows per KV head.  The definition, the cutting of the work
+// and the joining are kv_attention.hip's; what differs is how a tile of 32 tokens is computed:
+//   s_t = scale * sum_c k_scale[t,c] * (q_c . k_code[t,c])      (c: groups of 32 channels)
+//   e_t = 2^(s_t log2e - m),  l = sum_t e_t,  o_c = sum_t fp16(e_t v_scale[t,c]) v_code[t,c],  out = o / l
+// m is a running reference, 15 octaves below the largest s_t log2e + E_t seen, where 2^E_t bounds token
+// t's V scales: so every weight e_t v_scale fits fp16, has its 11 bits down to 2^-29 of the row's
+// largest, and is rounded once.  Codes are exact in fp16, q is scaled per row by a power of two into
+// [-1, 1) (as in kv_attention.hip); sums are fp32.
+//
+// Layout.  S^T = K Q^T: the lane of token l % 16 and channel group l / 16 has, in the cache's order, its
+// eight channels of every group of 32 side by side: one load, and no byte moves before the conversion
+// (two codes per instruction).  O^T = V^T P^T: lane column c has channels 2 c, 2 c + 1 of every group;
+// nibbles of two tokens are put into one byte, which the conversion turns into the pair that the
+// matrix unit wants.  Scales come one token per lane (K's in the lower, V's in the upper half of the
+// wave) and reach the lanes of the scores through the wave's LDS, in the order of their tokens there.
+#include <type_traits>
+
+#include "kv_attention.h"
+
+namespace qlq {
+
+using namespace attn;
+
+namespace {
+
+// The runs of groups of a 4-bit row: NG <= 8, no 5 or 7: at most two.
+template <int NG>
+struct Runs {
+  static constexpr int P1 = NG >= 8 ? 8 : NG >= 4 ? 4 : NG >= 2 ? 2 : 1, P2 = NG - P1;
+  static_assert(P2 == 0 || P2 == 1 || P2 == 2, "two runs of a power of two");
+};
+
+// BYTES (1 .. 32, a power of two) at p, aligned to 16 at the most, as dwords.
+template <int BYTES>
+struct Bytes {
+  static constexpr int N = BYTES < 4 ? 1 : BYTES / 4;
+  uint32_t d[N];
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    if constexpr (BYTES == 0) {
+      d[0] = 0;
+    } else if constexpr (BYTES == 1) {
+      d[0] = *p;
+    } else if constexpr (BYTES == 2) {
+      d[0] = *reinterpret_cast<const uint16_t*>(p);
+    } else if constexpr (BYTES == 4) {
+      d[0] = *reinterpret_cast<const uint32_t*>(p);
+    } else if constexpr (BYTES == 8) {
+      const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+      d[0] = v.x, d[1] = v.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < BYTES / 16; ++i) {
+        const u32x4 v = ld16(p + 16 * i);
+        d[4 * i] = v.x, d[4 * i + 1] = v.y, d[4 * i + 2] = v.z, d[4 * i + 3] = v.w;
+      }
+    }
+  }
+};
+
+// Octaves from a row's reference up to its largest weight: 2^15 is the largest power of two in fp16.
+constexpr float kLift = 15.0f;
+
+constexpr int waves_of(int NG) { return NG <= 4 ? 8 : 4; }
+constexpr bool pairs_rows(int NG) { return NG == 3 || NG == 4; }
+
+// A wave's LDS: the token scales of its tile, in the order in which lanes hold the tokens (lane group
+// g: 4 g .. 4 g + 3, then 16 more), or what joining needs.
+template <int NG>
+union WaveLds {
+  struct {
+    uint16_t s[2][NG][32];       // K, V scales (fp16) by group
+    float ev[32];                // exponents that bound the V scales
+  };
+  JoinLds join;
+};
+
+template <int NG, int R>
+__global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttnArgs a) {
+  constexpr int D = 32 * NG, TR = 16 * R, kWaves = waves_of(NG), P1 = Runs<NG>::P1, P2 = Runs<NG>::P2;
+  constexpr bool kTwo = P2 > 0;
+  __shared__ __align__(16) WaveLds<NG> lds[kWaves];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  WaveLds<NG>& mine = lds[wave];
+  // Neighbouring KV heads per workgroup, one per wave, and kWaves / HW waves on a head's line; the
+  // head groups of one part sit on one XCD (workgroup b goes to XCD b % 8).
+  const int HW = 1 << a.hw_shift, HG = a.Hk >> a.hw_shift, TS = kWaves >> a.hw_shift;
+  int part = blockIdx.x / HG, hg = blockIdx.x % HG;
+  if (a.parts % 8 == 0) {
+    const int li = blockIdx.x >> 3;
+    part = (li / HG) * 8 + (blockIdx.x & 7);
+    hg = li % HG;
+  }
+  const int h = hg * HW + (wave & (HW - 1)), me = part * TS + (wave >> a.hw_shift);   // head, place on its line
+  const Extent mine_e = lane < a.B ? extent_of(a, lane) : Extent{};
+  const int total = total_units<TR>(a, mine_e, lane);
+  const int U = max(1, (total + a.parts * TS - 1) / (a.parts * TS)), u_end = min(total, (me + 1) * U);
+  for (int u = me * U; u < u_end;) {
+    const Tile it = tile_of<TR>(a, mine_e, u, lane);
+    if (it.units == 0) break;                                  // (only if lengths change meanwhile or overflow the sum)
+    const int u_next = min(u_end, it.begin + it.units);
+    const int wf = it.begin / U;                               // this tile's chunks: one per wave that its units reach
+    const Chunks ck{wf, (it.begin + it.units - 1) / U - wf + 1, me - wf};
+    const int nq = it.e.nq, L = it.e.L, r0 = it.qt * TR, rows = nq * a.G;
+    const int i0 = r0 / a.G, i1 = min(nq - 1, (r0 + TR - 1) / a.G);
+    const int p0 = L - nq;                                     // position of query 0
+    const int tend = min(max(a.causal ? p0 + i1 + 1 : L, 0), L);
+    const int tmin = a.window > 0 ? min(max(0, p0 + i0 - a.window + 1), tend) : 0;      // the first token that a row sees
+    const int tbeg = tmin & ~31;
+    const int begin = begin_of(a, it.e);
+    const int c0 = max(tbeg, begin + 32 * (u - it.begin));     // a multiple of 32
+    const int c1 = min(tend, begin + 32 * (u_next - it.begin));
+    u = u_next;
+
+    int c16 = lane & 15, g4 = lane >> 4;
+    asm volatile("" : "+v"(c16), "+v"(g4));                    // (nothing computed from them outlives a tile)
+
+    // q's rows (packed: query token, then head of the group), channels 32 n + 8 g4 .. + 7.
+    u32x4 qraw[R][NG];
+    int qpos[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int row = r0 + 16 * r + c16;
+      const bool live = row < rows;
+      const int i = live ? row / a.G : i0, g = live ? row - i * a.G : 0;
+      qpos[r] = live ? p0 + i : -1;
+      const uint16_t* qp = a.q + (int64_t)(it.e.qs + i) * a.q_stride + (int64_t)(h * a.G + g) * D + 8 * g4;
+#pragma unroll
+      for (int n = 0; n < NG; ++n) qraw[r][n] = ld16(qp + 32 * n);
+    }
+
+    f32x4 o[NG][2][R];
+    float m[R], l[R];
+#pragma unroll
+    for (int n = 0; n < NG; ++n)
+#pragma unroll
+      for (int r = 0; r < R; ++r) o[n][0][r] = o[n][1][r] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int r = 0; r < R; ++r) m[r] = kNegInf, l[r] = 0.0f;
+
+    // Tiles start at multiples of 32 tokens and pages hold 16 or more, so each half of a tile lies in
+    // one page, whose first entry is uniform.  -1: the page is outside the pool (its tokens are left out).
+    const int hk = a.Hk, page_mask = (1 << a.page_shift) - 1;
+    const ConstInt* table = (const ConstInt*)(uintptr_t)(a.block_table + (int64_t)it.b * a.max_pages);
+    auto page_of = [&](int t) { return table[min(t, a.max_tokens - 1) >> a.page_shift]; };
+    auto entry_of = [&](int page, int t) {
+      return page >= 0 && page < a.pages ? (page << a.page_shift) + (t & page_mask) : -1;
+    };
+    const uint32_t row_bytes = (uint32_t)hk * (D / 2);         // from one token to the next
+    const uint32_t koff = c16 * row_bytes + 4 * P1 * g4, koff2 = c16 * row_bytes + 16 * P1 + 4 * P2 * g4;
+    const uint32_t voff = 4 * g4 * row_bytes + P1 * c16, voff2 = 4 * g4 * row_bytes + 16 * P1 + P2 * c16;
+
+    Bytes<4 * P1> k1[2];
+    Bytes<4 * P2> k2[2];
+    Bytes<P1> v1[8];
+    Bytes<P2> v2[8];
+    KScales<NG> sc;                                            // lanes 0 .. 31: K scales of token lane, 32 .. 63: V's
+    auto load_k = [&](int e0, int e1) {                        // and the scales
+      const int64_t at = ((int64_t)(max(lane & 16 ? e1 : e0, 0) + c16)) * hk + h;
+      sc.load((lane < 32 ? a.k_scales : a.v_scales) + at * NG);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint8_t* p = a.k_codes + ((int64_t)max(u ? e1 : e0, 0) * hk + h) * (D / 2);
+        k1[u].load(p + koff);
+        if constexpr (kTwo) k2[u].load(p + koff2);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    auto load_v = [&](int e0, int e1) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint8_t* p = a.v_codes + ((int64_t)max(u ? e1 : e0, 0) * hk + h) * (D / 2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v1[4 * u + j].load(p + (size_t)j * row_bytes + voff);
+          if constexpr (kTwo) v2[4 * u + j].load(p + (size_t)j * row_bytes + voff2);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    int e0 = entry_of(page_of(c0), c0), e1 = entry_of(page_of(c0 + 16), c0 + 16);   // of the tile's halves
+    int g0 = page_of(c0 + 32), g1 = page_of(c0 + 48);          // the next tile's pages
+    load_k(e0, e1);
+    load_v(e0, e1);
+
+    // q: per query row a power of two into [-1, 1), fp16; rows past the last are zero.
+    f16x8 qf[R][NG];
+    float cs[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool live = r0 + 16 * r + c16 < rows;
+      float f[NG][8], am = 0.0f;
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        const uint32_t d[4] = {qraw[r][n].x, qraw[r][n].y, qraw[r][n].z, qraw[r][n].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          f[n][2 * e] = live ? bf16_bits_to_f32(d[e] & 0xFFFF) : 0.0f;
+          f[n][2 * e + 1] = live ? bf16_bits_to_f32(d[e] >> 16) : 0.0f;
+          am = fmaxf(am, fmaxf(fabsf(f[n][2 * e]), fabsf(f[n][2 * e + 1])));
+        }
+      }
+      am = max_across16(am);
+      const int ex = am > 0.0f ? __builtin_amdgcn_frexp_expf(am) : 0;   // am < 2^ex
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) qf[r][n][e] = (_Float16)__builtin_ldexpf(f[n][e], -ex);
+      cs[r] = __builtin_ldexpf(a.scale * kLog2e, ex);
+    }
+
+    const int spos = ((lane >> 2) & 3) * 8 + ((lane >> 4) & 1) * 4 + (lane & 3);   // token lane % 32 in the order of the scores
+    uint16_t* sput = &mine.s[lane >> 5][0][spos];
+    for (int base = c0; base < c1; base += 32) {
+      // (tokens before every row's window, behind the last and on pages outside the pool: scales 0)
+      const bool all_valid = e0 >= 0 && e1 >= 0 && base + 32 <= c1 && base >= tmin;
+      const int n0 = entry_of(g0, base + 32), n1 = entry_of(g1, base + 48);
+      const int t0 = base + 4 * g4;                            // this lane's first token (u = j = 0)
+      auto there = [&](int u, int j) {
+        const int t = t0 + 16 * u + j;
+        return (u ? e1 : e0) >= 0 && t < c1 && t >= tmin;
+      };
+      {
+        const int t = base + (lane & 31);
+        const bool in = all_valid || ((lane & 16 ? e1 : e0) >= 0 && t < c1 && t >= tmin);
+        uint32_t top = 0;
+#pragma unroll
+        for (int n = 0; n < KScales<NG>::N; ++n) {
+          const uint32_t d = in ? sc.d[n] & 0x7FFF7FFFu : 0u;
+          top = max(top, max(d & 0xFFFFu, d >> 16));
+          sput[64 * n] = (uint16_t)d;                          // (group 2 n)
+          if (2 * n + 1 < NG) sput[64 * n + 32] = (uint16_t)(d >> 16);
+        }
+        // 2^E >= the largest: its exponent + 1 (a zero counts as the smallest scale)
+        const float f = fmaxf(f16_lo(top), 0x1p-24f);
+        if (lane >= 32) mine.ev[spos] = (float)min(__builtin_amdgcn_frexp_expf(f), 17);
+      }
+      wave_sync();
+
+      // S^T: tokens 16 u + 4 g4 + j, query c16
+      float s[R][2][4];
+      f16x8 ks[NG];
+#pragma unroll
+      for (int n = 0; n < NG; ++n) ks[n] = __builtin_bit_cast(f16x8, ld16(&mine.s[0][n][8 * g4]));
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          u32x4 kw;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = n < P1 ? i * P1 + n : i * P2 + n - P1;
+            kw[i] = n < P1 ? e2m1x2_to_f16(k1[u].d[(n < P1 ? at : 0) / 4], at % 4)
+                           : e2m1x2_to_f16(k2[u].d[(n < P1 ? 0 : at) / 4], at % 4);
+          }
+          const f16x8 kf = __builtin_bit_cast(f16x8, kw);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const f32x4 d = mfma_f16_k32(kf, qf[r][n], (f32x4){0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              s[r][u][j] = n == 0 ? (float)ks[n][4 * u + j] * d[j] : __builtin_fmaf((float)ks[n][4 * u + j], d[j], s[r][u][j]);
+          }
+        }
+      }
+      float ev[2][4];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) *reinterpret_cast<f32x4*>(ev[u]) = *reinterpret_cast<const f32x4*>(&mine.ev[8 * g4 + 4 * u]);
+      load_k(n0, n1);
+      g0 = page_of(base + 64);
+      g1 = page_of(base + 80);
+
+      // whole tile visible to every row?
+      const bool open = all_valid && (!a.causal || base + 31 <= p0 + i0) && (a.window <= 0 || base > p0 + i1 - a.window);
+      float e[R][2][4];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float mx = kNegInf;
+        if (!open) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int t = t0 + 16 * u + j;
+              const bool see = there(u, j) && (!a.causal || t <= qpos[r]) && (a.window <= 0 || t > qpos[r] - a.window);
+              s[r][u][j] = see ? s[r][u][j] * cs[r] : kNegInf;
+            }
+        } else {
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[r][u][j] *= cs[r];
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx = fmaxf(mx, s[r][u][j] + ev[u][j]);
+        mx = max_across16(mx);
+        const float mn = fmaxf(m[r], mx - kLift);
+        const float ref = mn == kNegInf ? 0.0f : mn;
+        if (__ballot(mn > m[r])) {
+          const float corr = __builtin_amdgcn_exp2f(m[r] - ref);
+          l[r] *= corr;
+#pragma unroll
+          for (int n = 0; n < NG; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[n][0][r][j] *= corr, o[n][1][r][j] *= corr;
+          m[r] = mn;
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            e[r][u][j] = __builtin_amdgcn_exp2f(s[r][u][j] - ref);
+            l[r] += e[r][u][j];
+          }
+      }
+
+      // O^T: per group, the weights times their V scales, and the channel pairs' two rows of V^T
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        const f16x8 vs = __builtin_bit_cast(f16x8, ld16(&mine.s[1][n][8 * g4]));
+        f16x8 w[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[r][i] = (_Float16)__builtin_fmaf((float)vs[i], e[r][i / 4][i & 3], 0.0f);
+        const int b = n < P1 ? n : n - P1;                     // byte of the lane's run
+        u32x4 lo, hi;                                          // channels 2 c16 and 2 c16 + 1: tokens 2 i, 2 i + 1
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t x = n < P1 ? v1[2 * i].d[b / 4] : v2[2 * i].d[0], y = n < P1 ? v1[2 * i + 1].d[b / 4] : v2[2 * i + 1].d[0];
+          const uint32_t even = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), odd = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
+          lo[i] = e2m1x2_to_f16(even, b % 4);
+          hi[i] = e2m1x2_to_f16(odd, b % 4);
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          o[n][0][r] = mfma_f16_k32(__builtin_bit_cast(f16x8, lo), w[r], o[n][0][r]);
+          o[n][1][r] = mfma_f16_k32(__builtin_bit_cast(f16x8, hi), w[r], o[n][1][r]);
+        }
+      }
+      load_v(n0, n1);
+      e0 = n0;
+      e1 = n1;
+    }
+
+    // A lane has, per 16-row subtile, channels 32 n + 8 g4 .. + 7 of its row.
+    asm volatile("" : "+v"(c16), "+v"(g4));
+    const bool split = ck.count > 1;
+    const __amdgpu_buffer_rsrc_t rs = partial_rsrc(a.partials, a.partials_bytes);
+    auto part_row = [&](int c, int row) { return (int64_t)((ck.slot(c) * hk + h) * a.tile_rows + row) * (D + 4); };
+    auto out_row = [&](int grow) {                             // index of [token][query head]
+      const int i = grow / a.G;
+      return (int64_t)(it.e.qs + i) * a.Hq + h * a.G + (grow - i * a.G);
+    };
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float Lsum = sum_across16(l[r]);                   // over the lane groups of a query
+      const int row = 16 * r + c16;
+      if (r0 + row < rows) {
+        const int64_t at = split ? part_row(ck.mine, row) : out_row(r0 + row);
+        const float inv = Lsum == 0.0f ? 0.0f : 1.0f / Lsum;   // (NaN stays NaN)
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[2 * j] = o[n][0][r][j], v[2 * j + 1] = o[n][1][r][j];
+          if (split) store_run<8>(rs, at + 32 * n + 8 * g4, v);
+          else store_out<8>(a.out + at * D + 32 * n + 8 * g4, v, inv);
+        }
+        if (g4 == 0) {
+          if (split) {
+            const float ml[2] = {m[r], Lsum};
+            store_run<2>(rs, at + D, ml);
+          } else if (a.lse) {
+            a.lse[at] = Lsum == 0.0f ? kNegInf : (m[r] + __builtin_amdgcn_logf(Lsum)) * kLn2;
+          }
+        }
+      }
+    }
+    if (!split) continue;
+    join_chunks<D, (NG >= 4)>(a, rs, mine.join, lane, ck, min(TR, rows - r0), part_row,
+                              [&](int row) { return out_row(r0 + row); },
+                              [&](int level, int c) { return level * a.level_counters + ck.slot(c) * hk + h; });
+  }
+}
+
+template <int NG>
+hipError_t launch_ng(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t st) {
+  if constexpr (pairs_rows(NG))
+    if (p.R == 2) {
+      kv4_attention_kernel<NG, 2><<<(int)p.grid, waves_of(NG) * 64, 0, st>>>(a);
+      return hipGetLastError();
+    }
+  kv4_attention_kernel<NG, 1><<<(int)p.grid, waves_of(NG) * 64, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+KvAttnPlan plan_kv4_attention(int64_t T, int64_t B, int64_t Hk, int64_t G, int64_t D, bool one_each) {
+  KvAttnPlan p;
+  const int64_t rows = one_each ? G : (T + B - 1) / B * G;   // query rows of an average sequence
+  const bool pairs = pairs_rows((int)(D / 32));
+  if (rows > (pairs ? 32 : 64)) return plan_kv_attention(T, B, Hk, G, D, one_each);   // the many-row kernel's
+  p.R = rows <= 16 || !pairs ? 1 : 2;
+  const int64_t TR = 16 * p.R;
+  while ((2 << p.hw_shift) <= 4 && Hk % (2 << p.hw_shift) == 0) ++p.hw_shift;
+  const int waves = waves_of((int)(D / 32));
+  const int64_t HG = Hk >> p.hw_shift;
+  const int64_t parts = 256 / HG;                              // one workgroup per CU
+  p.parts = (int)(parts >= 8 ? parts / 8 * 8 : parts < 1 ? 1 : parts);
+  p.grid = p.parts * HG;
+  p.waves = p.parts * (waves >> p.hw_shift);
+  p.tile_rows = (int)(one_each && G < TR ? G : TR);
+  p.counters = 2 * p.waves * Hk;
+  p.tiles = one_each ? B * ((G + TR - 1) / TR) : T * G / TR + B;
+  return p;
+}
+
+hipError_t launch_kv4_attention(const KvAttnArgs& a, const KvAttnPlan& p, int D, hipStream_t st) {
+  if (p.R == 16) return launch_kv4_attention_tile(a, p, D, st);
+  switch (D / 32) {
+    case 1: return launch_ng<1>(a, p, st);
+    case 2: return launch_ng<2>(a, p, st);
+    case 3: return launch_ng<3>(a, p, st);
+    case 4: return launch_ng<4>(a, p, st);
+    case 6: return launch_ng<6>(a, p, st);
+    default: return launch_ng<8>(a, p, st);
+  }
+}
+
+}  // namespace qlq

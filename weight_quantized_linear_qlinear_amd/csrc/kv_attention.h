@@ -1,5 +1,5 @@
-// Building blocks that the two attention kernels over the 8-bit cache share (kv_attention.hip:
-// few query rows; kv_attention_tile.hip: many).
+// Building blocks that the attention kernels over the paged cache share (kv_attention.hip and
+// kv4_attention.hip: few query rows over 8 and 4 bits; kv_attention_tile.hip: many, over either).
 #pragma once
 
 #include "qlq_device.h"
@@ -41,6 +41,16 @@ __device__ __forceinline__ f16x8 i8x8_to_f16(u32x2 w) {
 template <bool HI>
 __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t w) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI));
+}
+
+// Byte `at` (a constant once unrolled) of w, two e2m1 codes, as fp16 times `one` (a power of two).
+__device__ __forceinline__ uint32_t e2m1x2_to_f16(uint32_t w, int at, float one = 1.0f) {
+  switch (at) {
+    case 0: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, one, 0));
+    case 1: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, one, 1));
+    case 2: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, one, 2));
+    default: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, one, 3));
+  }
 }
 
 // Memory that no kernel writes meanwhile, read through the scalar cache.
@@ -159,6 +169,66 @@ __device__ __forceinline__ int wave_scan(int v) {             // inclusive
   v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast 15 into rows 1, 3
   v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast 31 into rows 2, 3
   return v;
+}
+
+// The few-row kernels' cutting of the work, in units of 32 tokens.
+
+// The first token that any query of the sequence can see (rounded down to a tile of 32), and
+// the tiles of 32 from there.
+__device__ __forceinline__ int begin_of(const KvAttnArgs& a, const Extent& e) {
+  return a.window > 0 ? min(max(0, e.L - e.nq - a.window + 1), e.L) & ~31 : 0;
+}
+__device__ __forceinline__ int units_of(const KvAttnArgs& a, const Extent& e) {
+  return max(1, (e.L - begin_of(a, e) + 31) >> 5);
+}
+
+// The work of one KV head is a line of units (32 tokens of one query tile), tile after tile;
+// wave w of its waves takes units w U .. (w + 1) U - 1, whatever tiles they belong to.
+// `mine` is the extent of sequence `lane` (nq 0 past the last), kept for the first 64.
+template <int TR>
+__device__ __forceinline__ int total_units(const KvAttnArgs& a, const Extent& mine, int lane) {
+  int total = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 64) {
+    Extent e = mine;
+    if (b0) e = b0 + lane < a.B ? extent_of(a, b0 + lane) : Extent{};
+    total += wave_sum((e.nq * a.G + TR - 1) / TR * units_of(a, e));
+  }
+  return __builtin_amdgcn_readfirstlane(total);
+}
+
+struct Tile {
+  Extent e;
+  int b, qt;                     // sequence, query tile
+  int begin, units;              // its place on the line
+};
+
+// The tile that unit u belongs to (0 <= u < total): every wave on its own, 64 sequences at a time.
+template <int TR>
+__device__ __forceinline__ Tile tile_of(const KvAttnArgs& a, const Extent& mine, int u, int lane) {
+  Tile t{};
+  int before = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 64) {
+    Extent e = mine;
+    if (b0) e = b0 + lane < a.B ? extent_of(a, b0 + lane) : Extent{};
+    const int n = (e.nq * a.G + TR - 1) / TR * units_of(a, e);
+    const int inc = before + wave_scan(n);
+    const uint64_t hit = __ballot(u < inc && u >= inc - n);
+    if (hit) {
+      const int src = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
+      auto of = [&](int v) { return __builtin_amdgcn_readlane(v, src); };
+      t.e.qs = of(e.qs);
+      t.e.nq = of(e.nq);
+      t.e.L = of(e.L);
+      t.b = b0 + src;
+      t.units = units_of(a, t.e);
+      const int begin = of(inc - n);
+      t.qt = (u - begin) / t.units;
+      t.begin = begin + t.qt * t.units;
+      return t;
+    }
+    before = __builtin_amdgcn_readlane(inc, 63);
+  }
+  return t;
 }
 
 // W floats (2, or a multiple of 4) to a partial row at float offset `at`.

@@ -111,64 +111,6 @@ __device__ __forceinline__ void pv_piece(const Raw<2 * P, NT> (&v)[8], const f16
 // Octaves from a row's reference up to its largest weight: 2^15 is the largest power of two in fp16.
 constexpr float kLift = 15.0f;
 
-// The first token that any query of the sequence can see (rounded down to a tile of 32), and
-// the tiles of 32 from there.
-__device__ __forceinline__ int begin_of(const KvAttnArgs& a, const Extent& e) {
-  return a.window > 0 ? min(max(0, e.L - e.nq - a.window + 1), e.L) & ~31 : 0;
-}
-__device__ __forceinline__ int units_of(const KvAttnArgs& a, const Extent& e) {
-  return max(1, (e.L - begin_of(a, e) + 31) >> 5);
-}
-
-// The work of one KV head is a line of units (32 tokens of one query tile), tile after tile;
-// wave w of its waves takes units w U .. (w + 1) U - 1, whatever tiles they belong to.
-// `mine` is the extent of sequence `lane` (nq 0 past the last), kept for the first 64.
-template <int TR>
-__device__ __forceinline__ int total_units(const KvAttnArgs& a, const Extent& mine, int lane) {
-  int total = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 64) {
-    Extent e = mine;
-    if (b0) e = b0 + lane < a.B ? extent_of(a, b0 + lane) : Extent{};
-    total += wave_sum((e.nq * a.G + TR - 1) / TR * units_of(a, e));
-  }
-  return __builtin_amdgcn_readfirstlane(total);
-}
-
-struct Tile {
-  Extent e;
-  int b, qt;                     // sequence, query tile
-  int begin, units;              // its place on the line
-};
-
-// The tile that unit u belongs to (0 <= u < total): every wave on its own, 64 sequences at a time.
-template <int TR>
-__device__ __forceinline__ Tile tile_of(const KvAttnArgs& a, const Extent& mine, int u, int lane) {
-  Tile t{};
-  int before = 0;
-  for (int b0 = 0; b0 < a.B; b0 += 64) {
-    Extent e = mine;
-    if (b0) e = b0 + lane < a.B ? extent_of(a, b0 + lane) : Extent{};
-    const int n = (e.nq * a.G + TR - 1) / TR * units_of(a, e);
-    const int inc = before + wave_scan(n);
-    const uint64_t hit = __ballot(u < inc && u >= inc - n);
-    if (hit) {
-      const int src = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)hit) - 1);
-      auto of = [&](int v) { return __builtin_amdgcn_readlane(v, src); };
-      t.e.qs = of(e.qs);
-      t.e.nq = of(e.nq);
-      t.e.L = of(e.L);
-      t.b = b0 + src;
-      t.units = units_of(a, t.e);
-      const int begin = of(inc - n);
-      t.qt = (u - begin) / t.units;
-      t.begin = begin + t.qt * t.units;
-      return t;
-    }
-    before = __builtin_amdgcn_readlane(inc, 63);
-  }
-  return t;
-}
-
 // Waves per workgroup (one workgroup per CU).  Heads of 32 and 64 leave registers for two waves per
 // SIMD, which their short rows need: 32 sequences of 16000 tokens, 4 heads of 64, 62 us against 74,
 // 16 x 5 tokens in a window of 1024, 16 heads of 64, 18.1 against 20.2; from 96 on eight waves are

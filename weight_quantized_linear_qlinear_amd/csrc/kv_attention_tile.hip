@@ -21,6 +21,8 @@
 // share a SIMD; the matrix cores are busy 31 % of the time, LDS 25 %.  Measured (MI355X): two chunks of
 // 1500 and 804 queries over 8192 and 4394 tokens, 32 heads over 8 of 128, 313 to 333 us (235 GFLOP,
 // 730 TFLOP/s); a prompt of 512 tokens on its own 49 us, half of it storing and joining partial sums.
+#include <type_traits>
+
 #include "kv_attention.h"
 
 namespace qlq {
@@ -116,7 +118,7 @@ struct TileShape {
   static constexpr int KLD = D + 8;              // fp16 per token row of K' (16 bytes of padding: no bank conflicts)
 };
 
-template <int NG>
+template <int NG, int BITS>
 struct TileLds {
   typedef TileShape<NG> S;
   union {
@@ -127,7 +129,7 @@ struct TileLds {
     JoinLds join[kTileWaves];
   };
   // by tile % 4 (written two tiles ahead):
-  float vs[4][S::T];                             // V scales, 0 for a token that is not there
+  float vs[4][BITS == 4 ? NG : 1][S::T];         // V scales (4 bits: by group), 0 for a token that is not there
   uint32_t top[4][kTileWaves];                   // per wave's tokens: largest K scale (fp16 bits; bit 15: one is not there) and V scale
 };
 
@@ -153,6 +155,10 @@ constexpr int kNoScale = -1000;
 // scale 2^24 times as large, which earlier rows of its query tile do not even see, 5 bits were left.)
 constexpr int kCodeShift = 8;
 constexpr float kCode = 0x1p-8f;
+// 4 bits: codes reach 6, so the largest scale goes to 2^12 .. 2^13, V' stays below 49152 and has its 11
+// bits down to 2^-26 of the largest; K' overflows for scales above 10917: 2^-7 from 8192 on.
+constexpr int kTop4 = 13;
+constexpr uint32_t kBig4 = 0x7000;
 
 // N products that take one operand from LDS each, in exactly this order: AHEAD reads in front,
 // then a product and the read of a later one in turn (left alone, the compiler reads each operand
@@ -171,16 +177,24 @@ __device__ __forceinline__ void products(Read read, Product product) {
   }
 }
 
+// Where the 4-bit row's order puts things (kv_rows.h): its runs of P1 and P2 groups.
 template <int NG>
+struct Runs4 {
+  static constexpr int P1 = NG >= 8 ? 8 : NG >= 4 ? 4 : NG >= 2 ? 2 : 1, P2 = NG - P1;
+};
+
+template <int NG, int BITS>
 __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAttnArgs a) {
   typedef TileShape<NG> S;
   constexpr int D = S::D, T = S::T, TPW = T / kTileWaves, NB = T / 32, NL = TPW * D / 16;
   extern __shared__ __align__(16) uint8_t smem_raw[];
-  TileLds<NG>& sm = *reinterpret_cast<TileLds<NG>*>(smem_raw);
+  typedef TileLds<NG, BITS> Lds;
+  Lds& sm = *reinterpret_cast<Lds*>(smem_raw);
+  constexpr int P1 = Runs4<NG>::P1, P2 = Runs4<NG>::P2;     // (4 bits)
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int hk = a.Hk, h = blockIdx.x % hk, part = blockIdx.x / hk;    // a head's parts on one XCD where Hk is a multiple of 8
   const int page_mask = (1 << a.page_shift) - 1;
-  const uint32_t row_bytes = (uint32_t)hk * D;
+  const uint32_t row_bytes = (uint32_t)hk * (BITS == 4 ? D / 2 : D);
 
   int total = 0;
   walk_tiles<T>(a, lane, [&](int, int, int n) {
@@ -232,10 +246,22 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
     f16x8 qf[2 * NG];
     float cs;
     {
-      const uint16_t* qp = a.q + (int64_t)(e.qs + qi) * a.q_stride + (int64_t)(h * a.G + qg) * D + 8 * half;
+      const uint16_t* qp = a.q + (int64_t)(e.qs + qi) * a.q_stride + (int64_t)(h * a.G + qg) * D;
       u32x4 raw[2 * NG];
+      if constexpr (BITS == 4) {
+        // in the order of the rows: bytes 8 k + 4 half + j, channel pairs
 #pragma unroll
-      for (int k = 0; k < 2 * NG; ++k) raw[k] = ld16(qp + 16 * k);
+        for (int k = 0; k < 2 * NG; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int run = k < 2 * P1 ? 0 : P1, P = k < 2 * P1 ? P1 : P2 > 0 ? P2 : 1;
+            const int b = 8 * (k - 2 * run) + 4 * half + j;
+            raw[k][j] = *reinterpret_cast<const uint32_t*>(qp + 32 * (run + b % P) + 2 * (b / P));
+          }
+      } else {
+#pragma unroll
+        for (int k = 0; k < 2 * NG; ++k) raw[k] = ld16(qp + 8 * half + 16 * k);
+      }
       float am = 0.0f;
 #pragma unroll
       for (int k = 0; k < 2 * NG; ++k) {
@@ -270,18 +296,32 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
     };
     const int li = min(lane, NL - 1);
     const int krow = li / (D / 16), kchunk = li % (D / 16), vgrp = li / (D / 4), vcb = li % (D / 4);
-    const uint32_t koff = krow * row_bytes + 16 * kchunk, voff = 4 * vgrp * row_bytes + 4 * vcb;
+    constexpr int KB = BITS == 4 ? 8 : 16, VB = BITS == 4 ? 2 : 4;          // bytes of 16 codes of K, of 4 of V
+    const uint32_t koff = krow * row_bytes + KB * kchunk, voff = 4 * vgrp * row_bytes + VB * vcb;
+    // 4 bits: the two bytes of a V block are the channel pairs vch and vch + vnext, of groups vg and vg2
+    const bool second = P2 > 0 && vcb >= 8 * P1;
+    const int vp = second ? (P2 > 0 ? P2 : 1) : P1, vb = 2 * (vcb - (second ? 8 * P1 : 0));
+    const int vg = (second ? P1 : 0) + vb % vp, vg2 = vp > 1 ? vg + 1 : vg, vch = 32 * vg + 2 * (vb / vp), vnext = vp > 1 ? 32 : 2;
     const int first_t = TPW * wave;                          // this wave's first token of a tile
-    u32x4 kraw;
-    uint32_t vraw[4], ksraw;
+    typename std::conditional<BITS == 4, u32x2, u32x4>::type kraw;
+    typename std::conditional<BITS == 4, KScales<NG>, uint32_t>::type ksraw;
+    uint32_t vraw[4];
     TileScale next{kNoScale, false, false};
     auto load = [&](int entry) {
       const int64_t at64 = (int64_t)max(entry, 0) * hk + h;
-      kraw = ld16(a.k_codes + at64 * D + koff);
-      ksraw = a.k_scales[(at64 + (int64_t)krow * hk) * NG + kchunk / 2];
-      const uint8_t* vp = a.v_codes + at64 * D + voff;
+      if constexpr (BITS == 4) {
+        kraw = *reinterpret_cast<const u32x2*>(a.k_codes + at64 * (D / 2) + koff);
+        ksraw.load(a.k_scales + (at64 + (int64_t)krow * hk) * NG);
+        const uint8_t* vp = a.v_codes + at64 * (D / 2) + voff;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) vraw[i] = *reinterpret_cast<const uint32_t*>(vp + (size_t)i * row_bytes);
+        for (int i = 0; i < 4; ++i) vraw[i] = *reinterpret_cast<const uint16_t*>(vp + (size_t)i * row_bytes);
+      } else {
+        kraw = ld16(a.k_codes + at64 * D + koff);
+        ksraw = a.k_scales[(at64 + (int64_t)krow * hk) * NG + kchunk / 2];
+        const uint8_t* vp = a.v_codes + at64 * D + voff;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vraw[i] = *reinterpret_cast<const uint32_t*>(vp + (size_t)i * row_bytes);
+      }
     };
     // The loaded tile, number n, into LDS buffer n % 2.
     auto convert = [&](int n) {
@@ -290,13 +330,48 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
       next.gap = __ballot((top & 0x8000u) != 0) != 0;
       top = row8(top & 0x7FFF7FFFu, MaxU16());
       top = __builtin_amdgcn_readfirstlane(top);
-      next.big = (top & 0xFFFF) > 0x6000;
+      next.big = (top & 0xFFFF) > (BITS == 4 ? kBig4 : 0x6000);
       const uint32_t vt = top >> 16;
-      if (vt) next.e = max(next.e, (vt >= 0x400 ? (int)(vt >> 10) - 14 : 8 - __builtin_clz(vt)) - 6);
+      if (vt) next.e = max(next.e, (vt >= 0x400 ? (int)(vt >> 10) - 14 : 8 - __builtin_clz(vt)) - (BITS == 4 ? kTop4 : 6));
+      // tokens 4 g .. 4 g + 3 of the tile: piece 4 (g / 8) + 2 (g / 4 % 2) + g % 2, half g / 2 % 2 of it
+      const int g = first_t / 4 + vgrp;
+      const int p = 4 * (g >> 3) + 2 * ((g >> 2) & 1) + (g & 1), hf = (g >> 1) & 1;
+      if constexpr (BITS == 4) {
+        const f32x4 va = *reinterpret_cast<const f32x4*>(&sm.vs[n & 3][vg][first_t + 4 * vgrp]);
+        const f32x4 vb = *reinterpret_cast<const f32x4*>(&sm.vs[n & 3][vg2][first_t + 4 * vgrp]);
+        if (lane < NL) {
+          const float kone = next.big ? 0x1p-7f : 1.0f;      // (the codes take the 2^-7, as below)
+          const bool ksecond = P2 > 0 && kchunk >= 2 * P1;
+          u32x4 w[2];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int s1 = j % P1, s2 = P2 > 0 ? P1 + j % (P2 > 0 ? P2 : 1) : 0;
+            auto both = [&](int i) { return __builtin_amdgcn_perm(ksraw.d[i / 2], ksraw.d[i / 2], i & 1 ? 0x03020302u : 0x01000100u); };
+            const uint32_t sc = P2 > 0 ? (ksecond ? both(s2) : both(s1)) : both(s1);
+            w[j / 4][j & 3] = mul2(e2m1x2_to_f16(kraw[j / 4], j & 3, kone), __builtin_bit_cast(f16x2, sc));
+          }
+          _Float16* kp = &sm.k[buf][first_t + krow][16 * kchunk];
+          st16(kp, w[0]);
+          st16(kp + 8, w[1]);
+          // V: nibbles of tokens (0, 1) and (2, 3) into bytes; codes are finite, so a scale of 0 clears a token
+          const uint32_t x = vraw[0] | vraw[2] << 16, y = vraw[1] | vraw[3] << 16;
+          const uint32_t even = (x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), odd = ((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {                      // byte i / 2, channel i % 2 of its pair
+            const f32x4 sv = i < 2 ? va : vb;
+            const f16x2 v01 = {(_Float16)__builtin_ldexpf(sv[0], -next.e), (_Float16)__builtin_ldexpf(sv[1], -next.e)};
+            const f16x2 v23 = {(_Float16)__builtin_ldexpf(sv[2], -next.e), (_Float16)__builtin_ldexpf(sv[3], -next.e)};
+            const uint32_t nib = i & 1 ? odd : even;
+            const uint32_t lo = e2m1x2_to_f16(nib, i / 2, 1.0f), hi = e2m1x2_to_f16(nib, 2 + i / 2, 1.0f);
+            const int d = vch + (i / 2) * vnext + (i & 1);
+            *reinterpret_cast<u32x2*>(&sm.v[buf][d][8 * (p ^ swizzle<T>(d)) + 4 * hf]) = (u32x2){mul2(lo, v01), mul2(hi, v23)};
+          }
+        }
+      } else {
       const f16x2 s2 = __builtin_bit_cast(f16x2, (ksraw & 0xFFFF) | ksraw << 16);
       const uint32_t upper = next.big ? 0x48484848u : 0x64646464u;        // (the codes take the 2^-7: a small scale
       const float zero = next.big ? 9.0f : 1152.0f;                       // beside a big one keeps its bits)
-      f32x4 vsc = *reinterpret_cast<const f32x4*>(&sm.vs[n & 3][first_t + 4 * vgrp]);
+      f32x4 vsc = *reinterpret_cast<const f32x4*>(&sm.vs[n & 3][0][first_t + 4 * vgrp]);
       if (lane < NL) {
         const uint32_t kd[4] = {kraw.x, kraw.y, kraw.z, kraw.w};
         u32x4 w[2];
@@ -318,9 +393,6 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
         const f16x2 v01 = {(_Float16)vsc[0], (_Float16)vsc[1]}, v23 = {(_Float16)vsc[2], (_Float16)vsc[3]};
         const uint32_t a01 = __builtin_amdgcn_perm(r[1], r[0], 0x05010400u), b01 = __builtin_amdgcn_perm(r[1], r[0], 0x07030602u);
         const uint32_t a23 = __builtin_amdgcn_perm(r[3], r[2], 0x05010400u), b23 = __builtin_amdgcn_perm(r[3], r[2], 0x07030602u);
-        // tokens 4 g .. 4 g + 3 of the tile: piece 4 (g / 8) + 2 (g / 4 % 2) + g % 2, half g / 2 % 2 of it
-        const int g = first_t / 4 + vgrp;
-        const int p = 4 * (g >> 3) + 2 * ((g >> 2) & 1) + (g & 1), hf = (g >> 1) & 1;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint32_t s01 = i < 2 ? a01 : b01, s23 = i < 2 ? a23 : b23;
@@ -332,6 +404,7 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
           *reinterpret_cast<u32x2*>(&sm.v[buf][d][8 * (p ^ swizzle<T>(d)) + 4 * hf]) = (u32x2){mul2(lo, v01), mul2(hi, v23)};
         }
       }
+      }
     };
     // The scales, two tiles ahead: lane l has token l % TPW of this wave's, K's block l / TPW.
     const int srow = lane & (TPW - 1), sblock = lane / TPW % NG;
@@ -341,7 +414,7 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
       st_t = t0;
       st_page = page;
       const int64_t at64 = (int64_t)max(entry_of(page, t0), 0) * hk + (int64_t)srow * hk + h;
-      svr = a.v_scales[at64];
+      svr = BITS == 4 ? a.v_scales[at64 * NG + sblock] : a.v_scales[at64];
       skr = a.k_scales[at64 * NG + sblock];
     };
     auto stat_write = [&](int n) {
@@ -350,10 +423,11 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
       const uint32_t kb = there ? skr & 0x7FFF : 0u, vb = there ? max(svr & 0x7FFF, 1u) : 0u;
       uint32_t top = across16(row16(kb | vb << 16, MaxU16()), MaxU16());
       if (__ballot(!there)) top |= 0x8000u;
-      if (lane < TPW) sm.vs[n & 3][first_t + lane] = f16_lo(vb);
+      if (lane < (BITS == 4 ? NG : 1) * TPW) sm.vs[n & 3][BITS == 4 ? lane / TPW : 0][first_t + srow] = f16_lo(vb);
       if (lane == 0) sm.top[n & 3][wave] = top;
     };
 
+    auto there = [](float vs) { return BITS == 4 ? vs != 0.0f : vs > 0.0f; };   // (a NaN: there)
     const int vswz = half ^ swizzle<T>(c32);                 // this lane's pieces: (4 k + 2 t) ^ vswz
     f32x16 o[NG];
     float m = kNegInf, l = 0.0f;
@@ -415,7 +489,7 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
             for (int k = 0; k < NB; ++k)
 #pragma unroll
               for (int i = 0; i < 16; ++i)
-                s[k][i] = sm.vs[n & 3][32 * k + 8 * (i / 4) + 4 * half + (i & 3)] > 0.0f ? s[k][i] : kNegInf;
+                s[k][i] = there(sm.vs[n & 3][0][32 * k + 8 * (i / 4) + 4 * half + (i & 3)]) ? s[k][i] : kNegInf;
           }
           const int64_t from = (int64_t)qpos - t4;             // (may be far below and above the tile)
           int hi = (int)max(min(from, (int64_t)T), (int64_t)-1), lo = (int)max(min(from - a.window, (int64_t)T), (int64_t)-1);
@@ -521,28 +595,36 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
   }
 }
 
-template <int NG>
+template <int NG, int BITS>
 hipError_t launch_ng(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t st) {
   static std::atomic<uint64_t> done{0};
-  constexpr int bytes = (int)sizeof(TileLds<NG>);
+  constexpr int bytes = (int)sizeof(TileLds<NG, BITS>);
   static_assert(bytes <= 160 * 1024, "LDS");
-  if (hipError_t e = set_lds_limit(reinterpret_cast<const void*>(kv_attention_tile_kernel<NG>), bytes, done); e != hipSuccess)
+  if (hipError_t e = set_lds_limit(reinterpret_cast<const void*>(kv_attention_tile_kernel<NG, BITS>), bytes, done); e != hipSuccess)
     return e;
-  kv_attention_tile_kernel<NG><<<(int)p.grid, kTileWaves * 64, bytes, st>>>(a);
+  kv_attention_tile_kernel<NG, BITS><<<(int)p.grid, kTileWaves * 64, bytes, st>>>(a);
   return hipGetLastError();
+}
+
+template <int BITS>
+hipError_t launch_tile(const KvAttnArgs& a, const KvAttnPlan& p, int D, hipStream_t st) {
+  switch (D / 32) {
+    case 1: return launch_ng<1, BITS>(a, p, st);
+    case 2: return launch_ng<2, BITS>(a, p, st);
+    case 3: return launch_ng<3, BITS>(a, p, st);
+    case 4: return launch_ng<4, BITS>(a, p, st);
+    case 6: return launch_ng<6, BITS>(a, p, st);
+    default: return launch_ng<8, BITS>(a, p, st);
+  }
 }
 
 }  // namespace
 
 hipError_t launch_kv_attention_tile(const KvAttnArgs& a, const KvAttnPlan& p, int D, hipStream_t st) {
-  switch (D / 32) {
-    case 1: return launch_ng<1>(a, p, st);
-    case 2: return launch_ng<2>(a, p, st);
-    case 3: return launch_ng<3>(a, p, st);
-    case 4: return launch_ng<4>(a, p, st);
-    case 6: return launch_ng<6>(a, p, st);
-    default: return launch_ng<8>(a, p, st);
-  }
+  return launch_tile<8>(a, p, D, st);
+}
+hipError_t launch_kv4_attention_tile(const KvAttnArgs& a, const KvAttnPlan& p, int D, hipStream_t st) {
+  return launch_tile<4>(a, p, D, st);
 }
 
 }  // namespace qlq

@@ -109,6 +109,38 @@ hipError_t launch_rope_kv(const RopeArgs& a, hipStream_t st);
 hipError_t launch_kv_gather(const void* kq, const void* ks, const void* vq, const void* vs, int64_t pool, int H, int D,
                             const void* slots, int slot64, int64_t n, void* ko, void* vo, hipStream_t st);
 
+// Norms of query and key heads, rotary positions of several axes, and 8-bit or 4-bit cache entries
+// (norm_rope_kv.hip).
+struct NormRopeArgs {
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  uint16_t *q_out, *k_out;
+  int64_t q_out_stride, k_out_stride;
+  const uint16_t *wq, *wk;     // bf16 [D] or null: no norm
+  double eps;
+  const void* positions;       // int32 or int64 [A, T]
+  int pos64;
+  const int32_t* axes;         // [R / 2], or null: one axis
+  int A;
+  const double* inv_freq;      // [R / 2]
+  double factor;
+  int R, interleaved;          // rotated channels (0: none)
+  int T, Hq, Hk, D;
+  const void* slots;           // int32 or int64 [T]
+  int slot64;
+  int64_t pool;
+  uint8_t* k_codes;
+  uint16_t* k_scales;
+  uint8_t* v_codes;
+  uint16_t* v_scales;
+  int vec_in, vec_out, vec_w;  // 16-byte aligned rows, weights
+  int TW;                      // tokens per workgroup (set by the launcher)
+};
+// kout: 0 K to k_out (bf16; or no K), 8 or 4 K and V into a cache of that many bits.
+hipError_t launch_norm_rope(const NormRopeArgs& a, int kout, hipStream_t st);
+hipError_t launch_kv4_gather(const void* kq, const void* ks, const void* vq, const void* vs, int64_t pool, int H, int D,
+                             const void* slots, int slot64, int64_t n, void* ko, void* vo, hipStream_t st);
+
 // Attention over the paged cache (kv_attention.hip).
 struct KvAttnArgs {
   const uint16_t* q;           // bf16, token stride q_stride elements
@@ -143,6 +175,11 @@ struct KvAttnPlan {
 KvAttnPlan plan_kv_attention(int64_t T, int64_t B, int64_t Hk, int64_t G, int64_t D, bool one_each);
 hipError_t launch_kv_attention_tile(const KvAttnArgs& a, const KvAttnPlan& p, int D, hipStream_t st);
 hipError_t launch_kv_attention(const KvAttnArgs& a, const KvAttnPlan& p, int D, hipStream_t st);
+
+// The same over the 4-bit cache (kv4_attention.hip): scales of K and V [slots, H, D / 32] both.
+KvAttnPlan plan_kv4_attention(int64_t T, int64_t B, int64_t Hk, int64_t G, int64_t D, bool one_each);
+hipError_t launch_kv4_attention_tile(const KvAttnArgs& a, const KvAttnPlan& p, int D, hipStream_t st);
+hipError_t launch_kv4_attention(const KvAttnArgs& a, const KvAttnPlan& p, int D, hipStream_t st);
 
 // Raises kernel k's dynamic-LDS limit to `bytes` on the current device, once per
 // device (bit d of `done` records device d; devices past 63 set it every call).

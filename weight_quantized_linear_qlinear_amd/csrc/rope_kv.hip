@@ -16,7 +16,7 @@
 // place.  Bound by HBM for many tokens, by latency for few.  Measured (MI355X, kernel alone):
 // 8191 tokens of 32 + 8 + 8 heads of 128 in 41.4 us (185 MB, 4.5 TB/s), 2048 in 13.9 us, 16 of
 // 28 + 4 + 4 heads in 4.4 us; gathering 8191 slots of 8 heads 10.7 us (51 MB, 4.8 TB/s).
-#include "qlq_device.h"
+#include "kv_rows.h"
 #include "qlq_launch.h"
 
 namespace qlq {
@@ -24,39 +24,6 @@ namespace qlq {
 namespace {
 
 constexpr int kRopeWaves = 4;
-
-__device__ __forceinline__ uint32_t kv_f16_scale(float absmax, float qmax) {   // the codec's rule
-  if (absmax == 0.0f) return 0x3C00u;
-  const float c = __builtin_amdgcn_fmed3f(absmax / qmax, 65504.0f, -65504.0f);
-  const uint32_t s = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)c);
-  return s == 0u ? 1u : s;
-}
-
-__device__ __forceinline__ float f16_value(uint32_t b) { return (float)__builtin_bit_cast(_Float16, (uint16_t)b); }
-
-__device__ __forceinline__ int64_t load_index(const void* p, int is64, int64_t i) {
-  return is64 ? static_cast<const int64_t*>(p)[i] : (int64_t)static_cast<const int32_t*>(p)[i];
-}
-
-// Eight bf16 at p (any alignment unless vec).
-__device__ __forceinline__ u32x4 load8(const uint16_t* p, bool vec) {
-  if (vec) return ld16(p);
-  u32x4 r;
-  r.x = p[0] | ((uint32_t)p[1] << 16);
-  r.y = p[2] | ((uint32_t)p[3] << 16);
-  r.z = p[4] | ((uint32_t)p[5] << 16);
-  r.w = p[6] | ((uint32_t)p[7] << 16);
-  return r;
-}
-
-__device__ __forceinline__ void unpack8(u32x4 v, float* f) {
-  const uint32_t d[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    f[2 * e] = bf16_bits_to_f32(d[e] & 0xFFFF);
-    f[2 * e + 1] = bf16_bits_to_f32(d[e] >> 16);
-  }
-}
 
 // Angles of the positions of tokens t0 .. t0 + n - 1: cs[k R/2 + i] = (factor cos, factor sin).
 __device__ __forceinline__ void token_angles(const RopeArgs& a, int64_t t0, int n, float2* cs) {
