@@ -11,11 +11,11 @@
 // to a border a code's neighbour is up to half of its value away, so that an order of fp32 additions
 // would show; the fp64 rate of a CU is the fp32 one, and K is a small share of the rows.
 //
-// One workgroup takes TW tokens (or a share of one token's heads, while tokens are few): its threads
-// compute the tokens' angles once for all heads into LDS.  A head row is D / 8 lanes of a wave, 8
-// channels each; a wave's rows are all of one kind (K first, as the longest, then V, then q).  The row
-// passes through the wave's LDS for the pair partners, and 4-bit codes pass through it into the order
-// of the cache.
+// A wave takes one token, or a share of its heads while tokens are few, and works on its own: no barrier.  It
+// computes the token's angles once, into its LDS.  A head row is D / 8 lanes, 8 channels each, so a
+// lane's channels stay the same from row to row, and what their rotation multiplies them and their
+// partners by (weights included: two operations per channel) stays in registers for all heads of q.
+// Rows pass through the wave's LDS for the partners, 4-bit codes for the order of the cache.
 #include "kv_rows.h"
 #include "qlq_launch.h"
 
@@ -25,6 +25,7 @@ namespace {
 
 constexpr int kWaves = 4;
 
+// What a channel and its partner are multiplied by: x c + partner s.
 template <class T>
 struct alignas(2 * sizeof(T)) Turn {
   T c, s;
@@ -54,13 +55,18 @@ __device__ __forceinline__ void sincos_quarter(double r, double* s, double* c) {
   *c = __builtin_fma(q, z, 1.0);
 }
 
-// Angles of tokens t0 .. t0 + n - 1: (factor cos, factor sin) at [k R/2 + i], in fp32 and (where) in fp64.
-__device__ __forceinline__ void token_angles(const NormRopeArgs& a, int64_t t0, int n, Turn<double>* wide, Turn<float>* cs) {
+// The rotation of token t, channel by channel, in fp32 and (where) in fp64: (factor cos, -+ factor sin); (1, 0)
+// from channel R on.  Channel ch stands at [ch % 8][ch / 8], so that the lanes of a row read side by side.
+__device__ __forceinline__ void token_turns(const NormRopeArgs& a, int64_t t, int lane, int tpr, Turn<double>* wide, Turn<float>* cs) {
+  auto put = [&](int ch, double c, double s) {
+    const int at = (ch & 7) * tpr + (ch >> 3);
+    if (wide) wide[at] = {c, s};
+    cs[at] = {(float)c, (float)s};
+  };
   const int half = a.R / 2;
-  for (int j = threadIdx.x; j < n * half; j += kWaves * 64) {
-    const int k = j / half, i = j - k * half;
+  for (int i = lane; i < half; i += 64) {
     const int64_t axis = a.axes ? min(max(a.axes[i], 0), a.A - 1) : 0;
-    const int64_t pos = load_index(a.positions, a.pos64, axis * a.T + t0 + k);
+    const int64_t pos = load_index(a.positions, a.pos64, axis * a.T + t);
     const double th = (double)pos * a.inv_freq[i];
     const double q = rint(th * 0x1.45f306dc9c883p-1);                    // 2 / pi
     double r = __builtin_fma(-q, 0x1.921fb54442d18p+0, th);             // pi / 2, high part
@@ -70,302 +76,388 @@ __device__ __forceinline__ void token_angles(const NormRopeArgs& a, int64_t t0, 
     const int quarter = (int)((int64_t)q & 3);
     const double cc = (quarter & 1 ? s : c) * (quarter == 1 || quarter == 2 ? -a.factor : a.factor);
     const double ss = (quarter & 1 ? c : s) * (quarter >= 2 ? -a.factor : a.factor);
-    if (wide) wide[j] = {cc, ss};
-    cs[j] = {(float)cc, (float)ss};
+    put(a.interleaved ? 2 * i : i, cc, -ss);
+    put(a.interleaved ? 2 * i + 1 : i + half, cc, ss);
   }
+  for (int ch = a.R + lane; ch < 8 * tpr; ch += 64) put(ch, 1.0, 0.0);
 }
 
-// Sum over the n lanes of a row that begins at lane `first` (c: this lane's place in it).
-template <class T>
-__device__ __forceinline__ T row_sum(T v, int n, int first, int c) {
-  if ((n & (n - 1)) == 0) {
-    for (int d = 1; d < n; d *= 2) v += __shfl_xor(v, d, 64);
-    return v;
-  }
-  int step = 1;
-  for (; n % (2 * step) == 0; step *= 2) v += __shfl_xor(v, step, 64);   // (rows begin at multiples of 2 step)
-  T sum = v;
-  for (int d = step; d < n; d += step) {
-    const int at = c + d >= n ? c + d - n : c + d;
-    sum += __shfl(v, (first + at) & 63, 64);
-  }
-  return sum;
+// Another lane's value, for steps within 4, 8 and 16 lanes in the vector unit.
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
+template <int CTRL>
+__device__ __forceinline__ int other(int v) { return __builtin_amdgcn_mov_dpp(v, CTRL, 0xf, 0xf, true); }
+template <int CTRL>
+__device__ __forceinline__ uint32_t other(uint32_t v) { return (uint32_t)other<CTRL>((int)v); }
+template <int CTRL>
+__device__ __forceinline__ float other(float v) { return __builtin_bit_cast(float, other<CTRL>(__builtin_bit_cast(int, v))); }
+template <int CTRL>
+__device__ __forceinline__ double other(double v) {
+  const u32x2 w = __builtin_bit_cast(u32x2, v);
+  return __builtin_bit_cast(double, (u32x2){other<CTRL>(w.x), other<CTRL>(w.y)});
 }
+
+struct Add {
+  template <class T>
+  __device__ __forceinline__ T operator()(T a, T b) const { return a + b; }
+};
+struct Max {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+  __device__ __forceinline__ double operator()(double a, double b) const { return fmax(a, b); }
+  __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return max(a, b); }
+};
 
 // The four lanes of a group of 32 channels, to each of them.
 template <class T, class OP>
 __device__ __forceinline__ T quad(T v, OP op) {
-  v = op(v, __shfl_xor(v, 1, 64));
-  return op(v, __shfl_xor(v, 2, 64));
+  v = op(v, other<kXor1>(v));
+  return op(v, other<kXor2>(v));
 }
 
-// A row's 8 channels (place c), times their weights in f, rotated.  mine: the wave's copy of the row
-// (bf16); w: its weights, or null; wpart: those of the partner channels where they are a whole chunk.
-template <class T>
-__device__ __forceinline__ void rotate(const NormRopeArgs& a, const uint16_t* mine, const uint16_t* w, int c,
-                                       const Turn<T>* cs, u32x4 wpart, T* f) {
-  const int half = a.R / 2;
-  if (a.interleaved) {
+// Over the n lanes of a row (N where the compiler knows them, else 0); first: its first lane, c: this one's place.
+template <int N, class T, class OP>
+__device__ __forceinline__ T over_row(T v, int n, int first, int c, OP op) {
+  if constexpr (N == 4 || N == 8 || N == 16 || N == 32 || N == 64) {
+    v = quad(v, op);
+    if constexpr (N >= 8) v = op(v, other<kHalfMirror>(v));
+    if constexpr (N >= 16) v = op(v, other<kMirror>(v));
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = c * 4 + e;                                // pair (2 i, 2 i + 1)
-      if (i < half) {
-        const Turn<T> t = cs[i];
-        const T x = f[2 * e], y = f[2 * e + 1];
-        f[2 * e] = x * t.c - y * t.s;
-        f[2 * e + 1] = x * t.s + y * t.c;
-      }
-    }
-  } else if (a.R % 16 == 0) {
-    const bool low = c * 8 < half;
-    const int i0 = low ? c * 8 : c * 8 - half;
-    float o[8], v[8];
-    unpack8(ld16(mine + (low ? c * 8 + half : c * 8 - half)), o);
-    unpack8(wpart, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const Turn<T> t = cs[i0 + e];
-      const T y = w ? (T)o[e] * (T)v[e] : (T)o[e];
-      f[e] = f[e] * t.c + (low ? -y : y) * t.s;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int ch = c * 8 + e;
-      if (ch < a.R) {
-        const bool low = ch < half;
-        const int other = low ? ch + half : ch - half;
-        const Turn<T> t = cs[low ? ch : other];
-        T y = (T)bf16_bits_to_f32(mine[other]);
-        if (w) y *= (T)bf16_bits_to_f32(w[other]);
-        f[e] = f[e] * t.c + (low ? -y : y) * t.s;
-      }
-    }
+    for (int d = 16; d < N; d *= 2) v = op(v, __shfl_xor(v, d, 64));
+    return v;
   }
+  int step = 1;
+  for (; n % (2 * step) == 0; step *= 2) v = op(v, __shfl_xor(v, step, 64));   // (rows begin at multiples of 2 step)
+  T all = v;
+  for (int d = step; d < n; d += step) {
+    const int at = c + d >= n ? c + d - n : c + d;
+    all = op(all, __shfl(v, (first + at) & 63, 64));
+  }
+  return all;
 }
 
-// Codes of 8 quotients x / s in 64 bits, rounded once; 2 per byte.
-__device__ __forceinline__ void e2m1_from_f64(const double* x, double s, uint32_t* b) {
+__device__ __forceinline__ void wave_sync() {                 // the wave's LDS writes before its reads
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Codes of 8 quotients y / s in 64 bits, rounded once; 2 per byte.
+__device__ __forceinline__ void e2m1_from_f64(const double* y, double s, uint32_t* b) {
   const double inv = 1.0 / s;
   float v[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    double q = x[e] * inv;
-    q = __builtin_fma(__builtin_fma(-q, s, x[e]), inv, q);    // (exact where the quotient is: ties stay ties)
-    const double m = fabs(q);
-    const double step = m < 2.0 ? 0.5 : m < 4.0 ? 1.0 : 2.0, per = m < 2.0 ? 2.0 : m < 4.0 ? 1.0 : 0.5;
-    v[e] = (float)copysign(fmin(rint(m * per) * step, 6.0), q);
+    double q = y[e] * inv;
+    q = __builtin_fma(__builtin_fma(-q, s, y[e]), inv, q);    // (exact where the quotient is: ties stay ties)
+    // 21 bits, the last one set if anything is behind them: next to a border (3 bits) the side stays
+    const u32x2 w = __builtin_bit_cast(u32x2, q);
+    v[e] = (float)__builtin_bit_cast(double, (u32x2){0u, w.y | min(w.x, 1u)});
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) b[e] = f32x2_to_e2m1x2_sat(v[2 * e], v[2 * e + 1]);
 }
 
-enum Kind { kK, kV, kQ };
+// Where a lane stands in the rows of its wave, and the wave's LDS.  KOUT: where K goes: 0 to bf16 (or
+// there is none), 8 and 4 into a cache of that many bits, with V.  TPR: lanes per row, 0 for those that
+// have no instance of their own.
+template <int KOUT, int TPR>
+struct Lane {
+  int D, tpr, rpw, r, c;         // channels, lanes per row, rows per wave; this lane's row and place in it
+  bool live;                     // (there are lanes left over where 64 / tpr is no whole number)
+  int half, pc;                  // R / 2; the chunk that holds this one's partners (where R % 16 == 0)
+  bool chunks;
+  // LDS: the token's turns in fp64 (4 bits) and fp32, the wave's rows, codes (4 bits)
+  Turn<double>* wide;
+  Turn<float>* cs;
+  uint16_t* mine;
+  uint8_t* bytes;
 
-// KOUT: where K goes: 0 to bf16 (or there is none), 8 and 4 into a cache of that many bits, with V.
-template <int KOUT>
-__global__ __launch_bounds__(kWaves * 64) void norm_rope_kernel(NormRopeArgs a) {
-  extern __shared__ __align__(16) uint8_t smem[];            // angles: [TW][R / 2] in fp64 (4 bits), then fp32
-  __shared__ __align__(16) uint16_t rows[kWaves][512];       // 64 lanes x 8 channels per wave
-  __shared__ __align__(16) uint8_t bytes[kWaves][KOUT == 4 ? 256 : 16];
-  Turn<double>* wide = KOUT == 4 ? reinterpret_cast<Turn<double>*>(smem) : nullptr;
-  Turn<float>* cs_all = reinterpret_cast<Turn<float>*>(smem + (KOUT == 4 ? (size_t)a.TW * a.R * 8 : 0));
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t t0 = (int64_t)blockIdx.x * a.TW;
-  const int ntok = (int)min((int64_t)a.TW, a.T - t0);
-  const int tpr = a.D / 8, rpw = 64 / tpr;                    // lanes per row, rows per wave
-  const int r = lane / tpr, c = lane - r * tpr, half = a.R / 2;
-  const bool lane_live = r < rpw;
-  const int nk = (ntok * a.Hk + rpw - 1) / rpw, nv = KOUT ? nk : 0, nq = (ntok * a.Hq + rpw - 1) / rpw;
-
-  // Weights of this lane's channels and of their partners (a whole chunk where R % 16 == 0).
-  const int pc = c * 8 < half ? c + half / 8 : c - half / 8;
-  const bool whole = !a.interleaved && a.R % 16 == 0 && c * 8 < a.R && lane_live;
-  u32x4 wk = {0u, 0u, 0u, 0u}, wkp = wk, wq = wk, wqp = wk;
-  if (lane_live) {
-    if (a.wk) wk = load8(a.wk + c * 8, a.vec_w);
-    if (a.wq) wq = load8(a.wq + c * 8, a.vec_w);
-    if (a.wk && whole) wkp = load8(a.wk + pc * 8, a.vec_w);
-    if (a.wq && whole) wqp = load8(a.wq + pc * 8, a.vec_w);
+  __device__ __forceinline__ Lane(const NormRopeArgs& a, int lane, uint8_t* lds) {
+    D = TPR ? TPR * 8 : a.D;
+    tpr = TPR ? TPR : a.D / 8;
+    rpw = 64 / tpr;
+    r = lane / tpr;
+    c = lane - r * tpr;
+    live = r < rpw;
+    half = a.R / 2;
+    chunks = a.R % 16 == 0;
+    pc = c * 8 >= a.R || a.interleaved || !chunks ? c : c * 8 < half ? c + half / 8 : c - half / 8;
+    wide = KOUT == 4 ? reinterpret_cast<Turn<double>*>(lds) : nullptr;
+    cs = reinterpret_cast<Turn<float>*>(lds + (KOUT == 4 ? 16 * D : 0));
+    uint16_t* rows = reinterpret_cast<uint16_t*>(cs + D);
+    mine = rows + (live ? r : 0) * D;
+    bytes = reinterpret_cast<uint8_t*>(rows + 512) + (live ? r : 0) * (D / 2);
   }
-  Kv4Run run{0, 1};
-  if (KOUT == 4) run = kv4_run(a.D / 32, c / 4);
 
-  struct Row {
-    u32x4 raw;
-    int64_t slot;
-    int tok, head, kind;
-    bool live;
-  };
-  auto load = [&](int batch) -> Row {
-    Row w;
-    w.kind = batch < nk ? kK : batch < nk + nv ? kV : kQ;     // uniform for the wave
-    const int H = w.kind == kQ ? a.Hq : a.Hk;
-    const int at = (batch - (w.kind == kK ? 0 : w.kind == kV ? nk : nk + nv)) * rpw + r;
-    w.live = lane_live && at < ntok * H;
-    w.tok = w.live ? at / H : 0;
-    w.head = w.live ? at - w.tok * H : 0;
-    w.raw = (u32x4){0u, 0u, 0u, 0u};
-    w.slot = -1;
-    const int64_t t = t0 + w.tok;
-    if (w.live) {
-      const uint16_t* p = w.kind == kQ ? a.q + t * a.q_stride : w.kind == kK ? a.k + t * a.k_stride : a.v + t * a.v_stride;
-      w.raw = load8(p + (int64_t)w.head * a.D + c * 8, a.vec_in);
-      if (KOUT && w.kind != kQ) w.slot = load_index(a.slots, a.slot64, t);
-    }
-    return w;
-  };
-  const int step = gridDim.y * kWaves, all = nk + nv + nq;
-  int batch = blockIdx.y * kWaves + wave;
-  Row next = load(batch);
-  if (a.R) token_angles(a, t0, ntok, wide, cs_all);
-  __syncthreads();
-  for (; batch < all; batch += step) {                        // uniform per wave
-    const Row cur = next;
-    next = load(batch + step);                                // the next batch's rows are in flight meanwhile
-    const int64_t t = t0 + cur.tok;
-    const uint16_t* w = cur.kind == kQ ? a.wq : cur.kind == kK ? a.wk : nullptr;
-    const bool turns = a.R && cur.kind != kV;
-    uint16_t* mine = rows[wave] + (lane_live ? r : 0) * a.D;
-    if (turns && !a.interleaved) {
-      // the wave's rows through its own LDS: written and read by this wave alone, in order
-      if (cur.live) st16(mine + c * 8, cur.raw);
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-    }
-    float f[8];
-    unpack8(cur.raw, f);
-    const bool turning = turns && cur.live && c * 8 < a.R;
-    const u32x4 wown = cur.kind == kQ ? wq : wk, wpart = cur.kind == kQ ? wqp : wkp;
-    uint32_t b[4];                                            // 4 bits: the lane's codes, channels 2 j and 2 j + 1 in b[j]
-    uint32_t sb = 0;
-    const bool exact = KOUT == 4 && cur.kind == kK && (a.R || w);
-    if (exact) {
-      double x[8], rho = 1.0;
+  // Over the lanes of a row, or of a group of 32 channels.
+  template <class T, class OP>
+  __device__ __forceinline__ T row(T v, OP op) const { return over_row<TPR>(v, tpr, r * tpr, c, op); }
+
+  __device__ __forceinline__ u32x4 load(const uint16_t* p, int batch, int H, int vec) const {
+    const int head = batch * rpw + r;
+    u32x4 raw = {0u, 0u, 0u, 0u};
+    if (live && head < H) raw = load8(p + head * D + c * 8, vec);
+    return raw;
+  }
+
+  // The channel that channel ch turns with.
+  __device__ __forceinline__ int partner(const NormRopeArgs& a, int ch) const {
+    return ch >= a.R ? ch : a.interleaved ? ch ^ 1 : ch < half ? ch + half : ch - half;
+  }
+  // This lane's weights, own and partners'.
+  __device__ __forceinline__ void weights(const NormRopeArgs& a, const uint16_t* w, u32x4* own, u32x4* part) const {
+    if (!live) return;
+    *own = load8(w + c * 8, a.vec_w);
+    if (a.interleaved) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = f[e];
-      if (w) {
-        double ss = 0.0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = __builtin_fma(x[e], x[e], ss);
-        ss = row_sum(ss, tpr, r * tpr, c);
-        rho = 1.0 / sqrt(ss / a.D + a.eps);
-        float v[8];
-        unpack8(wown, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= (double)v[e];
-      }
-      if (turning) rotate(a, mine, w, c, wide + cur.tok * half, wpart, x);
-      double am = 0.0;
-      int bad = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[e] *= rho;
-        am = fmax(am, fabs(x[e]));
-        bad |= !(fabs(x[e]) < __builtin_inf());
-      }
-      am = quad(am, [](double p, double q) { return fmax(p, q); });
-      bad = quad(bad, [](int p, int q) { return p | q; });
-      sb = kv4_f16_scale((float)(am / 6.0), am == 0.0, bad != 0);
-      e2m1_from_f64(x, (double)f16_value(sb), b);
+      for (int i = 0; i < 4; ++i) (*part)[i] = (*own)[i] >> 16 | (*own)[i] << 16;
+    } else if (chunks) {
+      *part = load8(w + pc * 8, a.vec_w);
     } else {
-      if (w) {
-        float ss = 0.0f, v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(f[e], f[e], ss);
-        ss = row_sum(ss, tpr, r * tpr, c);
-        const float rho = 1.0f / sqrtf(ss / (float)a.D + (float)a.eps);
-        unpack8(wown, v);
+      for (int i = 0; i < 4; ++i) (*part)[i] = w[partner(a, c * 8 + 2 * i)] | (uint32_t)w[partner(a, c * 8 + 2 * i + 1)] << 16;
+    }
+  }
+
+  // What channel e of the lane at place c and its partner are multiplied by, weights (if any) included.
+  template <class T>
+  __device__ __forceinline__ Turn<T> turn(int e, const Turn<T>* turns, bool weighted, u32x4 own, u32x4 part, int c) const {
+    auto at = [](u32x4 v, int i) { return (T)bf16_bits_to_f32(i & 1 ? v[i / 2] >> 16 : v[i / 2] & 0xFFFF); };
+    Turn<T> v = turns[e * tpr + c];
+    if (weighted) v.c *= at(own, e), v.s *= at(part, e);
+    return v;
+  }
+
+  // The partners of this lane's channels (x).
+  __device__ __forceinline__ void partners(const NormRopeArgs& a, u32x4 raw, bool there, const float* x, float* o) const {
+    if (a.interleaved) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= v[e];
-        if (turning) rotate(a, mine, w, c, cs_all + cur.tok * half, wpart, f);
+      for (int e = 0; e < 8; ++e) o[e] = x[e ^ 1];
+      return;
+    }
+    if (there) st16(mine + c * 8, raw);
+    wave_sync();
+    if (chunks) {
+      unpack8(ld16(mine + pc * 8), o);
+    } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] *= rho;
-      } else if (turning) {
-        rotate(a, mine, w, c, cs_all + cur.tok * half, wpart, f);
-      }
+      for (int e = 0; e < 8; ++e) o[e] = bf16_bits_to_f32(mine[partner(a, c * 8 + e)]);
     }
     __builtin_amdgcn_wave_barrier();                          // reads above before the next rows' writes
+  }
 
-    if (cur.kind == kQ || KOUT == 0) {
-      if (cur.live) {
-        uint16_t* out = (cur.kind == kQ ? a.q_out + t * a.q_out_stride : a.k_out + t * a.k_out_stride) +
-                        (int64_t)cur.head * a.D + c * 8;
-        const u32x4 p = {pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                         pack_bf16x2(f[6], f[7])};
-        if (a.vec_out) {
-          st16(out, p);
-        } else {
-          const uint32_t d[4] = {p.x, p.y, p.z, p.w};
+  // Rows of one batch of q or k in fp32, v their turns: f becomes the result.
+  __device__ __forceinline__ void norm_turn(const NormRopeArgs& a, u32x4 raw, bool there, bool normed, const Turn<float>* v,
+                                            float* f) const {
+    float rho = 1.0f, o[8];
+    if (normed) {
+      float ss = 0.0f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) out[e] = (uint16_t)(d[e / 2] >> (16 * (e & 1)));
-        }
+      for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(f[e], f[e], ss);
+      ss = row(ss, Add());
+      rho = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, 1.0f / (float)D, (float)a.eps));
+      if (__ballot(!(ss < __builtin_inff()))) {               // squares beyond fp32: the sum again, in 64 bits
+        double s2 = 0.0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s2 = __builtin_fma((double)f[e], (double)f[e], s2);
+        s2 = row(s2, Add());
+        if (!(ss < __builtin_inff())) rho = (float)(1.0 / sqrt(s2 / D + a.eps));
       }
-      continue;
     }
-    const bool stored = cur.live && cur.slot >= 0 && cur.slot < a.pool;
-    const int64_t at = cur.slot * a.Hk + cur.head;
+    partners(a, raw, there, f, o);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float y = __builtin_fmaf(o[e], v[e].s, f[e] * v[e].c);
+      f[e] = normed ? y * rho : y;
+    }
+  }
+
+  // The same in fp64, to 4-bit codes (two per byte) and the group's scale.
+  __device__ __forceinline__ uint32_t norm_turn_codes(const NormRopeArgs& a, u32x4 raw, bool there, const float* f, u32x4 own,
+                                                      u32x4 part, uint32_t* code) const {
+    float o[8];
+    partners(a, raw, there, f, o);
+    double y[8], rho = 1.0;
+    if (a.wk) {
+      double ss = 0.0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = __builtin_fma((double)f[e], (double)f[e], ss);
+      rho = 1.0 / sqrt(row(ss, Add()) / D + a.eps);
+    }
+    double am = 0.0, bad = 0.0;
+    int place = c;
+    asm volatile("" : "+v"(place), "+v"(own), "+v"(part));    // (angles and weights kept in fp64 for all batches: 190 registers)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const Turn<double> v = turn(e, wide, a.wk != nullptr, own, part, place);
+      y[e] = __builtin_fma((double)o[e], v.s, (double)f[e] * v.c) * rho;
+      am = fmax(am, fabs(y[e]));
+      bad = __builtin_fma(y[e], 0.0, bad);                    // NaN with a NaN or an infinity
+      if (e % 2) __builtin_amdgcn_sched_barrier(0);           // (all angles in registers at once: one wave fewer)
+    }
+    am = quad(am, Max());
+    bad = quad(bad, Add());
+    const uint32_t sb = kv4_f16_scale((float)(am / 6.0), am == 0.0, bad != 0.0);
+    e2m1_from_f64(y, (double)f16_value(sb), code);
+    return sb;
+  }
+
+  // bf16 as it came to 4-bit codes.  x has 8 bits and a border times s 14, so a quotient that is not on a
+  // border is 2^-14 or more away from it: x times a reciprocal (2^-22), to 16 bits, is on the right side, and on it
+  // where the quotient is.
+  __device__ __forceinline__ uint32_t codes4(const float* f, uint32_t* code) const {
+    uint32_t am = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) am = max(am, __builtin_bit_cast(uint32_t, f[e]) & 0x7FFFFFFFu);
+    am = quad(am, Max());
+    const uint32_t sb = kv4_f16_scale(__builtin_bit_cast(float, am) / 6.0f, am == 0, am >= 0x7F800000u);
+    const float s = f16_value(sb), r0 = __builtin_amdgcn_rcpf(s);
+    auto quotient = [&](float x) {
+      return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x * r0) + 0x80u) & 0xFFFFFF00u);
+    };
+#pragma unroll
+    for (int e = 0; e < 4; ++e) code[e] = f32x2_to_e2m1x2_sat(quotient(f[2 * e]), quotient(f[2 * e + 1]));
+    return sb;
+  }
+
+  __device__ __forceinline__ void store_bf16(uint16_t* out, const float* f, int vec) const {
+    const u32x4 p = {pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+    if (vec) {
+      st16(out, p);
+    } else {
+      const uint32_t d[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) out[e] = (uint16_t)(d[e / 2] >> (16 * (e & 1)));
+    }
+  }
+
+  // A row of 4-bit codes and its scales to entry `at` (there: this lane has a row, stored: it has a slot).
+  __device__ __forceinline__ void store4(Kv4Run run, const uint32_t* code, uint32_t sb, bool there, bool stored, uint8_t* codes,
+                                         uint16_t* scales, int64_t at) const {
+    if (there) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) bytes[run.first + (4 * (c & 3) + j) * run.step] = (uint8_t)code[j];
+    }
+    wave_sync();
+    if (there && stored) {
+      *reinterpret_cast<uint32_t*>(codes + at * (D / 2) + 4 * c) = *reinterpret_cast<const uint32_t*>(bytes + 4 * c);
+      if ((c & 3) == 0) scales[at * (D / 32) + c / 4] = (uint16_t)sb;
+    }
+    __builtin_amdgcn_wave_barrier();                          // reads above before the next rows' writes
+  }
+
+  __device__ __forceinline__ void store8_k(const float* f, bool there, uint8_t* codes, uint16_t* scales, int64_t at) const {
+    float am = 0.0f, d[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(f[e]));
+    const uint32_t sb = kv_f16_scale(quad(am, Max()), 127.0f);
+    const RcpDiv dv(f16_value(sb));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) d[e] = dv(f[e]);
+    if (!there) return;
+    const u32x2 p = {f32_to_i8_sat(d[0]) | (f32_to_i8_sat(d[1]) << 8) | (f32_to_i8_sat(d[2]) << 16) | (f32_to_i8_sat(d[3]) << 24),
+                     f32_to_i8_sat(d[4]) | (f32_to_i8_sat(d[5]) << 8) | (f32_to_i8_sat(d[6]) << 16) | (f32_to_i8_sat(d[7]) << 24)};
+    *reinterpret_cast<u32x2*>(codes + at * D + c * 8) = p;
+    if ((c & 3) == 0) scales[at * (D / 32) + c / 4] = (uint16_t)sb;
+  }
+
+  __device__ __forceinline__ void store8_v(const float* f, bool there, uint8_t* codes, uint16_t* scales, int64_t at) const {
+    float am = 0.0f, d[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(f[e]));
+    const uint32_t sb = kv_f16_scale(row(am, Max()), 448.0f);
+    const RcpDiv dv(f16_value(sb));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) d[e] = dv(f[e]);
+    if (!there) return;
+    const u32x2 p = {f32x4_to_e4m3x4_sat(d[0], d[1], d[2], d[3]), f32x4_to_e4m3x4_sat(d[4], d[5], d[6], d[7])};
+    *reinterpret_cast<u32x2*>(codes + at * D + c * 8) = p;
+    if (c == 0) scales[at] = (uint16_t)sb;
+  }
+};
+
+template <int KOUT, int TPR>
+__global__ __launch_bounds__(kWaves * 64, 1) void norm_rope_kernel(NormRopeArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int me = blockIdx.x * kWaves + wave;
+  const int t = me / a.shares;
+  if (t >= a.T) return;
+  const Lane<KOUT, TPR> l(a, lane, smem + (size_t)wave * a.lds_bytes);
+  // this wave's share of the token's batches of rows: K's first, then V's, then q's
+  const int share = me - t * a.shares, nk = (a.Hk + l.rpw - 1) / l.rpw, nv = KOUT ? nk : 0;
+  const int n = nk + nv + (a.Hq + l.rpw - 1) / l.rpw;
+  const int b0 = (int)((int64_t)n * share / a.shares), b1 = (int)((int64_t)n * (share + 1) / a.shares);
+  const int k0 = min(b0, nk), k1 = min(b1, nk), v0 = max(min(b0, nk + nv) - nk, 0), v1 = max(min(b1, nk + nv) - nk, 0);
+  const int q0 = max(b0 - nk - nv, 0), q1 = max(b1 - nk - nv, 0);
+  const uint16_t* qrow = a.q + (int64_t)t * a.q_stride;
+  const uint16_t* krow = a.k + (int64_t)t * a.k_stride;
+  const uint16_t* vrow = a.v + (int64_t)t * a.v_stride;
+  // the first rows and the weights, in flight while the angles are computed
+  u32x4 kraw = {0u, 0u, 0u, 0u}, vraw = kraw, qraw = kraw, wk = kraw, wkp = kraw, wq = kraw, wqp = kraw;
+  if (k0 < k1) kraw = l.load(krow, k0, a.Hk, a.vec_in);
+  if (KOUT && v0 < v1) vraw = l.load(vrow, v0, a.Hk, a.vec_in);
+  if (q0 < q1) qraw = l.load(qrow, q0, a.Hq, a.vec_in);
+  if (a.wk && k0 < k1) l.weights(a, a.wk, &wk, &wkp);
+  if (a.wq && q0 < q1) l.weights(a, a.wq, &wq, &wqp);
+  int64_t slot = -1;
+  if (KOUT && (k0 < k1 || v0 < v1)) slot = load_index(a.slots, a.slot64, t);
+  const bool stored = slot >= 0 && slot < a.pool;
+  Kv4Run run{0, 1};
+  if (KOUT == 4) run = kv4_run(l.D / 32, l.c / 4);
+
+  if (k0 < k1 || q0 < q1) token_turns(a, t, lane, l.tpr, k0 < k1 ? l.wide : nullptr, l.cs);
+  wave_sync();
+
+  float f[8];
+  Turn<float> v[8];
+  uint32_t code[4], sb;
+  if (k0 < k1 && KOUT != 4) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = l.turn(e, l.cs, a.wk != nullptr, wk, wkp, l.c);
+  }
+  for (int b = k0; b < k1; ++b) {
+    const u32x4 raw = kraw;
+    if (b + 1 < k1) kraw = l.load(krow, b + 1, a.Hk, a.vec_in);   // in flight meanwhile
+    const int head = b * l.rpw + l.r;
+    const bool there = l.live && head < a.Hk;
+    const int64_t at = slot * a.Hk + head;
+    unpack8(raw, f);
     if constexpr (KOUT == 4) {
-      if (!exact) {                                           // bf16 as it came: quotients in fp32 decide the same
-        uint32_t am = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) am = max(am, __builtin_bit_cast(uint32_t, f[e]) & 0x7FFFFFFFu);
-        am = quad(am, [](uint32_t p, uint32_t q) { return max(p, q); });
-        sb = kv4_f16_scale(__builtin_bit_cast(float, am) / 6.0f, am == 0, am >= 0x7F800000u);
-        const RcpDiv dv(f16_value(sb));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) b[e] = f32x2_to_e2m1x2_sat(dv(f[2 * e]), dv(f[2 * e + 1]));
-      }
-      uint8_t* code = bytes[wave] + (lane_live ? r : 0) * (a.D / 2);
-      if (cur.live) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) code[run.first + (4 * (c & 3) + j) * run.step] = (uint8_t)b[j];
-      }
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-      if (stored) {
-        const uint32_t d = *reinterpret_cast<const uint32_t*>(code + 4 * c);
-        uint8_t* codes = cur.kind == kK ? a.k_codes : a.v_codes;
-        uint16_t* scales = cur.kind == kK ? a.k_scales : a.v_scales;
-        *reinterpret_cast<uint32_t*>(codes + at * (a.D / 2) + 4 * c) = d;
-        if ((c & 3) == 0) scales[at * (a.D / 32) + c / 4] = (uint16_t)sb;
-      }
-      __builtin_amdgcn_wave_barrier();                        // reads above before the next rows' writes
-    } else if constexpr (KOUT == 8) {
-      float am = 0.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) am = fmaxf(am, fabsf(f[e]));
-      am = quad(am, [](float p, float q) { return fmaxf(p, q); });
-      if (cur.kind == kV) {                                   // one scale for the whole row
-        float rm = am;
-        for (int g = 4; g < tpr; g += 4) {
-          const int src = c + g >= tpr ? c + g - tpr : c + g;
-          rm = fmaxf(rm, __shfl(am, (r * tpr + src) & 63, 64));
-        }
-        am = rm;
-      }
-      if (stored) {
-        sb = kv_f16_scale(am, cur.kind == kK ? 127.0f : 448.0f);
-        const RcpDiv dv(f16_value(sb));
-        float d[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] = dv(f[e]);
-        if (cur.kind == kK) {
-          const u32x2 p = {f32_to_i8_sat(d[0]) | (f32_to_i8_sat(d[1]) << 8) | (f32_to_i8_sat(d[2]) << 16) |
-                               (f32_to_i8_sat(d[3]) << 24),
-                           f32_to_i8_sat(d[4]) | (f32_to_i8_sat(d[5]) << 8) | (f32_to_i8_sat(d[6]) << 16) |
-                               (f32_to_i8_sat(d[7]) << 24)};
-          *reinterpret_cast<u32x2*>(a.k_codes + at * a.D + c * 8) = p;
-          if ((c & 3) == 0) a.k_scales[at * (a.D / 32) + c / 4] = (uint16_t)sb;
-        } else {
-          const u32x2 p = {f32x4_to_e4m3x4_sat(d[0], d[1], d[2], d[3]), f32x4_to_e4m3x4_sat(d[4], d[5], d[6], d[7])};
-          *reinterpret_cast<u32x2*>(a.v_codes + at * a.D + c * 8) = p;
-          if (c == 0) a.v_scales[at] = (uint16_t)sb;
-        }
+      sb = a.R || a.wk ? l.norm_turn_codes(a, raw, there, f, wk, wkp, code) : l.codes4(f, code);
+      l.store4(run, code, sb, there, stored, a.k_codes, a.k_scales, at);
+    } else {
+      l.norm_turn(a, raw, there, a.wk != nullptr, v, f);
+      if constexpr (KOUT == 8) l.store8_k(f, there && stored, a.k_codes, a.k_scales, at);
+      else if (there) l.store_bf16(a.k_out + (int64_t)t * a.k_out_stride + head * l.D + l.c * 8, f, a.vec_out);
+    }
+  }
+  if constexpr (KOUT != 0) {
+    for (int b = v0; b < v1; ++b) {
+      const u32x4 raw = vraw;
+      if (b + 1 < v1) vraw = l.load(vrow, b + 1, a.Hk, a.vec_in);
+      const int head = b * l.rpw + l.r;
+      const bool there = l.live && head < a.Hk;
+      const int64_t at = slot * a.Hk + head;
+      unpack8(raw, f);
+      if constexpr (KOUT == 4) {
+        sb = l.codes4(f, code);
+        l.store4(run, code, sb, there, stored, a.v_codes, a.v_scales, at);
+      } else {
+        l.store8_v(f, there && stored, a.v_codes, a.v_scales, at);
       }
     }
+  }
+  if (q0 >= q1) return;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = l.turn(e, l.cs, a.wq != nullptr, wq, wqp, l.c);
+  for (int b = q0; b < q1; ++b) {
+    const u32x4 raw = qraw;
+    if (b + 1 < q1) qraw = l.load(qrow, b + 1, a.Hq, a.vec_in);
+    const int head = b * l.rpw + l.r;
+    const bool there = l.live && head < a.Hq;
+    unpack8(raw, f);
+    l.norm_turn(a, raw, there, a.wq != nullptr, v, f);
+    if (there) l.store_bf16(a.q_out + (int64_t)t * a.q_out_stride + head * l.D + l.c * 8, f, a.vec_out);
   }
 }
 
@@ -405,20 +497,31 @@ __global__ __launch_bounds__(256) void kv4_gather_kernel(const uint8_t* __restri
   }
 }
 
+template <int KOUT>
+hipError_t launch_kout(const NormRopeArgs& a, int grid, size_t lds, hipStream_t st) {
+  switch (a.D) {
+    case 64: norm_rope_kernel<KOUT, 8><<<grid, kWaves * 64, lds, st>>>(a); break;
+    case 96: norm_rope_kernel<KOUT, 12><<<grid, kWaves * 64, lds, st>>>(a); break;
+    case 128: norm_rope_kernel<KOUT, 16><<<grid, kWaves * 64, lds, st>>>(a); break;
+    case 192: norm_rope_kernel<KOUT, 24><<<grid, kWaves * 64, lds, st>>>(a); break;
+    case 256: norm_rope_kernel<KOUT, 32><<<grid, kWaves * 64, lds, st>>>(a); break;
+    default: norm_rope_kernel<KOUT, 0><<<grid, kWaves * 64, lds, st>>>(a);
+  }
+  return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_norm_rope(const NormRopeArgs& a, int kout, hipStream_t st) {
   NormRopeArgs b = a;
   const int rpw = 64 / (a.D / 8);
   const int batches = (a.Hq + rpw - 1) / rpw + (kout ? 2 : 1) * ((a.Hk + rpw - 1) / rpw);
-  b.TW = a.T >= 2048 ? 2 : 1;
-  const int gy = a.T < 1024 ? (batches + kWaves - 1) / kWaves : 1;
-  const dim3 grid((unsigned)((a.T + b.TW - 1) / b.TW), (unsigned)gy);
-  const size_t lds = (size_t)b.TW * a.R * (kout == 4 ? 12 : 4);
-  if (kout == 0) norm_rope_kernel<0><<<grid, kWaves * 64, lds, st>>>(b);
-  else if (kout == 8) norm_rope_kernel<8><<<grid, kWaves * 64, lds, st>>>(b);
-  else norm_rope_kernel<4><<<grid, kWaves * 64, lds, st>>>(b);
-  return hipGetLastError();
+  const int want = (2048 + a.T - 1) / a.T;
+  b.shares = want < batches ? want : batches;
+  b.lds_bytes = 8 * a.D + 1024 + (kout == 4 ? 16 * a.D + 256 : 0);     // at most 53 KB in all
+  const int grid = (int)(((int64_t)a.T * b.shares + kWaves - 1) / kWaves);
+  const size_t lds = (size_t)kWaves * b.lds_bytes;
+  return kout == 0 ? launch_kout<0>(b, grid, lds, st) : kout == 8 ? launch_kout<8>(b, grid, lds, st) : launch_kout<4>(b, grid, lds, st);
 }
 
 hipError_t launch_kv4_gather(const void* kq, const void* ks, const void* vq, const void* vs, int64_t pool, int H, int D,
