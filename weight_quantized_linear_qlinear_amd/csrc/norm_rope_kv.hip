@@ -9,12 +9,14 @@
 // Angles, their reduction and the cosines are in 64 bits; q, and a K that goes to bf16 or to 8-bit
 // codes, are computed in fp32 from there.  A K that goes to 4-bit codes is computed in fp64 altogether: next
 // to a border a code's neighbour is up to half of its value away, so that an order of fp32 additions
-// would show; the fp64 rate of a CU is the fp32 one, and K is a small share of the rows.
+// would show; the fp64 rate of a CU is the fp32 one, and K is a small share of the rows.  (In fp32, and in
+// fp64 only the batches in which a code or a scale is within fp32's error of a border, one in 12: 8191
+// tokens the same, 16 tokens 5.5 against 4.3 us.)
 //
-// A wave takes one token, or a share of its heads while tokens are few, and works on its own: no barrier.  It
-// computes the token's angles once, into its LDS.  A head row is D / 8 lanes, 8 channels each, so a
-// lane's channels stay the same from row to row, and what their rotation multiplies them and their
-// partners by (weights included: two operations per channel) stays in registers for all heads of q.
+// One wave of a workgroup takes a token, or four do (or a share of its heads, while tokens are few), and
+// compute its rotation once, channel by channel, into LDS.  A head row is D / 8 lanes, 8 channels each,
+// so a lane's channels stay the same from row to row, and what their rotation multiplies them and
+// their partners by (weights included: two operations per channel) stays in registers for all heads.
 // Rows pass through the wave's LDS for the partners, 4-bit codes for the order of the cache.
 #include "kv_rows.h"
 #include "qlq_launch.h"
@@ -57,14 +59,15 @@ __device__ __forceinline__ void sincos_quarter(double r, double* s, double* c) {
 
 // The rotation of token t, channel by channel, in fp32 and (where) in fp64: (factor cos, -+ factor sin); (1, 0)
 // from channel R on.  Channel ch stands at [ch % 8][ch / 8], so that the lanes of a row read side by side.
-__device__ __forceinline__ void token_turns(const NormRopeArgs& a, int64_t t, int lane, int tpr, Turn<double>* wide, Turn<float>* cs) {
+__device__ __forceinline__ void token_turns(const NormRopeArgs& a, int64_t t, int first, int step, int tpr, Turn<double>* wide,
+                                            Turn<float>* cs) {
   auto put = [&](int ch, double c, double s) {
     const int at = (ch & 7) * tpr + (ch >> 3);
     if (wide) wide[at] = {c, s};
     cs[at] = {(float)c, (float)s};
   };
   const int half = a.R / 2;
-  for (int i = lane; i < half; i += 64) {
+  for (int i = first; i < half; i += step) {
     const int64_t axis = a.axes ? min(max(a.axes[i], 0), a.A - 1) : 0;
     const int64_t pos = load_index(a.positions, a.pos64, axis * a.T + t);
     const double th = (double)pos * a.inv_freq[i];
@@ -79,7 +82,7 @@ __device__ __forceinline__ void token_turns(const NormRopeArgs& a, int64_t t, in
     put(a.interleaved ? 2 * i : i, cc, -ss);
     put(a.interleaved ? 2 * i + 1 : i + half, cc, ss);
   }
-  for (int ch = a.R + lane; ch < 8 * tpr; ch += 64) put(ch, 1.0, 0.0);
+  for (int ch = a.R + first; ch < 8 * tpr; ch += step) put(ch, 1.0, 0.0);
 }
 
 // Another lane's value, for steps within 4, 8 and 16 lanes in the vector unit.
@@ -140,20 +143,13 @@ __device__ __forceinline__ void wave_sync() {                 // the wave's LDS 
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Codes of 8 quotients y / s in 64 bits, rounded once; 2 per byte.
-__device__ __forceinline__ void e2m1_from_f64(const double* y, double s, uint32_t* b) {
-  const double inv = 1.0 / s;
-  float v[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    double q = y[e] * inv;
-    q = __builtin_fma(__builtin_fma(-q, s, y[e]), inv, q);    // (exact where the quotient is: ties stay ties)
-    // 21 bits, the last one set if anything is behind them: next to a border (3 bits) the side stays
-    const u32x2 w = __builtin_bit_cast(u32x2, q);
-    v[e] = (float)__builtin_bit_cast(double, (u32x2){0u, w.y | min(w.x, 1u)});
-  }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) b[e] = f32x2_to_e2m1x2_sat(v[2 * e], v[2 * e + 1]);
+// The quotient y / s to 21 bits, the last of them set if anything is behind it: next to a border between
+// codes (4 bits) the side stays, and a tie is one only where the quotient is.
+__device__ __forceinline__ float quotient(double y, double s, double inv) {
+  double q = y * inv;
+  q = __builtin_fma(__builtin_fma(-q, s, y), inv, q);
+  const u32x2 w = __builtin_bit_cast(u32x2, q);
+  return (float)__builtin_bit_cast(double, (u32x2){0u, w.y | min(w.x, 1u)});
 }
 
 // Where a lane stands in the rows of its wave, and the wave's LDS.  KOUT: where K goes: 0 to bf16 (or
@@ -171,7 +167,7 @@ struct Lane {
   uint16_t* mine;
   uint8_t* bytes;
 
-  __device__ __forceinline__ Lane(const NormRopeArgs& a, int lane, uint8_t* lds) {
+  __device__ __forceinline__ Lane(const NormRopeArgs& a, int lane, uint8_t* token, uint8_t* own) {
     D = TPR ? TPR * 8 : a.D;
     tpr = TPR ? TPR : a.D / 8;
     rpw = 64 / tpr;
@@ -181,9 +177,9 @@ struct Lane {
     half = a.R / 2;
     chunks = a.R % 16 == 0;
     pc = c * 8 >= a.R || a.interleaved || !chunks ? c : c * 8 < half ? c + half / 8 : c - half / 8;
-    wide = KOUT == 4 ? reinterpret_cast<Turn<double>*>(lds) : nullptr;
-    cs = reinterpret_cast<Turn<float>*>(lds + (KOUT == 4 ? 16 * D : 0));
-    uint16_t* rows = reinterpret_cast<uint16_t*>(cs + D);
+    wide = KOUT == 4 ? reinterpret_cast<Turn<double>*>(token) : nullptr;
+    cs = reinterpret_cast<Turn<float>*>(token + (KOUT == 4 ? 16 * D : 0));
+    uint16_t* rows = reinterpret_cast<uint16_t*>(own);
     mine = rows + (live ? r : 0) * D;
     bytes = reinterpret_cast<uint8_t*>(rows + 512) + (live ? r : 0) * (D / 2);
   }
@@ -227,22 +223,24 @@ struct Lane {
     return v;
   }
 
-  // The partners of this lane's channels (x).
-  __device__ __forceinline__ void partners(const NormRopeArgs& a, u32x4 raw, bool there, const float* x, float* o) const {
+  // The partners of this lane's channels.
+  __device__ __forceinline__ u32x4 partners(const NormRopeArgs& a, u32x4 raw, bool there) const {
+    u32x4 o;
     if (a.interleaved) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = x[e ^ 1];
-      return;
+      for (int i = 0; i < 4; ++i) o[i] = raw[i] >> 16 | raw[i] << 16;
+      return o;
     }
     if (there) st16(mine + c * 8, raw);
     wave_sync();
     if (chunks) {
-      unpack8(ld16(mine + pc * 8), o);
+      o = ld16(mine + pc * 8);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = bf16_bits_to_f32(mine[partner(a, c * 8 + e)]);
+      for (int i = 0; i < 4; ++i) o[i] = mine[partner(a, c * 8 + 2 * i)] | (uint32_t)mine[partner(a, c * 8 + 2 * i + 1)] << 16;
     }
     __builtin_amdgcn_wave_barrier();                          // reads above before the next rows' writes
+    return o;
   }
 
   // Rows of one batch of q or k in fp32, v their turns: f becomes the result.
@@ -263,7 +261,7 @@ struct Lane {
         if (!(ss < __builtin_inff())) rho = (float)(1.0 / sqrt(s2 / D + a.eps));
       }
     }
-    partners(a, raw, there, f, o);
+    unpack8(partners(a, raw, there), o);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float y = __builtin_fmaf(o[e], v[e].s, f[e] * v[e].c);
@@ -271,33 +269,35 @@ struct Lane {
     }
   }
 
-  // The same in fp64, to 4-bit codes (two per byte) and the group's scale.
+  // The same in fp64, to 4-bit codes (byte j: channels 2 j and 2 j + 1) and the group's scale.
   __device__ __forceinline__ uint32_t norm_turn_codes(const NormRopeArgs& a, u32x4 raw, bool there, const float* f, u32x4 own,
                                                       u32x4 part, uint32_t* code) const {
     float o[8];
-    partners(a, raw, there, f, o);
-    double y[8], rho = 1.0;
+    unpack8(partners(a, raw, there), o);
+    double y[8], rho = 1.0, am = 0.0, bad = 0.0;
     if (a.wk) {
       double ss = 0.0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = __builtin_fma((double)f[e], (double)f[e], ss);
       rho = 1.0 / sqrt(row(ss, Add()) / D + a.eps);
     }
-    double am = 0.0, bad = 0.0;
     int place = c;
-    asm volatile("" : "+v"(place), "+v"(own), "+v"(part));    // (angles and weights kept in fp64 for all batches: 190 registers)
+    asm volatile("" : "+v"(place), "+v"(own), "+v"(part));    // (turns and weights kept in fp64 for all batches: 190 registers)
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const Turn<double> v = turn(e, wide, a.wk != nullptr, own, part, place);
       y[e] = __builtin_fma((double)o[e], v.s, (double)f[e] * v.c) * rho;
       am = fmax(am, fabs(y[e]));
       bad = __builtin_fma(y[e], 0.0, bad);                    // NaN with a NaN or an infinity
-      if (e % 2) __builtin_amdgcn_sched_barrier(0);           // (all angles in registers at once: one wave fewer)
     }
     am = quad(am, Max());
     bad = quad(bad, Add());
     const uint32_t sb = kv4_f16_scale((float)(am / 6.0), am == 0.0, bad != 0.0);
-    e2m1_from_f64(y, (double)f16_value(sb), code);
+    const double s = (double)f16_value(sb), inv = 1.0 / s;
+    *code = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *code |= f32x2_to_e2m1x2_sat(quotient(y[2 * j], s, inv), quotient(y[2 * j + 1], s, inv)) << (8 * j);
     return sb;
   }
 
@@ -314,8 +314,9 @@ struct Lane {
     auto quotient = [&](float x) {
       return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x * r0) + 0x80u) & 0xFFFFFF00u);
     };
+    *code = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) code[e] = f32x2_to_e2m1x2_sat(quotient(f[2 * e]), quotient(f[2 * e + 1]));
+    for (int j = 0; j < 4; ++j) *code |= f32x2_to_e2m1x2_sat(quotient(f[2 * j]), quotient(f[2 * j + 1])) << (8 * j);
     return sb;
   }
 
@@ -331,11 +332,11 @@ struct Lane {
   }
 
   // A row of 4-bit codes and its scales to entry `at` (there: this lane has a row, stored: it has a slot).
-  __device__ __forceinline__ void store4(Kv4Run run, const uint32_t* code, uint32_t sb, bool there, bool stored, uint8_t* codes,
+  __device__ __forceinline__ void store4(Kv4Run run, uint32_t code, uint32_t sb, bool there, bool stored, uint8_t* codes,
                                          uint16_t* scales, int64_t at) const {
     if (there) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) bytes[run.first + (4 * (c & 3) + j) * run.step] = (uint8_t)code[j];
+      for (int j = 0; j < 4; ++j) bytes[run.first + (4 * (c & 3) + j) * run.step] = (uint8_t)(code >> (8 * j));
     }
     wave_sync();
     if (there && stored) {
@@ -375,24 +376,35 @@ struct Lane {
   }
 };
 
+// A batch of K rows in fp64 takes the time of about three of q (in units: what shares are cut by).
+template <int KOUT>
+constexpr int kUnitsK = KOUT == 4 ? 3 : 1;
+
 template <int KOUT, int TPR>
-__global__ __launch_bounds__(kWaves * 64, 1) void norm_rope_kernel(NormRopeArgs a) {
+__global__ __launch_bounds__(kWaves * 64) void norm_rope_kernel(NormRopeArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int me = blockIdx.x * kWaves + wave;
-  const int t = me / a.shares;
-  if (t >= a.T) return;
-  const Lane<KOUT, TPR> l(a, lane, smem + (size_t)wave * a.lds_bytes);
-  // this wave's share of the token's batches of rows: K's first, then V's, then q's
-  const int share = me - t * a.shares, nk = (a.Hk + l.rpw - 1) / l.rpw, nv = KOUT ? nk : 0;
-  const int n = nk + nv + (a.Hq + l.rpw - 1) / l.rpw;
-  const int b0 = (int)((int64_t)n * share / a.shares), b1 = (int)((int64_t)n * (share + 1) / a.shares);
-  const int k0 = min(b0, nk), k1 = min(b1, nk), v0 = max(min(b0, nk + nv) - nk, 0), v1 = max(min(b1, nk + nv) - nk, 0);
-  const int q0 = max(b0 - nk - nv, 0), q1 = max(b1 - nk - nv, 0);
+  const int D = TPR ? TPR * 8 : a.D;
+  // waves per token and workgroup, the token's place in the workgroup, this wave's share of the token
+  const int wpt = 1 << a.wpt_shift, tok = wave >> a.wpt_shift, shares = wpt * gridDim.y;
+  const int share = blockIdx.y * wpt + (wave & (wpt - 1));
+  const int t = blockIdx.x * (kWaves >> a.wpt_shift) + tok;
+  const bool here = t < a.T;
+  constexpr int kPerChannel = KOUT == 4 ? 24 : 8, kOwn = 1024 + (KOUT == 4 ? 256 : 0);
+  const Lane<KOUT, TPR> l(a, lane, smem + tok * kPerChannel * D,
+                          smem + (kWaves >> a.wpt_shift) * kPerChannel * D + wave * kOwn);
+  // the token's batches of rows in a line: K's, q's, V's (V's last, so that their wave has something to do
+  // while another one computes the rotation)
+  constexpr int UK = kUnitsK<KOUT>;
+  const int nk = (a.Hk + l.rpw - 1) / l.rpw, nv = KOUT ? nk : 0, nq = (a.Hq + l.rpw - 1) / l.rpw, n = UK * nk + nq + nv;
+  const int u0 = here ? n * share / shares : n, u1 = here ? n * (share + 1) / shares : n;
+  const int k0 = min((u0 + UK - 1) / UK, nk), k1 = min((u1 + UK - 1) / UK, nk);
+  const int q0 = min(max(u0 - UK * nk, 0), nq), q1 = min(max(u1 - UK * nk, 0), nq);
+  const int v0 = max(u0 - UK * nk - nq, 0), v1 = max(u1 - UK * nk - nq, 0);
   const uint16_t* qrow = a.q + (int64_t)t * a.q_stride;
   const uint16_t* krow = a.k + (int64_t)t * a.k_stride;
   const uint16_t* vrow = a.v + (int64_t)t * a.v_stride;
-  // the first rows and the weights, in flight while the angles are computed
+  // the first rows and the weights, in flight while the rotation is computed
   u32x4 kraw = {0u, 0u, 0u, 0u}, vraw = kraw, qraw = kraw, wk = kraw, wkp = kraw, wq = kraw, wqp = kraw;
   if (k0 < k1) kraw = l.load(krow, k0, a.Hk, a.vec_in);
   if (KOUT && v0 < v1) vraw = l.load(vrow, v0, a.Hk, a.vec_in);
@@ -403,48 +415,49 @@ __global__ __launch_bounds__(kWaves * 64, 1) void norm_rope_kernel(NormRopeArgs 
   if (KOUT && (k0 < k1 || v0 < v1)) slot = load_index(a.slots, a.slot64, t);
   const bool stored = slot >= 0 && slot < a.pool;
   Kv4Run run{0, 1};
-  if (KOUT == 4) run = kv4_run(l.D / 32, l.c / 4);
+  if (KOUT == 4) run = kv4_run(D / 32, l.c / 4);
 
-  if (k0 < k1 || q0 < q1) token_turns(a, t, lane, l.tpr, k0 < k1 ? l.wide : nullptr, l.cs);
-  wave_sync();
-
+  if (here) token_turns(a, t, (wave & (wpt - 1)) * 64 + lane, wpt * 64, l.tpr, l.wide, l.cs);
   float f[8];
+  uint32_t code, sb;
+  if constexpr (KOUT != 0) {
+    for (int b = v0; b < v1; ++b) {
+      const u32x4 raw = vraw;
+      if (b + 1 < v1) vraw = l.load(vrow, b + 1, a.Hk, a.vec_in);   // in flight meanwhile
+      const int head = b * l.rpw + l.r;
+      const bool there = l.live && head < a.Hk;
+      const int64_t at = slot * a.Hk + head;
+      unpack8(raw, f);
+      if constexpr (KOUT == 4) {
+        sb = l.codes4(f, &code);
+        l.store4(run, code, sb, there, stored, a.v_codes, a.v_scales, at);
+      } else {
+        l.store8_v(f, there && stored, a.v_codes, a.v_scales, at);
+      }
+    }
+  }
+  if (wpt > 1) __syncthreads();
+  else wave_sync();
+
   Turn<float> v[8];
-  uint32_t code[4], sb;
   if (k0 < k1 && KOUT != 4) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = l.turn(e, l.cs, a.wk != nullptr, wk, wkp, l.c);
   }
   for (int b = k0; b < k1; ++b) {
     const u32x4 raw = kraw;
-    if (b + 1 < k1) kraw = l.load(krow, b + 1, a.Hk, a.vec_in);   // in flight meanwhile
+    if (b + 1 < k1) kraw = l.load(krow, b + 1, a.Hk, a.vec_in);
     const int head = b * l.rpw + l.r;
     const bool there = l.live && head < a.Hk;
     const int64_t at = slot * a.Hk + head;
     unpack8(raw, f);
     if constexpr (KOUT == 4) {
-      sb = a.R || a.wk ? l.norm_turn_codes(a, raw, there, f, wk, wkp, code) : l.codes4(f, code);
+      sb = a.R || a.wk ? l.norm_turn_codes(a, raw, there, f, wk, wkp, &code) : l.codes4(f, &code);
       l.store4(run, code, sb, there, stored, a.k_codes, a.k_scales, at);
     } else {
       l.norm_turn(a, raw, there, a.wk != nullptr, v, f);
       if constexpr (KOUT == 8) l.store8_k(f, there && stored, a.k_codes, a.k_scales, at);
-      else if (there) l.store_bf16(a.k_out + (int64_t)t * a.k_out_stride + head * l.D + l.c * 8, f, a.vec_out);
-    }
-  }
-  if constexpr (KOUT != 0) {
-    for (int b = v0; b < v1; ++b) {
-      const u32x4 raw = vraw;
-      if (b + 1 < v1) vraw = l.load(vrow, b + 1, a.Hk, a.vec_in);
-      const int head = b * l.rpw + l.r;
-      const bool there = l.live && head < a.Hk;
-      const int64_t at = slot * a.Hk + head;
-      unpack8(raw, f);
-      if constexpr (KOUT == 4) {
-        sb = l.codes4(f, code);
-        l.store4(run, code, sb, there, stored, a.v_codes, a.v_scales, at);
-      } else {
-        l.store8_v(f, there && stored, a.v_codes, a.v_scales, at);
-      }
+      else if (there) l.store_bf16(a.k_out + (int64_t)t * a.k_out_stride + head * D + l.c * 8, f, a.vec_out);
     }
   }
   if (q0 >= q1) return;
@@ -457,7 +470,7 @@ __global__ __launch_bounds__(kWaves * 64, 1) void norm_rope_kernel(NormRopeArgs 
     const bool there = l.live && head < a.Hq;
     unpack8(raw, f);
     l.norm_turn(a, raw, there, a.wq != nullptr, v, f);
-    if (there) l.store_bf16(a.q_out + (int64_t)t * a.q_out_stride + head * l.D + l.c * 8, f, a.vec_out);
+    if (there) l.store_bf16(a.q_out + (int64_t)t * a.q_out_stride + head * D + l.c * 8, f, a.vec_out);
   }
 }
 
@@ -498,7 +511,25 @@ __global__ __launch_bounds__(256) void kv4_gather_kernel(const uint8_t* __restri
 }
 
 template <int KOUT>
-hipError_t launch_kout(const NormRopeArgs& a, int grid, size_t lds, hipStream_t st) {
+hipError_t launch_kout(const NormRopeArgs& in, hipStream_t st) {
+  NormRopeArgs a = in;
+  const int rpw = 64 / (a.D / 8), nk = (a.Hk + rpw - 1) / rpw;
+  const int n = (a.Hq + rpw - 1) / rpw + (kUnitsK<KOUT> + (KOUT ? 1 : 0)) * nk;    // units of a token
+  // A wave per token from 800 tokens on, four before that, and more workgroups per token while there are
+  // fewer than 1024.  Into 4 bits, 32 + 2 x 8 heads of 128, gathered back, us, four waves and one: 130 tokens 8.1 and
+  // 14.0, 500 12.7 and 15.0, 700 14.3 and 16.1, 1000 18.1 and 16.9; heads of 64, 16 + 2 x 16: 500 11.8 and 11.6, 1000
+  // 15.8 and 12.9; normed and turned alone 700 tokens 8.2 and 10.1, 1000 9.9 and 10.9.  Two waves: 2048
+  // tokens 21.9 against 21.2, 8191 62 against 60.
+  a.wpt_shift = 0;
+  int gy = 1;
+  if (a.T < 800) {
+    a.wpt_shift = 2;
+    gy = (1024 + a.T - 1) / a.T;
+    if (gy > (n + kWaves - 1) / kWaves) gy = (n + kWaves - 1) / kWaves;
+  }
+  const int per = kWaves >> a.wpt_shift;
+  const dim3 grid((unsigned)((a.T + per - 1) / per), (unsigned)gy);
+  const size_t lds = (size_t)per * (KOUT == 4 ? 24 : 8) * a.D + kWaves * (1024 + (KOUT == 4 ? 256 : 0));   // at most 54 KB
   switch (a.D) {
     case 64: norm_rope_kernel<KOUT, 8><<<grid, kWaves * 64, lds, st>>>(a); break;
     case 96: norm_rope_kernel<KOUT, 12><<<grid, kWaves * 64, lds, st>>>(a); break;
@@ -513,15 +544,7 @@ hipError_t launch_kout(const NormRopeArgs& a, int grid, size_t lds, hipStream_t 
 }  // namespace
 
 hipError_t launch_norm_rope(const NormRopeArgs& a, int kout, hipStream_t st) {
-  NormRopeArgs b = a;
-  const int rpw = 64 / (a.D / 8);
-  const int batches = (a.Hq + rpw - 1) / rpw + (kout ? 2 : 1) * ((a.Hk + rpw - 1) / rpw);
-  const int want = (2048 + a.T - 1) / a.T;
-  b.shares = want < batches ? want : batches;
-  b.lds_bytes = 8 * a.D + 1024 + (kout == 4 ? 16 * a.D + 256 : 0);     // at most 53 KB in all
-  const int grid = (int)(((int64_t)a.T * b.shares + kWaves - 1) / kWaves);
-  const size_t lds = (size_t)kWaves * b.lds_bytes;
-  return kout == 0 ? launch_kout<0>(b, grid, lds, st) : kout == 8 ? launch_kout<8>(b, grid, lds, st) : launch_kout<4>(b, grid, lds, st);
+  return kout == 0 ? launch_kout<0>(a, st) : kout == 8 ? launch_kout<8>(a, st) : launch_kout<4>(a, st);
 }
 
 hipError_t launch_kv4_gather(const void* kq, const void* ks, const void* vq, const void* vs, int64_t pool, int H, int D,

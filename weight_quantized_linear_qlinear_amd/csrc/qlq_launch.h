@@ -134,7 +134,7 @@ struct NormRopeArgs {
   uint8_t* v_codes;
   uint16_t* v_scales;
   int vec_in, vec_out, vec_w;  // 16-byte aligned rows, weights
-  int shares, lds_bytes;       // waves per token, LDS of each (set by the launcher)
+  int wpt_shift;               // log2 of the waves per token in a workgroup (set by the launcher)
 };
 // kout: 0 K to k_out (bf16; or no K), 8 or 4 K and V into a cache of that many bits.
 hipError_t launch_norm_rope(const NormRopeArgs& a, int kout, hipStream_t st);
