@@ -31,32 +31,71 @@ struct Runs {
   static_assert(P2 == 0 || P2 == 1 || P2 == 2, "two runs of a power of two");
 };
 
-// BYTES (1 .. 32, a power of two) at p, aligned to 16 at the most, as dwords.
+// Memory from p on, for loads at a lane's 32-bit offset plus a uniform one (no vector instructions for addresses).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t region(const uint8_t* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), 0, -1, kBufferWord3);
+}
+
+// BYTES (1 .. 32, a power of two) there, aligned to 16 at the most, as dwords.
 template <int BYTES>
 struct Bytes {
   static constexpr int N = BYTES < 4 ? 1 : BYTES / 4;
   uint32_t d[N];
-  __device__ __forceinline__ void load(const uint8_t* p) {
+  __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t rs, uint32_t lane, uint32_t at) {
     if constexpr (BYTES == 0) {
       d[0] = 0;
     } else if constexpr (BYTES == 1) {
-      d[0] = *p;
+      d[0] = (uint8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, lane, at, 0);
     } else if constexpr (BYTES == 2) {
-      d[0] = *reinterpret_cast<const uint16_t*>(p);
+      d[0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, lane, at, 0);
     } else if constexpr (BYTES == 4) {
-      d[0] = *reinterpret_cast<const uint32_t*>(p);
+      d[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, lane, at, 0);
     } else if constexpr (BYTES == 8) {
-      const u32x2 v = *reinterpret_cast<const u32x2*>(p);
+      const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rs, lane, at, 0));
       d[0] = v.x, d[1] = v.y;
     } else {
 #pragma unroll
       for (int i = 0; i < BYTES / 16; ++i) {
-        const u32x4 v = ld16(p + 16 * i);
+        const u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, lane + 16 * i, at, 0));
         d[4 * i] = v.x, d[4 * i + 1] = v.y, d[4 * i + 2] = v.z, d[4 * i + 3] = v.w;
       }
     }
   }
 };
+
+// Of two, neither a signalling NaN (fmaxf makes sure of that with an instruction each).
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, __builtin_inff()); }
+
+__device__ __forceinline__ float largest_across16(float v) {  // over lanes l, l ^ 16, l ^ 32, l ^ 48
+  const int i = __builtin_bit_cast(int, v);
+  const auto a = __builtin_amdgcn_permlane16_swap(i, i, false, false);
+  const int x = (int)a[0], y = (int)a[1], j = __builtin_bit_cast(int, larger(__builtin_bit_cast(float, x), __builtin_bit_cast(float, y)));
+  const auto b = __builtin_amdgcn_permlane32_swap(j, j, false, false);
+  const int z = (int)b[0], w = (int)b[1];
+  return larger(__builtin_bit_cast(float, z), __builtin_bit_cast(float, w));
+}
+
+// fp16(v_i e_i) of eight, the products in fp32: one instruction each (the compiler's own choice takes three for
+// two).  The first wait state is for an exponential among e, whose result the next instruction may not read.
+__device__ __forceinline__ f16x8 weigh(f16x8 v, const float (&e)[2][4]) {
+  const u32x4 d = __builtin_bit_cast(u32x4, v);
+  u32x4 w;
+  uint32_t w0, w1, w2, w3;
+  asm("s_nop 0\n\t"
+      "v_fma_mixlo_f16 %0, %4, %8, 0 op_sel_hi:[1,0,0]\n\t"
+      "v_fma_mixlo_f16 %1, %5, %10, 0 op_sel_hi:[1,0,0]\n\t"
+      "v_fma_mixlo_f16 %2, %6, %12, 0 op_sel_hi:[1,0,0]\n\t"
+      "v_fma_mixlo_f16 %3, %7, %14, 0 op_sel_hi:[1,0,0]\n\t"
+      "v_fma_mixhi_f16 %0, %4, %9, 0 op_sel:[1,0,0] op_sel_hi:[1,0,0]\n\t"
+      "v_fma_mixhi_f16 %1, %5, %11, 0 op_sel:[1,0,0] op_sel_hi:[1,0,0]\n\t"
+      "v_fma_mixhi_f16 %2, %6, %13, 0 op_sel:[1,0,0] op_sel_hi:[1,0,0]\n\t"
+      "v_fma_mixhi_f16 %3, %7, %15, 0 op_sel:[1,0,0] op_sel_hi:[1,0,0]"
+      : "=&v"(w0), "=&v"(w1), "=&v"(w2), "=&v"(w3)
+      : "v"(d.x), "v"(d.y), "v"(d.z), "v"(d.w), "v"(e[0][0]), "v"(e[0][1]), "v"(e[0][2]), "v"(e[0][3]), "v"(e[1][0]),
+        "v"(e[1][1]), "v"(e[1][2]), "v"(e[1][3]));
+  w = (u32x4){w0, w1, w2, w3};
+  return __builtin_bit_cast(f16x8, w);
+}
 
 // Octaves from a row's reference up to its largest weight: 2^15 is the largest power of two in fp16.
 constexpr float kLift = 15.0f;
@@ -155,25 +194,27 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttn
     Bytes<P1> v1[8];
     Bytes<P2> v2[8];
     KScales<NG> sc;                                            // lanes 0 .. 31: K scales of token lane, 32 .. 63: V's
+    const uint64_t sbase = (uint64_t)(uintptr_t)((lane < 32 ? a.k_scales : a.v_scales) + ((int64_t)c16 * hk + h) * NG);
+    const uint32_t sstep = (uint32_t)hk * NG * 2;
     auto load_k = [&](int e0, int e1) {                        // and the scales
-      const int64_t at = ((int64_t)(max(lane & 16 ? e1 : e0, 0) + c16)) * hk + h;
-      sc.load((lane < 32 ? a.k_scales : a.v_scales) + at * NG);
+      const int f0 = max(e0, 0), f1 = max(e1, 0);
+      sc.load(reinterpret_cast<const uint16_t*>(sbase + (uint64_t)(uint32_t)(lane & 16 ? f1 : f0) * sstep));
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint8_t* p = a.k_codes + ((int64_t)max(u ? e1 : e0, 0) * hk + h) * (D / 2);
-        k1[u].load(p + koff);
-        if constexpr (kTwo) k2[u].load(p + koff2);
+        const __amdgpu_buffer_rsrc_t rs = region(a.k_codes + ((int64_t)(u ? f1 : f0) * hk + h) * (D / 2));
+        k1[u].load(rs, koff, 0);
+        if constexpr (kTwo) k2[u].load(rs, koff2, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
     };
     auto load_v = [&](int e0, int e1) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const uint8_t* p = a.v_codes + ((int64_t)max(u ? e1 : e0, 0) * hk + h) * (D / 2);
+        const __amdgpu_buffer_rsrc_t rs = region(a.v_codes + ((int64_t)max(u ? e1 : e0, 0) * hk + h) * (D / 2));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          v1[4 * u + j].load(p + (size_t)j * row_bytes + voff);
-          if constexpr (kTwo) v2[4 * u + j].load(p + (size_t)j * row_bytes + voff2);
+          v1[4 * u + j].load(rs, voff, j * row_bytes);
+          if constexpr (kTwo) v2[4 * u + j].load(rs, voff2, j * row_bytes);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -233,7 +274,7 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttn
         }
         // 2^E >= the largest: its exponent + 1 (a zero counts as the smallest scale)
         const float f = fmaxf(f16_lo(top), 0x1p-24f);
-        if (lane >= 32) mine.ev[spos] = (float)min(__builtin_amdgcn_frexp_expf(f), 17);
+        if (lane >= 32) mine.ev[spos] = (float)__builtin_amdgcn_frexp_expf(f);       // (0 for a NaN or an infinity)
       }
       wave_sync();
 
@@ -259,7 +300,7 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttn
             const f32x4 d = mfma_f16_k32(kf, qf[r][n], (f32x4){0.f, 0.f, 0.f, 0.f});
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              s[r][u][j] = n == 0 ? (float)ks[n][4 * u + j] * d[j] : __builtin_fmaf((float)ks[n][4 * u + j], d[j], s[r][u][j]);
+              s[r][u][j] = __builtin_fmaf((float)ks[n][4 * u + j], d[j], n == 0 ? 0.0f : s[r][u][j]);
           }
         }
       }
@@ -275,7 +316,7 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttn
       float e[R][2][4];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        float mx = kNegInf;
+        float mx = kNegInf, f = cs[r];                         // scores are s f
         if (!open) {
 #pragma unroll
           for (int u = 0; u < 2; ++u)
@@ -283,20 +324,16 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttn
             for (int j = 0; j < 4; ++j) {
               const int t = t0 + 16 * u + j;
               const bool see = there(u, j) && (!a.causal || t <= qpos[r]) && (a.window <= 0 || t > qpos[r] - a.window);
-              s[r][u][j] = see ? s[r][u][j] * cs[r] : kNegInf;
+              s[r][u][j] = see ? s[r][u][j] * f : kNegInf;
             }
-        } else {
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[r][u][j] *= cs[r];
+          f = 1.0f;
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) mx = fmaxf(mx, s[r][u][j] + ev[u][j]);
-        mx = max_across16(mx);
-        const float mn = fmaxf(m[r], mx - kLift);
+          for (int j = 0; j < 4; ++j) mx = larger(mx, __builtin_fmaf(s[r][u][j], f, ev[u][j]));
+        mx = largest_across16(mx);
+        const float mn = larger(m[r], mx - kLift);
         const float ref = mn == kNegInf ? 0.0f : mn;
         if (__ballot(mn > m[r])) {
           const float corr = __builtin_amdgcn_exp2f(m[r] - ref);
@@ -311,7 +348,7 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttn
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            e[r][u][j] = __builtin_amdgcn_exp2f(s[r][u][j] - ref);
+            e[r][u][j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][u][j], f, -ref));
             l[r] += e[r][u][j];
           }
       }
@@ -322,9 +359,7 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttn
         const f16x8 vs = __builtin_bit_cast(f16x8, ld16(&mine.s[1][n][8 * g4]));
         f16x8 w[R];
 #pragma unroll
-        for (int r = 0; r < R; ++r)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) w[r][i] = (_Float16)__builtin_fmaf((float)vs[i], e[r][i / 4][i & 3], 0.0f);
+        for (int r = 0; r < R; ++r) w[r] = weigh(vs, e[r]);
         const int b = n < P1 ? n : n - P1;                     // byte of the lane's run
         u32x4 lo, hi;                                          // channels 2 c16 and 2 c16 + 1: tokens 2 i, 2 i + 1
 #pragma unroll
