@@ -130,6 +130,48 @@ def test_single_tokens_ragged_lengths(heads, page):
     assert a.shape == p.check(what="decode through q_start").shape
 
 
+# Neighbouring KV heads that a workgroup takes together, by their number and channels: eight, four, two and ones
+# that have none, and query rows of one and of two groups of 16.
+TOGETHER = [(8, 8, 64), (16, 16, 64), (8, 4, 128), (12, 12, 128), (16, 8, 128), (20, 20, 128), (2, 2, 256), (6, 6, 256),
+            (12, 12, 256), (8, 8, 256), (6, 6, 64), (10, 10, 128), (3, 3, 256), (12, 6, 96)]
+
+
+@pytest.mark.parametrize("heads", TOGETHER)
+@pytest.mark.parametrize("page", [16, 64])
+def test_neighbouring_heads(heads, page):
+    Hq, Hk, D = heads
+    print(f"attention4 neighbouring heads={heads} page={page}", flush=True)
+    p = Problem(Hq + D + page, [1] * 6, [0, 1, 31, 700, 4099, 12345], Hq, Hk, D, page)
+    a = p.check(what="decode")
+    assert torch.equal(a, p.run()), "the same again"
+    p.check(window=100, what="decode, window")
+    p = Problem(Hq + D, [3, 1, 0, 11], [3, 900, 40, 2000], Hq, Hk, D, page, each=False)
+    p.check(what="several query tokens")
+    p.check(causal=False, what="not causal")
+    p.check(window=70, what="several query tokens, window")
+    p = Problem(Hq * D, [26], [5000], Hq, Hk, D, page, each=False)       # rows of the second group
+    p.check(what="one sequence")
+
+
+@pytest.mark.parametrize("heads", [(8, 8, 64), (4, 4, 128), (8, 8, 128), (2, 2, 256), (8, 8, 256)])
+def test_neighbouring_heads_bad_pages_and_unseen_entries(heads):
+    Hq, Hk, D = heads
+    print(f"attention4 neighbouring heads, bad pages heads={heads}", flush=True)
+    p = Problem(D + Hk, (1, 1, 1), (200, 64, 890), Hq, Hk, D, 16, each=False)
+    t = p.table.copy()
+    t[0, 2], t[1, :], t[2, 0], t[2, 5], t[0, 7] = -1, p.pool // 16, 1 << 30, -(1 << 31), p.pool // 16
+    out, lse = torch.full((p.T, Hq, D), 9.0, dtype=torch.bfloat16, device=dev()), torch.zeros((p.T, Hq), device=dev())
+    qlq.kv_attention(p.q, p.cache, _gpu(t.astype(np.int32), torch.int32), p.sl, 16, q_start=p.q0, out=out, lse=lse)
+    p.compare(out, lse, t, p.lens, what="bad pages")
+    assert not out[1].any()
+    out = p.check(window=40, what="before")
+    for b, L in enumerate(p.lens):
+        at = torch.from_numpy(p.used(b)[:L - 40]).to(dev())
+        p.cache.k_codes[at], p.cache.v_codes[at] = 0x77, 0xFF
+        p.cache.k_scales[at], p.cache.v_scales[at] = float("nan"), float("inf")
+    assert torch.equal(p.run(window=40), out)
+
+
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 4096])
 def test_page_sizes(page):
     Problem(page, [1, 1, 1], [5, 33, 300], 4, 2, 64, page).check(what=f"page {page}")
