@@ -190,6 +190,34 @@ HEADS = [(28, 4, 128, 128), (16, 16, 64, 64), (3, 1, 96, 96), (2, 2, 192, 64), (
          (1, 2, 224, 224), (2, 1, 512, 512)]
 
 
+def test_norms_whose_products_or_squares_leave_fp32():
+    # Rows and weights whose products x w are beyond fp32 though the results are not, beside rows of ordinary size;
+    # squares that fp32 loses beside an eps as small (powers of two move nothing in the derivation of the bounds).
+    rng = np.random.default_rng(77)
+    T, H, D = 9, 6, 128
+    spin_gpu, spin = _spin(rng, T, D, 1)
+    f, pos, _ = spin_gpu
+    for gain, wgain, eps in ((2.0 ** 123, 2.0 ** 20, 1e-6), (2.0 ** 66, 2.0 ** 63, 1e-6), (2.0 ** -72, 1.0, 2.0 ** -140),
+                             (2.0 ** -60, 8.0, 2.0 ** -126), (2.0 ** -40, 1.0, 2.0 ** -70)):
+        b = rng.standard_normal((T, H, D))
+        b[1::2] *= gain
+        b[::2] *= max(gain, 1e-3) if gain < 1 else 1.0
+        xb = oracle.f32_to_bf16_bits(b.astype(np.float32))
+        x, x64 = bf16_to_gpu(xb), bits_to_f64(xb)
+        wb = oracle.f32_to_bf16_bits((wgain * (1 + 0.3 * rng.standard_normal(D))).astype(np.float32))
+        w, w64 = bf16_to_gpu(wb), bits_to_f64(wb)
+        for inter in (False, True):
+            q, k = qlq.norm_rope(x, x, w, w, pos, f, eps=eps, interleaved=inter)
+            want, top = _turned(x64, w64, spin, inter, eps=float(np.float32(eps)))
+            _check_rows(q, want, top, f"q, gain {gain:.0e}")
+            assert torch.equal(q, k)
+        cache = qlq.kv_cache(64, H, D, device=dev(), bits=4)
+        at = torch.arange(T, device=dev())
+        qlq.norm_rope_kv_append(x, x, x, w, w, pos, f, cache, at, eps=eps)
+        want, _ = _turned(x64, w64, spin, False, eps=float(np.float32(eps)))
+        _check_entries4(cache, np.arange(T), want, x64, f"gain {gain:.0e}")
+
+
 @pytest.mark.parametrize("normed", [False, True])
 @pytest.mark.parametrize("inter", [False, True])
 @pytest.mark.parametrize("heads", HEADS)

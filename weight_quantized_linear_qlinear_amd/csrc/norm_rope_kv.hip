@@ -247,21 +247,30 @@ struct Lane {
   __device__ __forceinline__ void norm_turn(const NormRopeArgs& a, u32x4 raw, bool there, bool normed, const Turn<float>* v,
                                             float* f) const {
     float rho = 1.0f, o[8];
+    bool big = false;
     if (normed) {
       float ss = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = __builtin_fmaf(f[e], f[e], ss);
       ss = row(ss, Add());
       rho = __builtin_amdgcn_rsqf(__builtin_fmaf(ss, 1.0f / (float)D, (float)a.eps));
-      if (__ballot(!(ss < __builtin_inff()))) {               // squares beyond fp32: the sum again, in 64 bits
+      // squares beyond fp32, or (eps below 2^-64) lost under it: the sum again, in 64 bits
+      big = !(ss < __builtin_inff());
+      const bool lost = big || a.eps < 0x1p-64f;
+      if (__ballot(lost)) {
         double s2 = 0.0;
 #pragma unroll
         for (int e = 0; e < 8; ++e) s2 = __builtin_fma((double)f[e], (double)f[e], s2);
         s2 = row(s2, Add());
-        if (!(ss < __builtin_inff())) rho = (float)(1.0 / sqrt(s2 / D + a.eps));
+        if (lost) rho = (float)((big ? 0x1p64 : 1.0) / sqrt(s2 / D + a.eps));
       }
     }
     unpack8(partners(a, raw, there), o);
+    if (__ballot(big)) {                                      // x 2^-64: its products with weights stay in fp32
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (big) f[e] *= 0x1p-64f, o[e] *= 0x1p-64f;
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float y = __builtin_fmaf(o[e], v[e].s, f[e] * v[e].c);
