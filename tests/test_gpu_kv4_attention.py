@@ -172,6 +172,25 @@ def test_neighbouring_heads_bad_pages_and_unseen_entries(heads):
     assert torch.equal(p.run(window=40), out)
 
 
+@pytest.mark.parametrize("heads", [(64, 64, 32), (48, 48, 64), (96, 24, 96), (10, 10, 192)])
+def test_heads_of_long_lines_together(heads):
+    # more than ten tiles of 32 tokens for every wave of a head: a workgroup's waves take neighbouring heads; and one
+    # token less per sequence, where lengths change the choice under one and the same launch
+    Hq, Hk, D = heads
+    groups = Hk // (4 if Hk % 4 == 0 else 2)
+    waves = max(256 // groups // 8 * 8, 1) * (8 if D <= 128 else 4) * groups // Hk
+    n = 32 * (10 * waves // 3 + 4)
+    print(f"attention4 long lines heads={heads} tokens=3x{n}", flush=True)
+    p = Problem(D, [1, 1, 1], [n + 5, n, n - 700], Hq, Hk, D, 64)
+    a = p.check(what="together")
+    p.lens = [n // 2, n, 9]
+    p.sl.copy_(torch.tensor(p.lens, dtype=torch.int32))
+    p.check(what="one head each")
+    p.lens = [n + 5, n, n - 700]
+    p.sl.copy_(torch.tensor(p.lens, dtype=torch.int32))
+    assert torch.equal(p.run(), a)
+
+
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 4096])
 def test_page_sizes(page):
     Problem(page, [1, 1, 1], [5, 33, 300], 4, 2, 64, page).check(what=f"page {page}")

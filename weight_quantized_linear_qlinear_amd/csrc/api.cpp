@@ -1223,6 +1223,7 @@ static qlq_status run_attention(int bits, const void* q, int64_t q_stride, int64
   a.parts = p.parts;
   a.tile_rows = p.tile_rows;
   a.hw_shift = p.hw_shift;
+  a.together = p.together;
   a.level_counters = (int)p.counters;
   a.counters = static_cast<uint32_t*>(workspace);
   a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kAttnCounterBytes);

@@ -14,6 +14,14 @@
 // nibbles of two tokens are put into one byte, which the conversion turns into the pair that the
 // matrix unit wants.  Scales come one token per lane (K's in the lower, V's in the upper half of the
 // wave) and reach the lanes of the scores through the wave's LDS, in the order of their tokens there.
+//
+// Bound by HBM and by instruction issue alike, two waves per SIMD (237 registers): 64 tokens over up to 16384
+// each, 32 heads over 8 of 128 (755 MB), 169 us, 4.5 TB/s; without the arithmetic about 155, with the arithmetic alone about
+// as long.  A row is half a cache line at 128 channels, and the two heads that share one are read by two waves.
+// One token over 131071, 28 heads over 4 of 128: 33 us, where the bytes take 15: a start of four trips to
+// memory and two levels of joining, about 14 us.  A wave takes 16 rows; more rows are more tiles, which
+// read K and V again, mostly from L2: pairs of tiles per wave (32 rows) spill, 16 sequences of 32 rows
+// over 4000 tokens 90 us against 54.
 #include <type_traits>
 
 #include "kv_attention.h"
@@ -102,8 +110,10 @@ __device__ __forceinline__ f16x8 weigh(f16x8 v, const float (&e)[2][4]) {
 // Octaves from a row's reference up to its largest weight: 2^15 is the largest power of two in fp16.
 constexpr float kLift = 15.0f;
 
+// Waves per workgroup, one workgroup per CU.  Heads of 192 and 256 channels have 300 registers, one wave per
+// SIMD; held to 256 with eight waves, in us: 32 tokens over up to 9000 each 98 -> 89 and 126 -> 117, but 48 rows of
+// 256 x 16 over 4000 55 -> 81, 24 rows over 20000 46 -> 61, 32 rows of 192 x 16 over 4000 56 -> 68.
 constexpr int waves_of(int NG) { return NG <= 4 ? 8 : 4; }
-constexpr bool pairs_rows(int NG) { return NG == 3 || NG == 4; }
 
 // A wave's LDS: the token scales of its tile, in the order in which lanes hold the tokens (lane group
 // g: 4 g .. 4 g + 3, then 16 more), or what joining needs.
@@ -116,26 +126,28 @@ union WaveLds {
   JoinLds join;
 };
 
-template <int NG, int R>
+template <int NG>
 __global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttnArgs a) {
-  constexpr int D = 32 * NG, TR = 16 * R, kWaves = waves_of(NG), P1 = Runs<NG>::P1, P2 = Runs<NG>::P2;
+  constexpr int D = 32 * NG, TR = 16, kWaves = waves_of(NG), P1 = Runs<NG>::P1, P2 = Runs<NG>::P2;
   constexpr bool kTwo = P2 > 0;
   __shared__ __align__(16) WaveLds<NG> lds[kWaves];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   WaveLds<NG>& mine = lds[wave];
-  // Neighbouring KV heads per workgroup, one per wave, and kWaves / HW waves on a head's line; the
-  // head groups of one part sit on one XCD (workgroup b goes to XCD b % 8).
-  const int HW = 1 << a.hw_shift, HG = a.Hk >> a.hw_shift, TS = kWaves >> a.hw_shift;
+  // A head's units are cut over `waves` waves.  A workgroup's waves are on HW neighbouring KV heads, or all
+  // on one; the workgroups on one stretch of the heads' lines sit on one XCD (workgroup b goes to XCD b % 8).
+  const Extent mine_e = lane < a.B ? extent_of(a, lane) : Extent{};
+  const int total = total_units<TR>(a, mine_e, lane), waves = a.parts * (kWaves >> a.hw_shift);
+  const int U = max(1, (total + waves - 1) / waves);
+  const int hw_shift = U > a.together ? a.hw_shift : 0, HW = 1 << hw_shift, HG = a.Hk >> hw_shift;
+  const int parts = a.parts >> (a.hw_shift - hw_shift), TS = kWaves >> hw_shift;
   int part = blockIdx.x / HG, hg = blockIdx.x % HG;
-  if (a.parts % 8 == 0) {
+  if (parts % 8 == 0) {
     const int li = blockIdx.x >> 3;
     part = (li / HG) * 8 + (blockIdx.x & 7);
     hg = li % HG;
   }
-  const int h = hg * HW + (wave & (HW - 1)), me = part * TS + (wave >> a.hw_shift);   // head, place on its line
-  const Extent mine_e = lane < a.B ? extent_of(a, lane) : Extent{};
-  const int total = total_units<TR>(a, mine_e, lane);
-  const int U = max(1, (total + a.parts * TS - 1) / (a.parts * TS)), u_end = min(total, (me + 1) * U);
+  const int h = hg * HW + (wave & (HW - 1)), me = part * TS + (wave >> hw_shift);     // head, place on its line
+  const int u_end = min(total, (me + 1) * U);
   for (int u = me * U; u < u_end;) {
     const Tile it = tile_of<TR>(a, mine_e, u, lane);
     if (it.units == 0) break;                                  // (only if lengths change meanwhile or overflow the sum)
@@ -157,27 +169,22 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttn
     asm volatile("" : "+v"(c16), "+v"(g4));                    // (nothing computed from them outlives a tile)
 
     // q's rows (packed: query token, then head of the group), channels 32 n + 8 g4 .. + 7.
-    u32x4 qraw[R][NG];
-    int qpos[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int row = r0 + 16 * r + c16;
+    u32x4 qraw[NG];
+    int qpos;
+    {
+      const int row = r0 + c16;
       const bool live = row < rows;
       const int i = live ? row / a.G : i0, g = live ? row - i * a.G : 0;
-      qpos[r] = live ? p0 + i : -1;
+      qpos = live ? p0 + i : -1;
       const uint16_t* qp = a.q + (int64_t)(it.e.qs + i) * a.q_stride + (int64_t)(h * a.G + g) * D + 8 * g4;
 #pragma unroll
-      for (int n = 0; n < NG; ++n) qraw[r][n] = ld16(qp + 32 * n);
+      for (int n = 0; n < NG; ++n) qraw[n] = ld16(qp + 32 * n);
     }
 
-    f32x4 o[NG][2][R];
-    float m[R], l[R];
+    f32x4 o[NG][2];                                            // [group][channel of the pair]: channels 2 (4 g4 + j) + 0, 1 of it
+    float m = kNegInf, l = 0.0f;
 #pragma unroll
-    for (int n = 0; n < NG; ++n)
-#pragma unroll
-      for (int r = 0; r < R; ++r) o[n][0][r] = o[n][1][r] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int r = 0; r < R; ++r) m[r] = kNegInf, l[r] = 0.0f;
+    for (int n = 0; n < NG; ++n) o[n][0] = o[n][1] = (f32x4){0.f, 0.f, 0.f, 0.f};
 
     // Tiles start at multiples of 32 tokens and pages hold 16 or more, so each half of a tile lies in
     // one page, whose first entry is uniform.  -1: the page is outside the pool (its tokens are left out).
@@ -227,15 +234,14 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttn
     load_v(e0, e1);
 
     // q: per query row a power of two into [-1, 1), fp16; rows past the last are zero.
-    f16x8 qf[R][NG];
-    float cs[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const bool live = r0 + 16 * r + c16 < rows;
+    f16x8 qf[NG];
+    float cs;
+    {
+      const bool live = r0 + c16 < rows;
       float f[NG][8], am = 0.0f;
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
-        const uint32_t d[4] = {qraw[r][n].x, qraw[r][n].y, qraw[r][n].z, qraw[r][n].w};
+        const uint32_t d[4] = {qraw[n].x, qraw[n].y, qraw[n].z, qraw[n].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           f[n][2 * e] = live ? bf16_bits_to_f32(d[e] & 0xFFFF) : 0.0f;
@@ -248,8 +254,8 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttn
 #pragma unroll
       for (int n = 0; n < NG; ++n)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) qf[r][n][e] = (_Float16)__builtin_ldexpf(f[n][e], -ex);
-      cs[r] = __builtin_ldexpf(a.scale * kLog2e, ex);
+        for (int e = 0; e < 8; ++e) qf[n][e] = (_Float16)__builtin_ldexpf(f[n][e], -ex);
+      cs = __builtin_ldexpf(a.scale * kLog2e, ex);
     }
 
     const int spos = ((lane >> 2) & 3) * 8 + ((lane >> 4) & 1) * 4 + (lane & 3);   // token lane % 32 in the order of the scores
@@ -281,7 +287,7 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttn
       wave_sync();
 
       // S^T: tokens 16 u + 4 g4 + j, query c16
-      float s[R][2][4];
+      float s[2][4];
       f16x8 ks[NG];
 #pragma unroll
       for (int n = 0; n < NG; ++n) ks[n] = __builtin_bit_cast(f16x8, ld16(&mine.s[0][n][8 * g4]));
@@ -296,14 +302,9 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttn
             kw[i] = n < P1 ? e2m1x2_to_f16(k1[u].d[(n < P1 ? at : 0) / 4], at % 4)
                            : e2m1x2_to_f16(k2[u].d[(n < P1 ? 0 : at) / 4], at % 4);
           }
-          const f16x8 kf = __builtin_bit_cast(f16x8, kw);
+          const f32x4 d = mfma_f16_k32(__builtin_bit_cast(f16x8, kw), qf[n], (f32x4){0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            const f32x4 d = mfma_f16_k32(kf, qf[r][n], (f32x4){0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              s[r][u][j] = __builtin_fmaf((float)ks[n][4 * u + j], d[j], n == 0 ? 0.0f : s[r][u][j]);
-          }
+          for (int j = 0; j < 4; ++j) s[u][j] = __builtin_fmaf((float)ks[n][4 * u + j], d[j], n == 0 ? 0.0f : s[u][j]);
         }
       }
       float ev[2][4];
@@ -315,53 +316,48 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttn
 
       // whole tile visible to every row?
       const bool open = all_valid && (!a.causal || base + 31 <= p0 + i0) && (a.window <= 0 || base > p0 + i1 - a.window);
-      float e[R][2][4];
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        float mx = kNegInf, f = cs[r];                         // scores are s f
-        if (!open) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int t = t0 + 16 * u + j;
-              const bool see = there(u, j) && (!a.causal || t <= qpos[r]) && (a.window <= 0 || t > qpos[r] - a.window);
-              s[r][u][j] = see ? s[r][u][j] * f : kNegInf;
-            }
-          f = 1.0f;
-        }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) mx = larger(mx, __builtin_fmaf(s[r][u][j], f, ev[u][j]));
-        mx = largest_across16(mx);
-        const float mn = larger(m[r], mx - kLift);
-        const float ref = mn == kNegInf ? 0.0f : mn;
-        if (__ballot(mn > m[r])) {
-          const float corr = __builtin_amdgcn_exp2f(m[r] - ref);
-          l[r] *= corr;
-#pragma unroll
-          for (int n = 0; n < NG; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[n][0][r][j] *= corr, o[n][1][r][j] *= corr;
-          m[r] = mn;
-        }
+      float e[2][4];
+      float mx = kNegInf, f = cs;                              // scores are s f
+      if (!open) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            e[r][u][j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r][u][j], f, -ref));
-            l[r] += e[r][u][j];
+            const int t = t0 + 16 * u + j;
+            const bool see = there(u, j) && (!a.causal || t <= qpos) && (a.window <= 0 || t > qpos - a.window);
+            s[u][j] = see ? s[u][j] * f : kNegInf;
           }
+        f = 1.0f;
       }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx = larger(mx, __builtin_fmaf(s[u][j], f, ev[u][j]));
+      mx = largest_across16(mx);
+      const float mn = larger(m, mx - kLift);
+      const float ref = mn == kNegInf ? 0.0f : mn;
+      if (__ballot(mn > m)) {
+        const float corr = __builtin_amdgcn_exp2f(m - ref);
+        l *= corr;
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[n][0][j] *= corr, o[n][1][j] *= corr;
+        m = mn;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          e[u][j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][j], f, -ref));
+          l += e[u][j];
+        }
 
       // O^T: per group, the weights times their V scales, and the channel pairs' two rows of V^T
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
         const f16x8 vs = __builtin_bit_cast(f16x8, ld16(&mine.s[1][n][8 * g4]));
-        f16x8 w[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) w[r] = weigh(vs, e[r]);
+        const f16x8 w = weigh(vs, e);
         const int b = n < P1 ? n : n - P1;                     // byte of the lane's run
         u32x4 lo, hi;                                          // channels 2 c16 and 2 c16 + 1: tokens 2 i, 2 i + 1
 #pragma unroll
@@ -371,18 +367,15 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttn
           lo[i] = e2m1x2_to_f16(even, b % 4);
           hi[i] = e2m1x2_to_f16(odd, b % 4);
         }
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-          o[n][0][r] = mfma_f16_k32(__builtin_bit_cast(f16x8, lo), w[r], o[n][0][r]);
-          o[n][1][r] = mfma_f16_k32(__builtin_bit_cast(f16x8, hi), w[r], o[n][1][r]);
-        }
+        o[n][0] = mfma_f16_k32(__builtin_bit_cast(f16x8, lo), w, o[n][0]);
+        o[n][1] = mfma_f16_k32(__builtin_bit_cast(f16x8, hi), w, o[n][1]);
       }
       load_v(n0, n1);
       e0 = n0;
       e1 = n1;
     }
 
-    // A lane has, per 16-row subtile, channels 32 n + 8 g4 .. + 7 of its row.
+    // A lane has channels 32 n + 8 g4 .. + 7 of its row.
     asm volatile("" : "+v"(c16), "+v"(g4));
     const bool split = ck.count > 1;
     const __amdgpu_buffer_rsrc_t rs = partial_rsrc(a.partials, a.partials_bytes);
@@ -391,28 +384,24 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttn
       const int i = grow / a.G;
       return (int64_t)(it.e.qs + i) * a.Hq + h * a.G + (grow - i * a.G);
     };
+    const float Lsum = sum_across16(l);                    // over the lane groups of a query
+    if (r0 + c16 < rows) {
+      const int64_t at = split ? part_row(ck.mine, c16) : out_row(r0 + c16);
+      const float inv = Lsum == 0.0f ? 0.0f : 1.0f / Lsum;     // (NaN stays NaN)
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float Lsum = sum_across16(l[r]);                   // over the lane groups of a query
-      const int row = 16 * r + c16;
-      if (r0 + row < rows) {
-        const int64_t at = split ? part_row(ck.mine, row) : out_row(r0 + row);
-        const float inv = Lsum == 0.0f ? 0.0f : 1.0f / Lsum;   // (NaN stays NaN)
+      for (int n = 0; n < NG; ++n) {
+        float v[8];
 #pragma unroll
-        for (int n = 0; n < NG; ++n) {
-          float v[8];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[2 * j] = o[n][0][r][j], v[2 * j + 1] = o[n][1][r][j];
-          if (split) store_run<8>(rs, at + 32 * n + 8 * g4, v);
-          else store_out<8>(a.out + at * D + 32 * n + 8 * g4, v, inv);
-        }
-        if (g4 == 0) {
-          if (split) {
-            const float ml[2] = {m[r], Lsum};
-            store_run<2>(rs, at + D, ml);
-          } else if (a.lse) {
-            a.lse[at] = Lsum == 0.0f ? kNegInf : (m[r] + __builtin_amdgcn_logf(Lsum)) * kLn2;
-          }
+        for (int j = 0; j < 4; ++j) v[2 * j] = o[n][0][j], v[2 * j + 1] = o[n][1][j];
+        if (split) store_run<8>(rs, at + 32 * n + 8 * g4, v);
+        else store_out<8>(a.out + at * D + 32 * n + 8 * g4, v, inv);
+      }
+      if (g4 == 0) {
+        if (split) {
+          const float ml[2] = {m, Lsum};
+          store_run<2>(rs, at + D, ml);
+        } else if (a.lse) {
+          a.lse[at] = Lsum == 0.0f ? kNegInf : (m + __builtin_amdgcn_logf(Lsum)) * kLn2;
         }
       }
     }
@@ -425,12 +414,7 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttn
 
 template <int NG>
 hipError_t launch_ng(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t st) {
-  if constexpr (pairs_rows(NG))
-    if (p.R == 2) {
-      kv4_attention_kernel<NG, 2><<<(int)p.grid, waves_of(NG) * 64, 0, st>>>(a);
-      return hipGetLastError();
-    }
-  kv4_attention_kernel<NG, 1><<<(int)p.grid, waves_of(NG) * 64, 0, st>>>(a);
+  kv4_attention_kernel<NG><<<(int)p.grid, waves_of(NG) * 64, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -439,17 +423,28 @@ hipError_t launch_ng(const KvAttnArgs& a, const KvAttnPlan& p, hipStream_t st) {
 KvAttnPlan plan_kv4_attention(int64_t T, int64_t B, int64_t Hk, int64_t G, int64_t D, bool one_each) {
   KvAttnPlan p;
   const int64_t rows = one_each ? G : (T + B - 1) / B * G;   // query rows of an average sequence
-  const bool pairs = pairs_rows((int)(D / 32));
-  if (rows > (pairs ? 32 : 64)) return plan_kv_attention(T, B, Hk, G, D, one_each);   // the many-row kernel's
-  p.R = rows <= 16 || !pairs ? 1 : 2;
-  const int64_t TR = 16 * p.R;
+  const int NG = (int)(D / 32);
+  // From here on the many-row kernel.  16 and 64 sequences, in us, this kernel and that one: heads of 64, 96 rows 46
+  // and 58, 74 and 73; 128: 55 and 62, 75 and 74, 192 rows x 64: 122 and 87; of 96, 64 rows 45 and 63, 96: 57 and 67,
+  // 128: 72 and 71; of 128, 64 rows 80 and 97, 106 and 163, 96: 97 and 106, 185 and 168, 128: 123 and 117; of 192, 64
+  // rows 80 and 80, 112 and 110, 96: 98 and 114, 180 and 147; of 256 (where that one spills), 96 rows 78 and
+  // 145, 256 rows x 64: 260 and 351.
+  if (rows > (NG <= 2 ? 96 : NG == 8 ? 256 : 64)) return plan_kv_attention(T, B, Hk, G, D, one_each);
+  constexpr int64_t TR = 16;
+  // Heads per workgroup.  Four that share cache lines, where every wave has more than ten tiles to take; else one, whose
+  // chunks then sit close together.  Four and one, in us: 32 heads over 8 of 128, 64 tokens over 4000 each 82 and 96, over
+  // 30000 x 4 46 and 53, over 131071 49 and 55, over 30000 23.0 and 21.6, over 8000 19.0 and 16.6; 16 of 64, 4 over
+  // 30000 57 and 69, 1 over 8000 16.6 and 15.8; several tiles of rows, 24 rows over 20000 39 and 34 (32 over 8 of 128),
+  // 25.7 and 22.1 (16 over 4 of 64).  A row of 256 channels is a line: one (1 over 8000 27 and 25).  Eight
+  // heads instead of four: within 2 %, several rows 20 % slower.
   while ((2 << p.hw_shift) <= 4 && Hk % (2 << p.hw_shift) == 0) ++p.hw_shift;
-  const int waves = waves_of((int)(D / 32));
   const int64_t HG = Hk >> p.hw_shift;
   const int64_t parts = 256 / HG;                              // one workgroup per CU
   p.parts = (int)(parts >= 8 ? parts / 8 * 8 : parts < 1 ? 1 : parts);
+  p.together = NG == 8 || rows > TR ? 1 << 30 : 10;
+  if (p.parts % (1 << p.hw_shift) != 0) p.together = 0;        // (many heads, few workgroups for each: no other cut)
   p.grid = p.parts * HG;
-  p.waves = p.parts * (waves >> p.hw_shift);
+  p.waves = p.parts * (waves_of(NG) >> p.hw_shift);
   p.tile_rows = (int)(one_each && G < TR ? G : TR);
   p.counters = 2 * p.waves * Hk;
   p.tiles = one_each ? B * ((G + TR - 1) / TR) : T * G / TR + B;

@@ -158,7 +158,7 @@ struct KvAttnArgs {
   int page_shift, pages, max_pages, max_tokens;
   float scale;
   int causal, window;
-  int parts, tile_rows, hw_shift, level_counters;
+  int parts, tile_rows, hw_shift, together, level_counters;
   uint32_t* counters;
   float* partials;
   uint32_t partials_bytes;
@@ -166,6 +166,7 @@ struct KvAttnArgs {
 struct KvAttnPlan {
   int R = 1;                   // 16-row subtiles of query rows per wave (16: per workgroup, kv_attention_tile.hip)
   int hw_shift = 0;            // log2 of the KV heads per workgroup
+  int together = 0;            // 4 bits: ... where a wave has more units than this, else one
   int parts = 1;               // workgroups per group of heads
   int64_t waves = 1;           // parts that a head's work is cut into
   int64_t counters = 0;        // arrival counters per level of joining
