@@ -1,4 +1,4 @@
-// Attention over the paged 8-bit KV cache for many query rows per KV head (a prompt chunk over
+// Attention over the paged KV cache of 8 or 4 bits for many query rows per KV head (a prompt chunk over
 // its cached prefix).  The same definition, cache and cutting of the work as kv_attention.hip;
 // what differs is where the time goes: with hundreds of rows per K and V load it is the matrix
 // cores and the vector unit (exponentials, conversions), not HBM.
@@ -21,6 +21,10 @@
 // share a SIMD; the matrix cores are busy 31 % of the time, LDS 25 %.  Measured (MI355X): two chunks of
 // 1500 and 804 queries over 8192 and 4394 tokens, 32 heads over 8 of 128, 313 to 333 us (235 GFLOP,
 // 730 TFLOP/s); a prompt of 512 tokens on its own 49 us, half of it storing and joining partial sums.
+//
+// Over 4 bits (rows in the order of kv_rows.h) K and V come with an fp16 scale per 32 channels each; K' and V' are
+// the same, V's scales by group, their common 2^-E over all of a token's groups.  A tile's conversion is shared by
+// 256 rows, so the cache's width hardly shows: the two chunks above 320 us.
 #include <type_traits>
 
 #include "kv_attention.h"
