@@ -272,6 +272,26 @@ def test_kv_append_four_bits_without_rotation(D):
         _check_entries4(cache, np.arange(T), k64, v64, f"{T},{H}")
 
 
+@pytest.mark.parametrize("H,D", [(3, 128), (1, 256), (5, 384), (2, 512), (3, 96), (1, 32), (7, 224)])
+@pytest.mark.parametrize("n", [1, 67])
+def test_gather_four_bits_of_any_codes_and_scales(H, D, n):
+    print(f"gather4 H={H} D={D} n={n}", flush=True)
+    rng = np.random.default_rng(D + n)
+    P = 40
+    kc, vc = (rng.integers(0, 256, size=(P, H, D // 2)).astype(np.uint8) for _ in range(2))
+    ks, vs = (oracle.fp16_encode(rng.uniform(1e-3, 900, size=(P, H, D // 32)).astype(np.float32)) for _ in range(2))
+    up = lambda a, t: torch.from_numpy(a).view(t).to(dev())
+    cache = qlq.QuantizedKV4(up(kc, torch.uint8), up(ks, torch.float16), up(vc, torch.uint8), up(vs, torch.float16))
+    at = rng.integers(0, P, size=n)
+    at[n // 2], at[-1] = (-1, P) if n > 2 else (3, 3)
+    gk, gv = qlq.kv_gather(cache, torch.from_numpy(at).to(dev()))
+    inside = (at >= 0) & (at < P)
+    for got, c, sc in ((gk, kc, ks), (gv, vc, vs)):
+        want = np.zeros((n, H, D))
+        want[inside] = kvcache.kv4_values(c, sc)[at[inside]]
+        assert np.array_equal(bf16_bits(got), oracle.f32_to_bf16_bits(want.astype(np.float32)))
+
+
 @pytest.mark.parametrize("rotated", [False, True])
 def test_four_bit_groups_of_zeros_extremes_and_nans(rotated):
     T, D = 8, 96

@@ -21,7 +21,9 @@
 //
 // Bound by HBM for many tokens: 8192 tokens of 32 + 8 heads of 128, normed and turned, 33 us, 5.0 TB/s; by its one round of
 // waves for fewer (4095 tokens of 16 + 16 heads of 64 11 us, 3.0 TB/s; one token 3.7 us).  Into 4 bits by K's fp64 too: 8191
-// tokens of 32 + 8 + 8 heads of 128 48 us, 3.7 TB/s; 2048 tokens 17 us, two waves per SIMD.  Into 8 bits 333 tokens 6.7 us.
+// tokens of 32 + 8 + 8 heads of 128 40 us, 4.4 TB/s; 2048 tokens 17 us, two waves per SIMD.  Into 8 bits 333 tokens 6.7 us.
+#include <type_traits>
+
 #include "kv_rows.h"
 #include "qlq_launch.h"
 
@@ -393,8 +395,14 @@ struct Lane {
 template <int KOUT>
 constexpr int kUnitsK = KOUT == 4 ? 3 : 1;
 
+// Waves per SIMD that the registers have to leave room for.  Into 4 bits, from 128 channels on, four: q's weights are
+// then read behind K's rows, and spills of up to 12 bytes are worth it (us, three and four, heads of 128, 8191 tokens 61
+// and 54, 3000 the same; of 256 54 and 48; of 160 50 and 46; of 64, 3000 tokens 20.1 and 21.6, 8192 the same).
 template <int KOUT, int TPR>
-__global__ __launch_bounds__(kWaves * 64) void norm_rope_kernel(NormRopeArgs a) {
+constexpr int kRoom = KOUT == 4 && (TPR == 0 || TPR >= 16) ? 4 : 1;
+
+template <int KOUT, int TPR>
+__global__ __launch_bounds__(kWaves * 64, (kRoom<KOUT, TPR>)) void norm_rope_kernel(NormRopeArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int D = TPR ? TPR * 8 : a.D;
@@ -423,7 +431,7 @@ __global__ __launch_bounds__(kWaves * 64) void norm_rope_kernel(NormRopeArgs a) 
   if (KOUT && v0 < v1) vraw = l.load(vrow, v0, a.Hk, a.vec_in);
   if (q0 < q1) qraw = l.load(qrow, q0, a.Hq, a.vec_in);
   if (a.wk && k0 < k1) l.weights(a, a.wk, &wk, &wkp);
-  if (a.wq && q0 < q1) l.weights(a, a.wq, &wq, &wqp);
+  if (KOUT != 4 && a.wq && q0 < q1) l.weights(a, a.wq, &wq, &wqp);
   int64_t slot = -1;
   if (KOUT && (k0 < k1 || v0 < v1)) slot = load_index(a.slots, a.slot64, t);
   const bool stored = slot >= 0 && slot < a.pool;
@@ -474,6 +482,7 @@ __global__ __launch_bounds__(kWaves * 64) void norm_rope_kernel(NormRopeArgs a) 
     }
   }
   if (q0 >= q1) return;
+  if (KOUT == 4 && a.wq) l.weights(a, a.wq, &wq, &wqp);
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = l.turn(e, l.cs, a.wq != nullptr, wq, wqp, l.c);
   for (int b = q0; b < q1; ++b) {
@@ -488,7 +497,7 @@ __global__ __launch_bounds__(kWaves * 64) void norm_rope_kernel(NormRopeArgs a) 
 }
 
 // Rows of chosen slots of a 4-bit cache back to bf16 (8 channels per thread); a slot outside the pool
-// gives zeros.  Bound by its loads of single bytes: 8191 tokens of 8 heads of 128 (43 MB) 12.7 us, 3.4 TB/s.
+// gives zeros.  For rows that kv4_gather_quads_kernel does not take; bound by its loads of single bytes.
 __global__ __launch_bounds__(256) void kv4_gather_kernel(const uint8_t* __restrict__ kq, const uint16_t* __restrict__ ks,
                                                          const uint8_t* __restrict__ vq, const uint16_t* __restrict__ vs,
                                                          int64_t pool, int H, int D, const void* __restrict__ slots,
@@ -520,6 +529,61 @@ __global__ __launch_bounds__(256) void kv4_gather_kernel(const uint8_t* __restri
     }
     st16(ko + i * 8, k);
     st16(vo + i * 8, v);
+  }
+}
+
+// The same where a row's groups are a multiple of four: a thread takes channels 8 j .. 8 j + 7 of four groups, whose
+// bytes 4 j .. 4 j + 3 of a run are dwords (in runs of four groups 16 bytes side by side).  Bound by HBM: 8191 tokens of 8
+// heads of 128 (43 MB) 8.9 us, 4.8 TB/s; byte by byte 12.5 (with heads of 256, 8192 tokens and their append, 47.0 and 48.0).
+__global__ __launch_bounds__(256) void kv4_gather_quads_kernel(const uint8_t* __restrict__ kq, const uint16_t* __restrict__ ks,
+                                                               const uint8_t* __restrict__ vq, const uint16_t* __restrict__ vs,
+                                                               int64_t pool, int H, int NG, const void* __restrict__ slots,
+                                                               int slot64, int64_t total, uint16_t* __restrict__ ko,
+                                                               uint16_t* __restrict__ vo) {
+  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+  const uint32_t quads = NG / 4, each = (uint32_t)H * NG;     // threads per slot
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += stride) {
+    const int64_t n = i / each;
+    const uint32_t e = (uint32_t)(i - n * each), j = e & 3, hq = e >> 2, h = hq / quads, g0 = 4 * (hq - h * quads);
+    const int64_t slot = load_index(slots, slot64, n);
+    const bool there = slot >= 0 && slot < pool;
+    const int64_t row = there ? slot * H + h : 0;
+    const Kv4Run run = kv4_run(NG, g0);
+    const int64_t at = row * (16 * NG) + run.first + 4 * j * run.step;
+    uint32_t kd[4], vd[4];
+    if (run.step == 4) {
+      const u32x4 a = ld16(kq + at), b = ld16(vq + at);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) kd[c] = a[c], vd[c] = b[c];
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        kd[c] = *reinterpret_cast<const uint32_t*>(kq + at + c * run.step);
+        vd[c] = *reinterpret_cast<const uint32_t*>(vq + at + c * run.step);
+      }
+    }
+    uint16_t kss[4], vss[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) kss[g] = ks[row * NG + g0 + g], vss[g] = vs[row * NG + g0 + g];
+    const int64_t out = ((n * H + h) * NG + g0) * 32 + 8 * j;
+    auto put = [&](auto G) {
+      constexpr int g = decltype(G)::value;
+      auto value8 = [&](const uint32_t (&d)[4], float s) {
+        u32x4 r;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const f32x2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(d[c], 1.0f, g);
+          r[c] = there ? pack_bf16x2(v.x * s, v.y * s) : 0u;
+        }
+        return r;
+      };
+      st16(ko + out + 32 * g, value8(kd, f16_value(kss[g])));
+      st16(vo + out + 32 * g, value8(vd, f16_value(vss[g])));
+    };
+    put(std::integral_constant<int, 0>());
+    put(std::integral_constant<int, 1>());
+    put(std::integral_constant<int, 2>());
+    put(std::integral_constant<int, 3>());
   }
 }
 
@@ -562,9 +626,17 @@ hipError_t launch_norm_rope(const NormRopeArgs& a, int kout, hipStream_t st) {
 
 hipError_t launch_kv4_gather(const void* kq, const void* ks, const void* vq, const void* vs, int64_t pool, int H, int D,
                              const void* slots, int slot64, int64_t n, void* ko, void* vo, hipStream_t st) {
-  const int64_t n8 = n * H * D / 8;
-  int64_t g = (n8 + 255) / 256;
+  const bool quads = D % 128 == 0;
+  const int64_t n8 = n * H * D / 8, total = quads ? n8 / 4 : n8;
+  int64_t g = (total + 255) / 256;
   if (g > 8192) g = 8192;
+  if (quads) {
+    kv4_gather_quads_kernel<<<(int)g, 256, 0, st>>>(static_cast<const uint8_t*>(kq), static_cast<const uint16_t*>(ks),
+                                                   static_cast<const uint8_t*>(vq), static_cast<const uint16_t*>(vs), pool, H,
+                                                   D / 32, slots, slot64, total, static_cast<uint16_t*>(ko),
+                                                   static_cast<uint16_t*>(vo));
+    return hipGetLastError();
+  }
   kv4_gather_kernel<<<(int)g, 256, 0, st>>>(static_cast<const uint8_t*>(kq), static_cast<const uint16_t*>(ks),
                                            static_cast<const uint8_t*>(vq), static_cast<const uint16_t*>(vs), pool, H, D,
                                            slots, slot64, n8, static_cast<uint16_t*>(ko), static_cast<uint16_t*>(vo));
