@@ -437,7 +437,8 @@ qlq_status qlq_kv4_gather(const void* k_codes, const void* k_scales, const void*
  * qlq_kv4_attention_workspace_bytes; one buffer may serve both operators' calls on one stream).  Code and
  * scale buffers 16-byte aligned.  k_t = k_code k_scale and v_t = v_code v_scale are not rounded with few rows;
  * weights times V scales are rounded to fp16: 2^-11, 2^-40 of the row's largest below 2^-29 of it.  With many
- * rows (as in qlq_kv_attention) K, V and the weights are rounded to 11 bits each. */
+ * rows (on average more than 64 per KV head and sequence, 96 for D 32 and 64, 256 for D 256) K, V and the
+ * weights are rounded to 11 bits each. */
 qlq_status qlq_kv4_attention(const void* q_bf16, int64_t q_stride, int64_t T, int64_t B, int64_t Hq, int64_t Hk,
                              int64_t D, const void* k_codes, const void* k_scales, const void* v_codes,
                              const void* v_scales, int64_t pool, const int32_t* block_table, int64_t max_pages,

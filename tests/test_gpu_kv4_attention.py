@@ -101,7 +101,7 @@ class Problem:
         A = abs(sc) * max((np.abs(q[:, h]) @ ku[:, h // (self.Hq // self.Hk)].T).max() for h in range(self.Hq)) if used.size else 0.0
         E = U * (42 * A + A1 + 3 * (2 * A + 56) + n / 32 + 40)
         W, tail = 2.0 ** -11, 2.0 ** -36
-        if -(-self.T // len(lens)) * (self.Hq // self.Hk) > (32 if self.D in (96, 128) else 64):
+        if -(-self.T // len(lens)) * (self.Hq // self.Hk) > {32: 96, 64: 96, 256: 256}.get(self.D, 64):
             E, W, tail = E + 2.0 ** -11 * A + U * A1, 2 * W, 2.0 ** -31
         got = bits_to_f64(bf16_bits(out))
         assert np.all(np.isfinite(got)), what
