@@ -545,3 +545,43 @@ def test_binding_refusals_on_the_gpu():
     for kw in (dict(page_size=24), dict(page_size=16, window=-1), dict(page_size=16, workspace=small)):
         with pytest.raises(qlq.QlqError):
             qlq.kv_attention(p.q, c, p.bt, p.sl, **kw)
+
+
+def _seeing(p, b, t, causal, window):
+    """The rows of sequence b that see its token t."""
+    pos = p.lens[b] - p.nqs[b] + np.arange(p.nqs[b])
+    see = (t <= pos) if causal else np.ones(pos.size, bool)
+    if window:
+        see &= t > pos - window
+    return p.starts[b] + np.nonzero(see)[0]
+
+
+def _check_nan_groups(p, bad, causal=True, window=0, what=""):
+    """V scales of (sequence, token, KV head, group) in `bad` become NaN: NaN in those channels of the rows that see the
+    token, and everything else as with the finite scales, to its bound."""
+    clean, lse, G = p.check(causal=causal, window=window, what=what), torch.zeros(p.T, p.Hq, device=dev()), p.Hq // p.Hk
+    want = torch.zeros(clean.shape, dtype=torch.bool)
+    for b, t, h, g in bad:
+        p.cache.v_scales[int(p.used(b)[t]), h, g] = float("nan")
+        want[torch.from_numpy(_seeing(p, b, t, causal, window)), h * G:(h + 1) * G, 32 * g:32 * g + 32] = True
+    out = p.run(causal=causal, window=window, lse=lse)
+    want = want.to(dev())
+    assert torch.equal(torch.isnan(out), want), f"{what}: {int((torch.isnan(out) & ~want).sum())} NaN more, {int((~torch.isnan(out) & want).sum())} fewer"
+    p.compare(torch.where(want, clean, out), lse, p.table, p.lens, causal=causal, window=window, what=what)
+
+
+@pytest.mark.parametrize("heads", [(4, 2, 64), (2, 1, 96), (4, 1, 128), (2, 1, 256), (3, 1, 192)])
+@pytest.mark.parametrize("case", [((1,), (700,)), ((1, 1, 1), (40, 100, 9000)), ((3,), (500,)), ((150,), (250,))])
+def test_groups_beside_a_nan_scale_of_the_heaviest_token(case, heads):
+    # the token that outweighs all others has a NaN scale in one group and V scales of 2^6 and more in its others
+    (nqs, lens), (Hq, Hk, D) = case, heads
+    print(f"attention4 NaN scale of the heaviest token nqs={nqs} heads={heads}", flush=True)
+    p = Problem(sum(lens) + D, nqs, lens, Hq, Hk, D, 16, each=False, qgain=4.0)
+    q, k, bad = bits_to_f64(p.qb), p.values()[0], []
+    for b, n in enumerate(nqs):
+        for h in range(Hk):
+            t = int(np.argmax(k[p.used(b)[:lens[b] - n + 1], h] @ q[p.starts[b], h * (Hq // Hk)]))
+            p.host[3][p.used(b)[t], h] = oracle.fp16_encode((2.0 ** (6 + np.arange(D // 32))).astype(np.float32))
+            bad.append((b, t, h, (b + h) % (D // 32)))
+    p.upload()
+    _check_nan_groups(p, bad, what="heaviest")

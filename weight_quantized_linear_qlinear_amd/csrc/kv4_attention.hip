@@ -4,9 +4,9 @@
 //   s_t = scale * sum_c k_scale[t,c] * (q_c . k_code[t,c])      (c: groups of 32 channels)
 //   e_t = 2^(s_t log2e - m),  l = sum_t e_t,  o_c = sum_t fp16(e_t v_scale[t,c]) v_code[t,c],  out = o / l
 // m is a running reference, 15 octaves below the largest s_t log2e + E_t seen, where 2^E_t bounds token
-// t's V scales: so every weight e_t v_scale fits fp16, has its 11 bits down to 2^-29 of the row's
-// largest, and is rounded once.  Codes are exact in fp16, q is scaled per row by a power of two into
-// [-1, 1) (as in kv_attention.hip); sums are fp32.
+// t's V scales (the finite ones: a NaN stays in its own group): so every weight e_t v_scale fits fp16,
+// has its 11 bits down to 2^-29 of the row's largest, and is rounded once.  Codes are exact in fp16, q is
+// scaled per row by a power of two into [-1, 1) (as in kv_attention.hip); sums are fp32.
 //
 // Layout.  S^T = K Q^T: the lane of token l % 16 and channel group l / 16 has, in the cache's order, its
 // eight channels of every group of 32 side by side: one load, and no byte moves before the conversion
@@ -280,9 +280,18 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttn
           sput[64 * n] = (uint16_t)d;                          // (group 2 n)
           if (2 * n + 1 < NG) sput[64 * n + 32] = (uint16_t)(d >> 16);
         }
-        // 2^E >= the largest: its exponent + 1 (a zero counts as the smallest scale)
+        if (__ballot(top >= 0x7C00u)) {                        // a NaN or an infinity: it bounds nothing
+          auto finite = [](uint32_t s) { return s < 0x7C00u ? s : 0u; };
+          top = 0;
+#pragma unroll
+          for (int n = 0; n < KScales<NG>::N; ++n) {
+            const uint32_t d = in ? sc.d[n] & 0x7FFF7FFFu : 0u;
+            top = max(top, max(finite(d & 0xFFFFu), finite(d >> 16)));
+          }
+        }
+        // 2^E >= the largest finite scale: its exponent + 1 (a zero counts as the smallest scale)
         const float f = fmaxf(f16_lo(top), 0x1p-24f);
-        if (lane >= 32) mine.ev[spos] = (float)__builtin_amdgcn_frexp_expf(f);       // (0 for a NaN or an infinity)
+        if (lane >= 32) mine.ev[spos] = (float)__builtin_amdgcn_frexp_expf(f);
       }
       wave_sync();
 
