@@ -585,3 +585,19 @@ def test_groups_beside_a_nan_scale_of_the_heaviest_token(case, heads):
             bad.append((b, t, h, (b + h) % (D // 32)))
     p.upload()
     _check_nan_groups(p, bad, what="heaviest")
+
+
+@pytest.mark.parametrize("heads", [(4, 2, 64), (2, 1, 96), (4, 2, 128), (2, 1, 256), (3, 1, 192), (2, 2, 32)])
+@pytest.mark.parametrize("case", [((5,), (40,)), ((4, 1, 9), (300, 1, 80)), ((24,), (5000,)), ((150,), (250,)), ((90, 300), (90, 421))])
+def test_a_nan_scale_of_v_stays_with_the_rows_that_see_its_token(case, heads):
+    (nqs, lens), (Hq, Hk, D) = case, heads
+    print(f"attention4 NaN scales nqs={nqs} heads={heads}", flush=True)
+    rng = np.random.default_rng(D + sum(lens))
+    for causal, window in ((True, 0), (True, 37), (False, 0)):
+        p = Problem(sum(nqs) + D + window, nqs, lens, Hq, Hk, D, 16, each=False)
+        bad = []
+        for b, (n, L) in enumerate(zip(nqs, lens)):
+            # the last token, one between the queries, one that the window hides from the later of them
+            for t in {L - 1, L - 1 - n // 2, max(0, L - n - max(window, 30) + 1 + n // 2)}:
+                bad.append((b, t, int(rng.integers(Hk)), int(rng.integers(D // 32))))
+        _check_nan_groups(p, bad, causal, window, what=f"causal={causal} window={window}")

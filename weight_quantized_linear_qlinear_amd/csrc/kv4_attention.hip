@@ -269,6 +269,7 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttn
         const int t = t0 + 16 * u + j;
         return (u ? e1 : e0) >= 0 && t < c1 && t >= tmin;
       };
+      bool bad;                                                // a scale of the tile is NaN or infinite
       {
         const int t = base + (lane & 31);
         const bool in = all_valid || ((lane & 16 ? e1 : e0) >= 0 && t < c1 && t >= tmin);
@@ -280,7 +281,8 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttn
           sput[64 * n] = (uint16_t)d;                          // (group 2 n)
           if (2 * n + 1 < NG) sput[64 * n + 32] = (uint16_t)(d >> 16);
         }
-        if (__ballot(top >= 0x7C00u)) {                        // a NaN or an infinity: it bounds nothing
+        bad = __ballot(top >= 0x7C00u) != 0;                   // a NaN or an infinity: it bounds nothing
+        if (bad) {
           auto finite = [](uint32_t s) { return s < 0x7C00u ? s : 0u; };
           top = 0;
 #pragma unroll
@@ -361,6 +363,28 @@ __global__ __launch_bounds__(waves_of(NG) * 64) void kv4_attention_kernel(KvAttn
           e[u][j] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][j], f, -ref));
           l += e[u][j];
         }
+
+      // V scales that are NaN or infinite go to the rows that see their tokens and to no others (0 NaN is NaN): as NaN
+      // into the sums of those rows' groups, and 0 takes their place.
+      if (__builtin_expect(bad, 0)) {
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          u32x4 v = ld16(&mine.s[1][n][8 * g4]);
+          int hit = 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if ((v[i / 2] >> (16 * (i & 1)) & 0xFFFFu) < 0x7C00u) continue;
+            v[i / 2] &= i & 1 ? 0x0000FFFFu : 0xFFFF0000u;
+            hit |= s[i / 4][i & 3] != kNegInf;
+          }
+          wave_sync();                                         // (the 16 lanes of a lane group write the same)
+          st16(&mine.s[1][n][8 * g4], v);
+          if (across16(hit, OrI()) != 0)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[n][0][j] = o[n][1][j] = __builtin_nanf("");
+        }
+        wave_sync();
+      }
 
       // O^T: per group, the weights times their V scales, and the channel pairs' two rows of V^T
 #pragma unroll

@@ -130,6 +130,9 @@ __device__ __forceinline__ int across16(int v, OP op) {       // over lanes l, l
 struct AddI {
   __device__ __forceinline__ int operator()(int a, int b) const { return a + b; }
 };
+struct OrI {
+  __device__ __forceinline__ int operator()(int a, int b) const { return a | b; }
+};
 struct AddF {
   __device__ __forceinline__ int operator()(int a, int b) const {
     return __builtin_bit_cast(int, __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b));

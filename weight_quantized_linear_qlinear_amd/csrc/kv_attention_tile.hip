@@ -133,8 +133,9 @@ struct TileLds {
     JoinLds join[kTileWaves];
   };
   // by tile % 4 (written two tiles ahead):
-  float vs[4][BITS == 4 ? NG : 1][S::T];         // V scales (4 bits: by group), 0 for a token that is not there
-  uint32_t top[4][kTileWaves];                   // per wave's tokens: largest K scale (fp16 bits; bit 15: one is not there) and V scale
+  float vs[4][BITS == 4 ? NG : 1][S::T];         // V scales (4 bits: by group, kBad for a NaN), 0 for a token that is not there
+  uint32_t top[4][kTileWaves];                   // per wave's tokens: largest K scale (fp16 bits; bit 15: see TileScale::gap) and V
+                                                 // scale (bit 31: one is kBad)
 };
 
 // Where piece p (8 tokens) of channel d lies in its row: p ^ swizzle(d), so that reads (16
@@ -150,9 +151,13 @@ __device__ __forceinline__ int swizzle(int d) {
 struct TileScale {
   int e;                         // V' = V 2^-e
   bool big;                      // K' = K 2^-7
-  bool gap;                      // a token is not there
+  bool gap;                      // a token is not there, or (4 bits) a V scale is kBad
 };
 constexpr int kNoScale = -1000;
+
+// In the place of a V scale that is NaN or infinite (4 bits): 0 NaN is NaN, so that it would reach the rows that
+// do not see its token.  Those that do get their NaN by a comparison.
+constexpr float kBad = -0x1p-24f;
 
 // V's codes go to fp16 as 2^-8 of themselves (exact: 2^-17 is the smallest) and their scales as 2^(8 - E), so
 // that a scale keeps its 11 bits down to 2^-27 of the largest.  (2^-19 with both as they are: beside a
@@ -424,14 +429,16 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
     auto stat_write = [&](int n) {
       // (tokens before every row's window are left out like those of a bad page: their entries may hold anything)
       const bool there = entry_of(st_page, st_t) >= 0 && st_t + srow >= sp.first && st_t + srow < c1;
-      const uint32_t kb = there ? skr & 0x7FFF : 0u, vb = there ? max(svr & 0x7FFF, 1u) : 0u;
+      const bool bad = BITS == 4 && there && (svr & 0x7FFF) >= 0x7C00;
+      const uint32_t kb = there ? skr & 0x7FFF : 0u, vb = there ? bad ? 1u : max(svr & 0x7FFF, 1u) : 0u;
       uint32_t top = across16(row16(kb | vb << 16, MaxU16()), MaxU16());
       if (__ballot(!there)) top |= 0x8000u;
-      if (lane < (BITS == 4 ? NG : 1) * TPW) sm.vs[n & 3][BITS == 4 ? lane / TPW : 0][first_t + srow] = f16_lo(vb);
+      if (BITS == 4 && __ballot(bad)) top |= 0x80008000u;
+      if (lane < (BITS == 4 ? NG : 1) * TPW) sm.vs[n & 3][BITS == 4 ? lane / TPW : 0][first_t + srow] = bad ? kBad : f16_lo(vb);
       if (lane == 0) sm.top[n & 3][wave] = top;
     };
 
-    auto there = [](float vs) { return BITS == 4 ? vs != 0.0f : vs > 0.0f; };   // (a NaN: there)
+    auto there = [](float vs) { return BITS == 4 ? vs != 0.0f : vs > 0.0f; };   // (kBad: there)
     const int vswz = half ^ swizzle<T>(c32);                 // this lane's pieces: (4 k + 2 t) ^ vswz
     f32x16 o[NG];
     float m = kNegInf, l = 0.0f;
@@ -509,6 +516,25 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
             for (int k = 0; k < NB; ++k)
 #pragma unroll
               for (int i = 0; i < 16; ++i) s[k][i] = 32 * k + 8 * (i / 4) + (i & 3) > lo ? s[k][i] : kNegInf;
+          }
+          if (BITS == 4 && now.gap && __builtin_expect(__ballot((sm.top[n & 3][lane & (kTileWaves - 1)] & 0x80000000u) != 0) != 0, 0)) {
+            uint32_t seen = 0, hit = 0;                      // the row's tokens by bit; the groups in which it sees a kBad
+#pragma unroll
+            for (int k = 0; k < NB; ++k)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) seen |= (s[k][i] != kNegInf ? 1u : 0u) << (16 * k + i);
+#pragma unroll 1
+            for (int q = 0; q < 4 * NB * NG; ++q) {          // (four tokens at a time: few registers)
+              const f32x4 vs = *reinterpret_cast<const f32x4*>(&sm.vs[n & 3][q / (4 * NB)][8 * (q % (4 * NB)) + 4 * half]);
+              const uint32_t bad = (vs.x < 0.0f ? 1u : 0u) | (vs.y < 0.0f ? 2u : 0u) | (vs.z < 0.0f ? 4u : 0u) | (vs.w < 0.0f ? 8u : 0u);
+              hit |= (bad & seen >> (4 * (q % (4 * NB))) ? 1u : 0u) << (q / (4 * NB));
+            }
+            const auto both = __builtin_amdgcn_permlane32_swap(hit, hit, false, false);
+            hit = both[0] | both[1];
+#pragma unroll
+            for (int d = 0; d < NG; ++d)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[d][i] = hit >> d & 1 ? __builtin_nanf("") : o[d][i];
           }
         }
         float mx = kNegInf;
