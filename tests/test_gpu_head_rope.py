@@ -440,3 +440,67 @@ def test_binding_refusals_on_the_gpu():
                  lambda: qlq.norm_rope(q, k, w, w, pos, f, attention_factor=float("nan"), axes=ax)):
         with pytest.raises(qlq.QlqError):
             call()
+
+
+def _odd_values(rng, T, H, D, R):
+    """Rows whose channels from R on hold infinities, NaNs and negative zeros beside ordinary values."""
+    b = oracle.f32_to_bf16_bits(rng.standard_normal((T, H, D)).astype(np.float32))
+    odd = np.array([0x7F80, 0xFF80, 0x7FC0, 0xFFC1, 0x8000, 0x0000, 0x7F81, 0x0001], np.uint16)
+    at = rng.random((T, H, D)) < 0.3
+    at[..., :R] = False
+    b[at] = rng.choice(odd, size=int(at.sum()))
+    return b
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("sizes", [(96, 32), (128, 64), (64, 10), (72, 20), (512, 34), (192, 96), (80, 2)])
+def test_channels_that_do_not_rotate_are_copied(sizes, inter):
+    D, R = sizes
+    rng = np.random.default_rng(D + R)
+    print(f"unrotated D={D} R={R} inter={inter}", flush=True)
+    for T, H in ((5, 3), (900, 2)):
+        b = _odd_values(rng, T, H, D, R)
+        x, zero = bf16_to_gpu(b), torch.zeros(R // 2, dtype=torch.int32, device=dev())
+        (f, pos, _), spin = _spin(rng, T, R, 1)
+        got = [qlq.rope(x, pos[None].contiguous(), f, 0.75, inter, axes=zero), *qlq.norm_rope(x, x, None, None, pos, f, EPS, 0.75, inter)]
+        in_place = x.clone()
+        got.append(qlq.rope(in_place, pos[None].contiguous(), f, 0.75, inter, axes=zero, out=in_place))
+        for g in got:
+            assert np.array_equal(bf16_bits(g)[..., R:], b[..., R:]), "channels from R on"
+            _check_rows(g[..., :R].contiguous(), *_turned(bits_to_f64(b[..., :R]), None, spin, inter, 0.75))
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_infinities_that_do_not_rotate_on_their_way_into_the_cache(inter):
+    # the entries of the plain append (8 bits), and the oracle's (4), in the groups of channels that do not rotate
+    T, H, D, R = 40, 2, 128, 32
+    rng = np.random.default_rng(3)
+    b = oracle.f32_to_bf16_bits(rng.standard_normal((T, H, D)).astype(np.float32))
+    at = rng.random((T, H, D - R)) < 0.05
+    b[..., R:][at] = rng.choice(np.array([0x7F80, 0xFF80], np.uint16), size=int(at.sum()))
+    x, s = bf16_to_gpu(b), torch.arange(T, device=dev())
+    (f, pos, _), spin = _spin(rng, T, R, 1)
+    plain, axes, four = qlq.kv_cache(T, H, D), qlq.kv_cache(T, H, D), qlq.kv_cache(T, H, D, bits=4)
+    qlq.rope_kv_append(x, x, x, pos, f, plain, s, interleaved=inter)
+    for c in (axes, four):
+        q = qlq.rope_kv_append(x, x, x, pos[None].contiguous(), f, c, s, interleaved=inter, axes=torch.zeros(R // 2, dtype=torch.int32, device=dev()))
+        assert np.array_equal(bf16_bits(q)[..., R:], b[..., R:])
+    assert torch.equal(plain.k_codes[..., R:], axes.k_codes[..., R:])
+    assert torch.equal(plain.k_scales[..., R // 32:], axes.k_scales[..., R // 32:])
+    want, _ = _turned(bits_to_f64(b), None, spin, inter)
+    _check_entries4(four, np.arange(T), want, bits_to_f64(b))
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_a_norm_with_an_infinity_that_does_not_rotate(inter):
+    # x / infinity: NaN where the infinity stands, zeros beside it
+    rng = np.random.default_rng(4)
+    x, _ = _rows(rng, 6, 2, 96)
+    x[2, 1, 71] = float("inf")
+    w, _ = _weight(rng, 96)
+    (f, pos, _), _ = _spin(rng, 6, 32, 1)
+    for g in qlq.norm_rope(x, x, w, w, pos, f, interleaved=inter):
+        want = torch.zeros(96, dtype=torch.bool, device=dev())
+        want[71] = True
+        assert torch.equal(torch.isnan(g[2, 1]), want) and not g[2, 1][~want].any()
+        assert bool(torch.isfinite(g[2, 0].float()).all()) and bool(torch.isfinite(g[3].float()).all())

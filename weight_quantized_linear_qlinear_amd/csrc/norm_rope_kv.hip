@@ -4,7 +4,8 @@
 // For a head row x of D channels at token t (weight w: optional, per channel, q's and k's own):
 //   y_c = x_c w_c / sqrt(mean_c x_c^2 + eps)
 //   theta_i = positions[axes[i]][t] inv_freq[i],  i < R/2;  (a, b) -> factor (a cos - b sin, a sin + b cos)
-//   for the pair (i, i + R/2), or (2 i, 2 i + 1) interleaved; channels from R on stay.
+//   for the pair (i, i + R/2), or (2 i, 2 i + 1) interleaved; channels from R on stay: without a weight as
+//   they came, bit for bit, with one multiplied by it and the row's factor alone.
 // The rotation is linear, so x w is rotated and the row's factor comes last; one rounding at the end.
 // Angles, their reduction and the cosines are in 64 bits; q, and a K that goes to bf16 or to 8-bit
 // codes, are computed in fp32 from there.  A K that goes to 4-bit codes is computed in fp64 altogether: next
@@ -201,6 +202,15 @@ struct Lane {
     return raw;
   }
 
+  // Of channels 2 i and 2 i + 1 of this lane (i < 4), those that rotate: the others have no partner (their turn is
+  // (1, 0), and 0 times an infinity is NaN).
+  __device__ __forceinline__ bool turns(const NormRopeArgs& a, int i) const { return c * 8 + 2 * i < a.R; }
+  __device__ __forceinline__ void drop_unturned(const NormRopeArgs& a, u32x4* part) const {
+    if (a.R == D) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) (*part)[i] = turns(a, i) ? (*part)[i] : 0u;
+  }
+
   // The channel that channel ch turns with.
   __device__ __forceinline__ int partner(const NormRopeArgs& a, int ch) const {
     return ch >= a.R ? ch : a.interleaved ? ch ^ 1 : ch < half ? ch + half : ch - half;
@@ -218,6 +228,7 @@ struct Lane {
 #pragma unroll
       for (int i = 0; i < 4; ++i) (*part)[i] = w[partner(a, c * 8 + 2 * i)] | (uint32_t)w[partner(a, c * 8 + 2 * i + 1)] << 16;
     }
+    drop_unturned(a, part);
   }
 
   // What channel e of the lane at place c and its partner are multiplied by, weights (if any) included.
@@ -235,6 +246,7 @@ struct Lane {
     if (a.interleaved) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] = raw[i] >> 16 | raw[i] << 16;
+      drop_unturned(a, &o);
       return o;
     }
     if (there) st16(mine + c * 8, raw);
@@ -246,6 +258,7 @@ struct Lane {
       for (int i = 0; i < 4; ++i) o[i] = mine[partner(a, c * 8 + 2 * i)] | (uint32_t)mine[partner(a, c * 8 + 2 * i + 1)] << 16;
     }
     __builtin_amdgcn_wave_barrier();                          // reads above before the next rows' writes
+    drop_unturned(a, &o);
     return o;
   }
 
@@ -335,8 +348,13 @@ struct Lane {
     return sb;
   }
 
-  __device__ __forceinline__ void store_bf16(uint16_t* out, const float* f, int vec) const {
-    const u32x4 p = {pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+  // A row in bf16; without a norm, channels that do not rotate are those of raw.
+  __device__ __forceinline__ void store_bf16(const NormRopeArgs& a, uint16_t* out, const float* f, u32x4 raw, bool normed, int vec) const {
+    u32x4 p = {pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7])};
+    if (!normed && a.R < D) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = turns(a, i) ? p[i] : raw[i];
+    }
     if (vec) {
       st16(out, p);
     } else {
@@ -478,7 +496,7 @@ __global__ __launch_bounds__(kWaves * 64, (kRoom<KOUT, TPR>)) void norm_rope_ker
     } else {
       l.norm_turn(a, raw, there, a.wk != nullptr, v, f);
       if constexpr (KOUT == 8) l.store8_k(f, there && stored, a.k_codes, a.k_scales, at);
-      else if (there) l.store_bf16(a.k_out + (int64_t)t * a.k_out_stride + head * D + l.c * 8, f, a.vec_out);
+      else if (there) l.store_bf16(a, a.k_out + (int64_t)t * a.k_out_stride + head * D + l.c * 8, f, raw, a.wk != nullptr, a.vec_out);
     }
   }
   if (q0 >= q1) return;
@@ -492,7 +510,7 @@ __global__ __launch_bounds__(kWaves * 64, (kRoom<KOUT, TPR>)) void norm_rope_ker
     const bool there = l.live && head < a.Hq;
     unpack8(raw, f);
     l.norm_turn(a, raw, there, a.wq != nullptr, v, f);
-    if (there) l.store_bf16(a.q_out + (int64_t)t * a.q_out_stride + head * D + l.c * 8, f, a.vec_out);
+    if (there) l.store_bf16(a, a.q_out + (int64_t)t * a.q_out_stride + head * D + l.c * 8, f, raw, a.wq != nullptr, a.vec_out);
   }
 }
 
