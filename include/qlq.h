@@ -438,7 +438,9 @@ qlq_status qlq_kv4_gather(const void* k_codes, const void* k_scales, const void*
  * scale buffers 16-byte aligned.  k_t = k_code k_scale and v_t = v_code v_scale are not rounded with few rows;
  * weights times V scales are rounded to fp16: 2^-11, 2^-40 of the row's largest below 2^-29 of it.  With many
  * rows (on average more than 64 per KV head and sequence, 96 for D 32 and 64, 256 for D 256) K, V and the
- * weights are rounded to 11 bits each. */
+ * weights are rounded to 11 bits each (K down to scales 2^-26 of the largest among 64 tokens, V of the largest so
+ * far, weights down to 2^-21 of a row's largest).  A V group with a NaN scale gives NaN in its channels of the rows
+ * that see its token, and in no others. */
 qlq_status qlq_kv4_attention(const void* q_bf16, int64_t q_stride, int64_t T, int64_t B, int64_t Hq, int64_t Hk,
                              int64_t D, const void* k_codes, const void* k_scales, const void* v_codes,
                              const void* v_scales, int64_t pool, const int32_t* block_table, int64_t max_pages,

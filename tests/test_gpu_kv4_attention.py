@@ -601,3 +601,45 @@ def test_a_nan_scale_of_v_stays_with_the_rows_that_see_its_token(case, heads):
             for t in {L - 1, L - 1 - n // 2, max(0, L - n - max(window, 30) + 1 + n // 2)}:
                 bad.append((b, t, int(rng.integers(Hk)), int(rng.integers(D // 32))))
         _check_nan_groups(p, bad, causal, window, what=f"causal={causal} window={window}")
+
+
+@pytest.mark.parametrize("heads", [(4, 2, 64), (2, 1, 96), (4, 1, 128), (2, 1, 256), (3, 1, 192), (3, 1, 32)])
+def test_small_keys_and_large_queries(heads):
+    # K scales down to fp16's smallest, whose products with the codes leave fp16's normal range
+    Hq, Hk, D = heads
+    print(f"attention4 small keys heads={heads}", flush=True)
+    for nqs, lens in (((150,), (250,)), ((3,), (250,))):
+        for octaves in (14, 20, 23):
+            p = Problem(D + octaves, nqs, lens, Hq, Hk, D, 16, each=False, qgain=2.0 ** octaves)
+            s, rng = p.used(0), np.random.default_rng(octaves)
+            p.host[0][s], p.host[1][s] = kvcache.kv4_quantize_values(2.0 ** -octaves * rng.standard_normal((s.size, Hk, D)))
+            p.upload()
+            p.check(what=f"2^-{octaves}")
+
+
+@pytest.mark.parametrize("heads", [(4, 2, 64), (4, 1, 128), (2, 1, 256), (2, 1, 96), (3, 1, 192)])
+def test_keys_beside_one_a_million_times_as_large(heads):
+    # Keys of 2^-11 in one tile with a key of 60000 that the last query alone sees.  All of them are code 0.5 of one scale
+    # whose bits below the 6th do not fall away by chance, and queries are positive: errors of K add up in every score.
+    # The others' scores alone set the bound (A and E of the module's docstring, K's 11 bits among it).
+    Hq, Hk, D = heads
+    n, L, G = 150, 250, Hq // Hk
+    p = Problem(D, (n,), (L,), Hq, Hk, D, 16, each=False, octaves=0)
+    s, rng = p.used(0), np.random.default_rng(D)
+    p.host[0][s], p.host[1][s] = 0x11, oracle.fp16_encode(np.float32(2.0 ** -10 * (1 + 7 / 1024)))
+    p.host[1][s[-1]] = oracle.fp16_encode(np.float32(60000.0))
+    p.upload()
+    p.qb = oracle.f32_to_bf16_bits((2.0 ** 9 * rng.uniform(1, 2, size=(p.T, Hq, D))).astype(np.float32))
+    p.q = bf16_to_gpu(p.qb)
+    q, (kv, vv) = bits_to_f64(p.qb), p.values()
+    lse = torch.zeros(p.T, Hq, device=dev())
+    out = bits_to_f64(bf16_bits(p.run(lse=lse)))[:-1]
+    o64, l64, _, S = layer.kv_attention(q, kv, vv, p.table, p.lens, p.page, p.starts)
+    ks = np.abs(kv[s[:-1]])
+    A = D ** -0.5 * max((np.abs(q[:-1, h]) @ ks[:, h // G].T).max() for h in range(Hq))
+    A1 = D ** -0.5 * np.abs(q).max() * ks.sum(-1).max()
+    E = U * (42 * A + A1 + 3 * (2 * A + 56) + L / 32 + 40) + 2.0 ** -11 * A
+    d = np.abs(lse.cpu().numpy().astype(np.float64) - l64)[:-1] - (2 * E + U * np.abs(l64[:-1]))
+    assert d.max() <= 0, f"lse {d.max():.3e} beyond the bound"
+    over = np.abs(out - o64[:-1]) - (2.0 ** -8 * np.abs(o64[:-1]) + S[:-1] * (2.0 ** -10 + 2 * E) + L * 2.0 ** -31 * np.abs(vv[s]).max())
+    assert np.max(over) <= 0, f"{np.max(over):.3e} beyond the bound"

@@ -23,8 +23,9 @@
 // 730 TFLOP/s); a prompt of 512 tokens on its own 49 us, half of it storing and joining partial sums.
 //
 // Over 4 bits (rows in the order of kv_rows.h) K and V come with an fp16 scale per 32 channels each; K' and V' are
-// the same, V's scales by group, their common 2^-E over all of a token's groups.  A tile's conversion is shared by
-// 256 rows, so the cache's width hardly shows: the two chunks above 320 us.
+// the same, V's scales by group, their common 2^-E over all of a token's groups, and K' of a tile takes the power of
+// two that its largest scale leaves room for.  A tile's conversion is shared by 256 rows, so the cache's width
+// hardly shows: the two chunks above 320 us.
 #include <type_traits>
 
 #include "kv_attention.h"
@@ -150,7 +151,7 @@ __device__ __forceinline__ int swizzle(int d) {
 // What a tile's values are scaled by, uniform for the workgroup.
 struct TileScale {
   int e;                         // V' = V 2^-e
-  bool big;                      // K' = K 2^-7
+  int k;                         // K' = K 2^-k (8 bits: 0 or 7)
   bool gap;                      // a token is not there, or (4 bits) a V scale is kBad
 };
 constexpr int kNoScale = -1000;
@@ -164,10 +165,14 @@ constexpr float kBad = -0x1p-24f;
 // scale 2^24 times as large, which earlier rows of its query tile do not even see, 5 bits were left.)
 constexpr int kCodeShift = 8;
 constexpr float kCode = 0x1p-8f;
-// 4 bits: codes reach 6, so the largest scale goes to 2^12 .. 2^13, V' stays below 49152 and has its 11
-// bits down to 2^-26 of the largest; K' overflows for scales above 10917: 2^-7 from 8192 on.
+// 4 bits: codes reach 6, so the largest scale goes to 2^12 .. 2^13, K' and V' stay below 49152 and have their 11
+// bits down to scales 2^-26 of the largest.  K's codes take its factor, 2^13 at most: from there on the smallest
+// scale of all has them.  (Without one, code 0.5 of a scale of 2^-20 lost 5 % and a scale of 2^-24 its odd halves.)
 constexpr int kTop4 = 13;
-constexpr uint32_t kBig4 = 0x7000;
+
+__device__ __forceinline__ int exponent_over(uint32_t f16) {   // the smallest e with 2^e above a positive fp16 (its bits)
+  return f16 >= 0x400 ? (int)(f16 >> 10) - 14 : 8 - __builtin_clz(f16);
+}
 
 // N products that take one operand from LDS each, in exactly this order: AHEAD reads in front,
 // then a product and the read of a later one in turn (left alone, the compiler reads each operand
@@ -315,7 +320,7 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
     typename std::conditional<BITS == 4, u32x2, u32x4>::type kraw;
     typename std::conditional<BITS == 4, KScales<NG>, uint32_t>::type ksraw;
     uint32_t vraw[4];
-    TileScale next{kNoScale, false, false};
+    TileScale next{kNoScale, 0, false};
     auto load = [&](int entry) {
       const int64_t at64 = (int64_t)max(entry, 0) * hk + h;
       if constexpr (BITS == 4) {
@@ -339,9 +344,9 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
       next.gap = __ballot((top & 0x8000u) != 0) != 0;
       top = row8(top & 0x7FFF7FFFu, MaxU16());
       top = __builtin_amdgcn_readfirstlane(top);
-      next.big = (top & 0xFFFF) > (BITS == 4 ? kBig4 : 0x6000);
-      const uint32_t vt = top >> 16;
-      if (vt) next.e = max(next.e, (vt >= 0x400 ? (int)(vt >> 10) - 14 : 8 - __builtin_clz(vt)) - (BITS == 4 ? kTop4 : 6));
+      const uint32_t kt = top & 0xFFFF, vt = top >> 16;
+      next.k = BITS == 4 ? max(exponent_over(max(kt, 1u)), 0) - kTop4 : kt > 0x6000 ? 7 : 0;
+      if (vt) next.e = max(next.e, exponent_over(vt) - (BITS == 4 ? kTop4 : 6));
       // tokens 4 g .. 4 g + 3 of the tile: piece 4 (g / 8) + 2 (g / 4 % 2) + g % 2, half g / 2 % 2 of it
       const int g = first_t / 4 + vgrp;
       const int p = 4 * (g >> 3) + 2 * ((g >> 2) & 1) + (g & 1), hf = (g >> 1) & 1;
@@ -349,7 +354,7 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
         const f32x4 va = *reinterpret_cast<const f32x4*>(&sm.vs[n & 3][vg][first_t + 4 * vgrp]);
         const f32x4 vb = *reinterpret_cast<const f32x4*>(&sm.vs[n & 3][vg2][first_t + 4 * vgrp]);
         if (lane < NL) {
-          const float kone = next.big ? 0x1p-7f : 1.0f;      // (the codes take the 2^-7, as below)
+          const float kone = __builtin_ldexpf(1.0f, -next.k);
           const bool ksecond = P2 > 0 && kchunk >= 2 * P1;
           u32x4 w[2];
 #pragma unroll
@@ -378,8 +383,8 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
         }
       } else {
       const f16x2 s2 = __builtin_bit_cast(f16x2, (ksraw & 0xFFFF) | ksraw << 16);
-      const uint32_t upper = next.big ? 0x48484848u : 0x64646464u;        // (the codes take the 2^-7: a small scale
-      const float zero = next.big ? 9.0f : 1152.0f;                       // beside a big one keeps its bits)
+      const uint32_t upper = next.k ? 0x48484848u : 0x64646464u;          // (the codes take the 2^-7: a small scale
+      const float zero = next.k ? 9.0f : 1152.0f;                         // beside a big one keeps its bits)
       f32x4 vsc = *reinterpret_cast<const f32x4*>(&sm.vs[n & 3][0][first_t + 4 * vgrp]);
       if (lane < NL) {
         const uint32_t kd[4] = {kraw.x, kraw.y, kraw.z, kraw.w};
@@ -429,12 +434,18 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
     auto stat_write = [&](int n) {
       // (tokens before every row's window are left out like those of a bad page: their entries may hold anything)
       const bool there = entry_of(st_page, st_t) >= 0 && st_t + srow >= sp.first && st_t + srow < c1;
-      const bool bad = BITS == 4 && there && (svr & 0x7FFF) >= 0x7C00;
-      const uint32_t kb = there ? skr & 0x7FFF : 0u, vb = there ? bad ? 1u : max(svr & 0x7FFF, 1u) : 0u;
+      const uint32_t kb = there ? skr & 0x7FFF : 0u, vb = there ? max(svr & 0x7FFF, 1u) : 0u;
       uint32_t top = across16(row16(kb | vb << 16, MaxU16()), MaxU16());
+      float vs = f16_lo(vb);
       if (__ballot(!there)) top |= 0x8000u;
-      if (BITS == 4 && __ballot(bad)) top |= 0x80008000u;
-      if (lane < (BITS == 4 ? NG : 1) * TPW) sm.vs[n & 3][BITS == 4 ? lane / TPW : 0][first_t + srow] = bad ? kBad : f16_lo(vb);
+      if (BITS == 4 && __builtin_expect(__ballot(top >= 0x7C000000u || (top & 0x7C00u) == 0x7C00u) != 0, 0)) {
+        // (a NaN or an infinity bounds nothing)
+        const bool bad = vb >= 0x7C00;
+        top = across16(row16((kb < 0x7C00 ? kb : 0u) | (bad ? 1u : vb) << 16, MaxU16()), MaxU16()) | 0x8000u;
+        if (__ballot(bad)) top |= 0x80000000u;
+        vs = bad ? kBad : vs;
+      }
+      if (lane < (BITS == 4 ? NG : 1) * TPW) sm.vs[n & 3][BITS == 4 ? lane / TPW : 0][first_t + srow] = vs;
       if (lane == 0) sm.top[n & 3][wave] = top;
     };
 
@@ -492,7 +503,7 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
       if (!skip) {
         const bool open = !now.gap && (!a.causal || base + T - 1 <= first_p) &&
                           (a.window <= 0 || base > last_p - a.window);
-        const float cst = now.big ? cs * 0x1p7f : cs;
+        const float cst = BITS == 4 ? __builtin_ldexpf(cs, now.k) : now.k ? cs * 0x1p7f : cs;
         const int t4 = base + 4 * half;
         if (!open) {
           if (now.gap) {
