@@ -85,7 +85,8 @@ __device__ __forceinline__ float largest_across16(float v) {  // over lanes l, l
 
 // fp16(v_i e_i) of eight, the products in fp32: one instruction each (the compiler's own choice takes three for
 // two).  The wait states: the result of an exponential, which may be among e, and of a write of a high half are
-// not there for the next instruction.
+// not there for the next instruction, and no vector instruction's for a matrix product within the next two (the
+// compiler, which knows this rule, does not look into the block).
 __device__ __forceinline__ f16x8 weigh(f16x8 v, const float (&e)[2][4]) {
   const u32x4 d = __builtin_bit_cast(u32x4, v);
   u32x4 w;
@@ -99,7 +100,7 @@ __device__ __forceinline__ f16x8 weigh(f16x8 v, const float (&e)[2][4]) {
       "v_fma_mixhi_f16 %1, %5, %11, 0 op_sel:[1,0,0] op_sel_hi:[1,0,0]\n\t"
       "v_fma_mixhi_f16 %2, %6, %13, 0 op_sel:[1,0,0] op_sel_hi:[1,0,0]\n\t"
       "v_fma_mixhi_f16 %3, %7, %15, 0 op_sel:[1,0,0] op_sel_hi:[1,0,0]\n\t"
-      "s_nop 0"
+      "s_nop 1"
       : "=&v"(w0), "=&v"(w1), "=&v"(w2), "=&v"(w3)
       : "v"(d.x), "v"(d.y), "v"(d.z), "v"(d.w), "v"(e[0][0]), "v"(e[0][1]), "v"(e[0][2]), "v"(e[0][3]), "v"(e[1][0]),
         "v"(e[1][1]), "v"(e[1][2]), "v"(e[1][3]));
