@@ -504,3 +504,21 @@ def test_a_norm_with_an_infinity_that_does_not_rotate(inter):
         want[71] = True
         assert torch.equal(torch.isnan(g[2, 1]), want) and not g[2, 1][~want].any()
         assert bool(torch.isfinite(g[2, 0].float()).all()) and bool(torch.isfinite(g[3].float()).all())
+
+
+@pytest.mark.parametrize("gains", [(2.0 ** 59, 2.0 ** 70, 1e-6), (2.0 ** -75, 2.0 ** -72, 2.0 ** -60), (2.0 ** -80, 2.0 ** -66, 2.0 ** -140),
+                                   (2.0 ** 62, 2.0 ** 100, 1.0), (2.0 ** 120, 2.0 ** -90, 1e-6)])
+def test_norms_whose_products_leave_fp32_beside_squares_that_do_not(gains):
+    gain, wgain, eps = gains
+    rng = np.random.default_rng(78)
+    print(f"norm_rope range gain={gain:.0e} weight={wgain:.0e} eps={eps:.0e}", flush=True)
+    for H, D in ((6, 128), (3, 72)):
+        (x, x64), (f, spin) = _rows(rng, 9, H, D, gain), _spin(rng, 9, D, 1)
+        wb = oracle.f32_to_bf16_bits((wgain * (1 + 0.3 * rng.standard_normal(D))).astype(np.float32))
+        w, w64 = bf16_to_gpu(wb), bits_to_f64(wb)
+        for inter in (False, True):
+            want, top = _turned(x64, w64, spin, inter, eps=float(np.float32(eps)))
+            for g in qlq.norm_rope(x, x, w, w, f[1], f[0], eps=eps, interleaved=inter):
+                # (results below 2^-126: bf16's steps there are 2^-133, half of one is the rounding)
+                over = np.abs(bits_to_f64(bf16_bits(g)) - want) - 2.0 ** -8 * np.abs(want) - 24 * U * top - 2.0 ** -134
+                assert np.max(over) <= 0, f"D={D} inter={inter}: {np.max(over):.3e} beyond the bound"

@@ -6,7 +6,8 @@
 //   theta_i = positions[axes[i]][t] inv_freq[i],  i < R/2;  (a, b) -> factor (a cos - b sin, a sin + b cos)
 //   for the pair (i, i + R/2), or (2 i, 2 i + 1) interleaved; channels from R on stay: without a weight as
 //   they came, bit for bit, with one multiplied by it and the row's factor alone.
-// The rotation is linear, so x w is rotated and the row's factor comes last; one rounding at the end.
+// Products with w and the rotation are one factor per channel and partner, and the row's factor goes to x (x w can leave
+// fp32 where y does not); one rounding at the end.
 // Angles, their reduction and the cosines are in 64 bits; q, and a K that goes to bf16 or to 8-bit
 // codes, are computed in fp32 from there.  A K that goes to 4-bit codes is computed in fp64 altogether: next
 // to a border a code's neighbour is up to half of its value away, so that an order of fp32 additions
@@ -285,16 +286,17 @@ struct Lane {
       }
     }
     unpack8(partners(a, raw, there), o);
-    if (__ballot(big)) {                                      // x 2^-64: its products with weights stay in fp32
+    if (__ballot(big)) {                                      // (rho is 2^64 of itself there)
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if (big) f[e] *= 0x1p-64f, o[e] *= 0x1p-64f;
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float y = __builtin_fmaf(o[e], v[e].s, f[e] * v[e].c);
-      f[e] = normed ? y * rho : y;
+    if (normed) {                                             // x rho is at most sqrt(D): its products with weights leave
+#pragma unroll                                                // fp32 only where the result does
+      for (int e = 0; e < 8; ++e) f[e] *= rho, o[e] *= rho;
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = __builtin_fmaf(o[e], v[e].s, f[e] * v[e].c);
   }
 
   // The same in fp64, to 4-bit codes (byte j: channels 2 j and 2 j + 1) and the group's scale.
