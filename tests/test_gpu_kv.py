@@ -1,5 +1,7 @@
 """GPU KV-cache codec against the oracle: codes, fp16 scale bits and decoded bf16
 values are all compared bit for bit."""
+import types
+
 import numpy as np
 import pytest
 import torch
@@ -102,3 +104,19 @@ def test_kv_quantize_every_bf16_below_absmax(part):
     assert np.array_equal(_u16(q.v_scales), vs)
     assert np.array_equal(q.k_codes.cpu().numpy(), kq)
     assert np.array_equal(q.v_codes.cpu().numpy(), vq)
+
+
+def test_entries_are_any_object_with_the_four_buffers():
+    kb, vb = _inputs(5, 6, 2, 64)
+    k, v = bf16_to_gpu(kb), bf16_to_gpu(vb)
+    want = qlq.kv_quantize(k, v)
+    held = types.SimpleNamespace(**{n: torch.zeros_like(getattr(want, n)) for n in ("k_codes", "k_scales", "v_codes", "v_scales")})
+    assert qlq.kv_quantize(k, v, out=held) is held
+    for n in ("k_codes", "k_scales", "v_codes", "v_scales"):
+        assert torch.equal(getattr(held, n), getattr(want, n))
+    for a, b in zip(qlq.kv_dequantize(held), qlq.kv_dequantize(want)):
+        assert torch.equal(a, b)
+    four = qlq.kv_cache(6, 2, 128, bits=4)               # as many bytes of codes
+    for call in (lambda: qlq.kv_quantize(k, v, out=four), lambda: qlq.kv_dequantize(four)):
+        with pytest.raises(ValueError):
+            call()

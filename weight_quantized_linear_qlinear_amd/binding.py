@@ -473,7 +473,7 @@ class QuantizedKV4:
 
 
 def _eight_bits(c):
-    if not isinstance(c, QuantizedKV):
+    if isinstance(c, QuantizedKV4):
         raise ValueError("this call takes 8-bit entries (QuantizedKV)")
 
 
