@@ -522,3 +522,32 @@ def test_norms_whose_products_leave_fp32_beside_squares_that_do_not(gains):
                 # (results below 2^-126: bf16's steps there are 2^-133, half of one is the rounding)
                 over = np.abs(bits_to_f64(bf16_bits(g)) - want) - 2.0 ** -8 * np.abs(want) - 24 * U * top - 2.0 ** -134
                 assert np.max(over) <= 0, f"D={D} inter={inter}: {np.max(over):.3e} beyond the bound"
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("heads", [(2, 1, 256, 256), (3, 2, 512, 512), (1, 1, 512, 34), (2, 3, 480, 96)])
+def test_wide_heads_of_many_tokens(heads, inter):
+    # a wave per token, its largest rows: alone, into 4 bits and into 8
+    Hq, Hk, D, R = heads
+    rng = np.random.default_rng(D + R + 7)
+    for T, n in ((801, 1), (1030, 2)):
+        print(f"wide heads={heads} inter={inter} T={T}", flush=True)
+        (q, q64), (k, k64), (v, v64) = _rows(rng, T, Hq, D), _rows(rng, T, Hk, D, 2.0), _rows(rng, T, Hk, D, 0.3)
+        (wq, wq64), (wk, wk64) = _weight(rng, D), _weight(rng, D)
+        (f, pos, ax), spin = _spin(rng, T, R, n)
+        want, wantk = _turned(q64, wq64, spin, inter, 0.75), _turned(k64, wk64, spin, inter, 0.75)
+        gq, gk = qlq.norm_rope(q, k, wq, wk, pos, f, EPS, 0.75, inter, ax)
+        _check_rows(gq, *want)
+        _check_rows(gk, *wantk)
+        s = torch.from_numpy(rng.permutation(T)).to(dev())
+        c4, c8, w8 = qlq.kv_cache(T, Hk, D, bits=4), qlq.kv_cache(T, Hk, D), qlq.kv_cache(T, Hk, D)
+        for c in (c4, c8):
+            assert torch.equal(qlq.norm_rope_kv_append(q, k, v, wq, wk, pos, f, c, s, EPS, 0.75, inter, ax), gq)
+        _check_entries4(c4, s.cpu().numpy(), wantk[0], v64, f"T={T}")
+        # 8 bits: V as the plain append has it, K within half a step and what the scale's rounding takes
+        qlq.kv_append(k, v, w8, s)
+        assert torch.equal(c8.v_codes, w8.v_codes) and torch.equal(c8.v_scales, w8.v_scales)
+        at = s.cpu().numpy()
+        step = np.repeat(oracle.fp16_decode(_values(c8.k_scales)[at]), 32, -1)
+        kv = codes(c8.k_codes).view(np.int8)[at] * step
+        assert np.max(np.abs(kv - wantk[0]) - step * (0.5 + 127 * 2.0 ** -11 + 2.0 ** -6) - 24 * U * wantk[1]) <= 0
