@@ -1,5 +1,6 @@
 """GPU KV-cache codec against the oracle: codes, fp16 scale bits and decoded bf16
 values are all compared bit for bit."""
+import dataclasses
 import types
 
 import numpy as np
@@ -120,3 +121,22 @@ def test_entries_are_any_object_with_the_four_buffers():
     for call in (lambda: qlq.kv_quantize(k, v, out=four), lambda: qlq.kv_dequantize(four)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_buffers_too_small_for_the_entries_are_refused():
+    # (refused on the host: nothing is launched)
+    kb, vb = _inputs(5, 6, 2, 64)
+    k, v = bf16_to_gpu(kb), bf16_to_gpu(vb)
+    good = qlq.kv_quantize(k, v)
+    for n in ("k_codes", "k_scales", "v_codes", "v_scales"):
+        t = getattr(good, n)
+        for bad in (t[:5].clone(), t.cpu(), t.transpose(0, 1)):
+            with pytest.raises(ValueError):
+                qlq.kv_quantize(k, v, out=dataclasses.replace(good, **{n: bad}))
+        if n != "k_codes":                               # (those give the sizes)
+            with pytest.raises(ValueError):
+                qlq.kv_dequantize(dataclasses.replace(good, **{n: t[:5].clone()}))
+    for n in ("k_out", "v_out"):
+        for bad in (torch.empty_like(k)[:5], torch.empty(6, 2, 64), torch.empty(6, 2, 64, dtype=torch.uint8, device=dev())):
+            with pytest.raises(ValueError):
+                qlq.kv_dequantize(good, **{n: bad})

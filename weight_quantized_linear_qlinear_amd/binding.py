@@ -472,9 +472,17 @@ class QuantizedKV4:
     v_scales: torch.Tensor    # float16 [T, H, D / 32]
 
 
-def _eight_bits(c):
+def _room(dev: torch.device, t: torch.Tensor, nbytes: int, name: str):
+    if t.device != dev or not t.is_contiguous() or t.numel() * t.element_size() < nbytes:
+        raise ValueError(f"{name} must be dense on {dev}, {nbytes} bytes or more")
+
+
+def _entries_room(c, T: int, H: int, D: int, dev: torch.device):
     if isinstance(c, QuantizedKV4):
         raise ValueError("this call takes 8-bit entries (QuantizedKV)")
+    for t, n, name in ((c.k_codes, D, "k_codes"), (c.k_scales, D // 32 * 2, "k_scales"), (c.v_codes, D, "v_codes"),
+                       (c.v_scales, 2, "v_scales")):
+        _room(dev, t, T * H * n, name)
 
 
 def kv_quantize(k: torch.Tensor, v: torch.Tensor, out: QuantizedKV | None = None) -> QuantizedKV:
@@ -484,7 +492,7 @@ def kv_quantize(k: torch.Tensor, v: torch.Tensor, out: QuantizedKV | None = None
         raise ValueError("k and v must be bf16 [T, H, D] of the same shape")
     T, H, D = k.shape
     if out is not None:
-        _eight_bits(out)
+        _entries_room(out, T, H, D, k.device)
     else:
         out = QuantizedKV(torch.empty((T, H, D), dtype=torch.int8, device=k.device),
                           torch.empty((T, H, max(D // 32, 1)), dtype=torch.float16, device=k.device),
@@ -497,15 +505,20 @@ def kv_quantize(k: torch.Tensor, v: torch.Tensor, out: QuantizedKV | None = None
 
 def kv_dequantize(q: QuantizedKV, k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None):
     """Cache entries -> bf16 (K, V) [T, H, D]."""
-    _eight_bits(q)
     _require_gpu(q.k_codes, q.k_scales, q.v_codes, q.v_scales)
     T, H, D = q.k_codes.shape
+    dev = q.k_codes.device
+    _entries_room(q, T, H, D, dev)
     if k_out is None:
-        k_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.k_codes.device)
+        k_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
     if v_out is None:
-        v_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.k_codes.device)
+        v_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=dev)
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t.dtype != torch.bfloat16:
+            raise ValueError(f"{name} must be bf16")
+        _room(dev, t, T * H * D * 2, name)
     _check(lib().qlq_kv_dequantize(_ptr(q.k_codes), _ptr(q.k_scales), _ptr(q.v_codes), _ptr(q.v_scales), T, H, D,
-                                   _ptr(k_out), _ptr(v_out), _stream(q.k_codes.device)))
+                                   _ptr(k_out), _ptr(v_out), _stream(dev)))
     return k_out, v_out
 
 
