@@ -453,6 +453,7 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
     const int vswz = half ^ swizzle<T>(c32);                 // this lane's pieces: (4 k + 2 t) ^ vswz
     f32x16 o[NG];
     float m = kNegInf, l = 0.0f;
+    uint32_t bad_groups = 0;                                 // (4 bits) those in which the row sees a kBad
     int cur_e = kNoScale;                                    // E that o was computed with
 #pragma unroll
     for (int n = 0; n < NG; ++n)
@@ -529,23 +530,17 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
               for (int i = 0; i < 16; ++i) s[k][i] = 32 * k + 8 * (i / 4) + (i & 3) > lo ? s[k][i] : kNegInf;
           }
           if (BITS == 4 && now.gap && __builtin_expect(__ballot((sm.top[n & 3][lane & (kTileWaves - 1)] & 0x80000000u) != 0) != 0, 0)) {
-            uint32_t seen = 0, hit = 0;                      // the row's tokens by bit; the groups in which it sees a kBad
+            uint32_t hit = 0;                                // the groups in which this row sees a kBad (a token that is not
+#pragma unroll 1                                             // there has 0)
+            for (int q = 0; q < 4 * NB * NG; ++q) {
+              const int d = q / (4 * NB), at = 8 * (q % (4 * NB));
+              const f32x4 vs = *reinterpret_cast<const f32x4*>(&sm.vs[n & 3][d][at + 4 * half]);
 #pragma unroll
-            for (int k = 0; k < NB; ++k)
-#pragma unroll
-              for (int i = 0; i < 16; ++i) seen |= (s[k][i] != kNegInf ? 1u : 0u) << (16 * k + i);
-#pragma unroll 1
-            for (int q = 0; q < 4 * NB * NG; ++q) {          // (four tokens at a time: few registers)
-              const f32x4 vs = *reinterpret_cast<const f32x4*>(&sm.vs[n & 3][q / (4 * NB)][8 * (q % (4 * NB)) + 4 * half]);
-              const uint32_t bad = (vs.x < 0.0f ? 1u : 0u) | (vs.y < 0.0f ? 2u : 0u) | (vs.z < 0.0f ? 4u : 0u) | (vs.w < 0.0f ? 8u : 0u);
-              hit |= (bad & seen >> (4 * (q % (4 * NB))) ? 1u : 0u) << (q / (4 * NB));
+              for (int i = 0; i < 4; ++i)
+                if (vs[i] < 0.0f && (!a.causal || at + i <= hi) && (a.window <= 0 || at + i > lo)) hit |= 1u << d;
             }
             const auto both = __builtin_amdgcn_permlane32_swap(hit, hit, false, false);
-            hit = both[0] | both[1];
-#pragma unroll
-            for (int d = 0; d < NG; ++d)
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[d][i] = hit >> d & 1 ? __builtin_nanf("") : o[d][i];
+            bad_groups |= both[0] | both[1];
           }
         }
         float mx = kNegInf;
@@ -601,6 +596,12 @@ __global__ __launch_bounds__(kTileWaves * 64) void kv_attention_tile_kernel(KvAt
       const int i = (r0 + row) / a.G;
       return (int64_t)(e.qs + i) * a.Hq + h * a.G + (r0 + row - i * a.G);
     };
+    if (BITS == 4 && __builtin_expect(__ballot(bad_groups != 0) != 0, 0)) {
+#pragma unroll
+      for (int d = 0; d < NG; ++d)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[d][i] = bad_groups >> d & 1 ? __builtin_nanf("") : o[d][i];
+    }
     const float L = across32(l, true), back = __builtin_ldexpf(1.0f, cur_e);
     if (c32 < live_rows) {
       if (!split) {
