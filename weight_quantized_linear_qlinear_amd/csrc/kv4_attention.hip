@@ -15,9 +15,11 @@
 // matrix unit wants.  Scales come one token per lane (K's in the lower, V's in the upper half of the
 // wave) and reach the lanes of the scores through the wave's LDS, in the order of their tokens there.
 //
-// Bound by HBM and by instruction issue alike, two waves per SIMD (237 registers): 64 tokens over up to 16384
-// each, 32 heads over 8 of 128 (755 MB), 169 us, 4.5 TB/s; without the arithmetic about 155, with the arithmetic alone about
+// Bound by HBM and by instruction issue alike, two waves per SIMD: 64 tokens over up to 16384
+// each, 32 heads over 8 of 128 (755 MB), 168 us, 4.5 TB/s; without the arithmetic about 155, with the arithmetic alone about
 // as long.  A row is half a cache line at 128 channels, and the two heads that share one are read by two waves.
+// Of the 239 registers (128 channels) the joining asks for the most, sixteen chunks' parts of two passes at a time:
+// with one pass at a time the kernel has 145 (32 and 64 channels) to 160, and 237 and 275 of 192 and 256.
 // One token over 131071, 28 heads over 4 of 128: 33 us, where the bytes take 15: four trips to memory to
 // start, eight tiles one after another (1.3 us each) and three levels of joining.  A wave takes 16 rows; more rows are more tiles, which
 // read K and V again, mostly from L2: with pairs of tiles per wave (32 rows, 252 registers) 16 sequences of
@@ -111,8 +113,8 @@ __device__ __forceinline__ f16x8 weigh(f16x8 v, const float (&e)[2][4]) {
 // Octaves from a row's reference up to its largest weight: 2^15 is the largest power of two in fp16.
 constexpr float kLift = 15.0f;
 
-// Waves per workgroup, one workgroup per CU.  Heads of 192 and 256 channels have 300 registers, one wave per
-// SIMD; held to 256 with eight waves, in us: 32 tokens over up to 9000 each 98 -> 89 and 126 -> 117, but 48 rows of
+// Waves per workgroup, one workgroup per CU.  Heads of 192 and 256 channels have 305 registers, the joining's among
+// them, one wave per SIMD; held to 256 with eight waves, in us: 32 tokens over up to 9000 each 98 -> 89 and 126 -> 117, but 48 rows of
 // 256 x 16 over 4000 55 -> 81, 24 rows over 20000 46 -> 61, 32 rows of 192 x 16 over 4000 56 -> 68.
 constexpr int waves_of(int NG) { return NG <= 4 ? 8 : 4; }
 
@@ -458,11 +460,14 @@ KvAttnPlan plan_kv4_attention(int64_t T, int64_t B, int64_t Hk, int64_t G, int64
   KvAttnPlan p;
   const int64_t rows = one_each ? G : (T + B - 1) / B * G;   // query rows of an average sequence
   const int NG = (int)(D / 32);
-  // From here on the many-row kernel.  16 and 64 sequences, in us, this kernel and that one: heads of 64, 96 rows 46
-  // and 58, 74 and 73; 128: 55 and 62, 75 and 74, 192 rows x 64: 122 and 87; of 96, 64 rows 45 and 63, 96: 57 and 67,
-  // 128: 72 and 71; of 128, 64 rows 80 and 97, 106 and 163, 96: 97 and 106, 185 and 168, 128: 123 and 117; of 192, 64
-  // rows 80 and 80, 112 and 110, 96: 98 and 114, 180 and 147; of 256 (where that one spills), 96 rows 78 and
-  // 145, 256 rows x 64: 260 and 351.
+  // From here on the many-row kernel.  16 sequences over 4000 tokens, then 64, kernel alone, in us, this one and that one:
+  //   96 (16 heads over 4)   64 rows 44 and 64, 124 and 139; 80 rows 50 and 64, 148 and 140; 96 rows 56 and 65, 174 and 145
+  //   128 (32 over 8)        64 rows 79 and 94, 211 and 294; 80 rows 87 and 97, 375 and 296; 96 rows 99 and 100, 370 and 299
+  //   192 (32 over 8)        80 rows 161 and 174, 667 and 521; 96 rows 181 and 179, 654 and 528
+  //   64 (32 over 8)         96 rows 72 and 81, 243 and 262; 128 rows 90 and 84, 299 and 264
+  //   256 (16 over 2; that one spills)  256 rows 155 and 223, 526 and 538; 512 rows 261 and 288, 1013 and 853
+  // The border of 96, 128 and 192 is the large calls'; small ones lose up to a third between 64 and 96 rows (8 heads over 2
+  // of 192, 16 x 80 rows 56 and 81).
   if (rows > (NG <= 2 ? 96 : NG == 8 ? 256 : 64)) return plan_kv_attention(T, B, Hk, G, D, one_each);
   constexpr int64_t TR = 16;
   // Heads per workgroup.  Four that share cache lines, where every wave has more than ten tiles to take; else one, whose

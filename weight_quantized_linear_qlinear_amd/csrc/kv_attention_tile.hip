@@ -25,7 +25,9 @@
 // Over 4 bits (rows in the order of kv_rows.h) K and V come with an fp16 scale per 32 channels each; K' and V' are
 // the same, V's scales by group, their common 2^-E over all of a token's groups, and K' of a tile takes the power of
 // two that its largest scale leaves room for.  A tile's conversion is shared by 256 rows, so the cache's width
-// hardly shows: the two chunks above 320 us.
+// hardly shows: the two chunks above 334 us.  By the counters the matrix cores are busy 30 % of that time, the vector
+// unit issues 44 %, and a wave waits a third of its own: matrix and vector work overlap little (products stand in
+// runs of 16 with nothing between, and a barrier per tile keeps the two waves of a SIMD in step).
 #include <type_traits>
 
 #include "kv_attention.h"

@@ -21,9 +21,11 @@
 // their partners by (weights included: two operations per channel) stays in registers for all heads.
 // Rows pass through the wave's LDS for the partners, 4-bit codes for the order of the cache.
 //
-// Bound by HBM for many tokens: 8192 tokens of 32 + 8 heads of 128, normed and turned, 33 us, 5.0 TB/s; by its one round of
-// waves for fewer (4095 tokens of 16 + 16 heads of 64 11 us, 3.0 TB/s; one token 3.7 us).  Into 4 bits by K's fp64 too: 8191
-// tokens of 32 + 8 + 8 heads of 128 40 us, 4.4 TB/s; 2048 tokens 17 us, two waves per SIMD.  Into 8 bits 333 tokens 6.7 us.
+// Bound by HBM for many tokens: 8192 tokens of 32 + 8 heads of 128, normed and turned, 33 us, 5.0 TB/s (32 heads turned
+// alone, three axes, 24 us, 5.5 TB/s); by its one round of waves for fewer (4095 tokens of 16 + 16 heads of 64 11 us, 3.0
+// TB/s; one token 3.6 us).  Into 4 bits by K's fp64 too: 8191 tokens of 32 + 8 + 8 heads of 128 40 us, 4.5 TB/s;
+// 2048 tokens 18 us, two waves per SIMD.  Into 8 bits 333 tokens 6.7 us, 2048 16 us, 8191 40 us (4.6 TB/s).  K and V alone
+// into 4 bits, 8191 tokens of 8 heads of 128 14 us (43 MB, 3.1 TB/s), of 16 of 64 15 us.
 #include <type_traits>
 
 #include "kv_rows.h"
@@ -517,7 +519,8 @@ __global__ __launch_bounds__(kWaves * 64, (kRoom<KOUT, TPR>)) void norm_rope_ker
 }
 
 // Rows of chosen slots of a 4-bit cache back to bf16 (8 channels per thread); a slot outside the pool
-// gives zeros.  For rows that kv4_gather_quads_kernel does not take; bound by its loads of single bytes.
+// gives zeros.  For rows that kv4_gather_quads_kernel does not take; bound by its loads of single bytes: 8191 tokens of 16
+// heads of 64 (43 MB) 11.0 us, 3.9 TB/s, of 8 of 96 and 4 of 192 (32 MB) 9.2 us, 3.5 TB/s.
 __global__ __launch_bounds__(256) void kv4_gather_kernel(const uint8_t* __restrict__ kq, const uint16_t* __restrict__ ks,
                                                          const uint8_t* __restrict__ vq, const uint16_t* __restrict__ vs,
                                                          int64_t pool, int H, int D, const void* __restrict__ slots,
@@ -613,10 +616,13 @@ hipError_t launch_kout(const NormRopeArgs& in, hipStream_t st) {
   const int rpw = 64 / (a.D / 8), nk = (a.Hk + rpw - 1) / rpw;
   const int n = (a.Hq + rpw - 1) / rpw + (kUnitsK<KOUT> + (KOUT ? 1 : 0)) * nk;    // units of a token
   // A wave per token from 800 tokens on, four before that, and more workgroups per token while there are
-  // fewer than 1024.  Into 4 bits, 32 + 2 x 8 heads of 128, gathered back, us, four waves and one: 130 tokens 8.1 and
-  // 14.0, 500 12.7 and 15.0, 700 14.3 and 16.1, 1000 18.1 and 16.9; heads of 64, 16 + 2 x 16: 500 11.8 and 11.6, 1000
-  // 15.8 and 12.9; normed and turned alone 700 tokens 8.2 and 10.1, 1000 9.9 and 10.9.  Two waves: 2048
-  // tokens 21.9 against 21.2, 8191 62 against 60.
+  // fewer than 1024.  Kernel alone, us, four waves and one, 32 + 8 heads of 128 and 16 + 16 of 64: normed and turned 300 tokens
+  // 5.7 and 10.1, 4.5 and 6.6; 700 8.6 and 11.0, 5.2 and 7.2; 1000 10.3 and 11.5, 6.0 and 7.3; 2000 12.6 and
+  // 13.2, 9.0 and 8.1; 4095 19.8 and 17.2, 14.0 and 10.9.  Into 8 bits 700 10.7 and 12.6, 8.0 and 8.8; 1000 13.0 and 13.4,
+  // 9.5 and 9.2; 2000 16.6 and 15.9, 13.9 and 11.0.  Into 4 bits 300 8.4 and 12.4, 7.8 and 8.9; 700 10.9 and 13.0,
+  // 10.0 and 9.2; 1000 12.8 and 13.7, 12.8 and 9.6; 1500 14.5 and 16.7, 12.3 and 11.4; 4095 29.2 and 24.0, 27.4 and 19.4.
+  // The sides cross between 500 tokens (64 channels, 4 bits) and 2500 (128, normed and turned): one border for all
+  // forms, with up to 15 % lost around it.  Two waves, 4 bits with the gather: 2048 tokens 21.9 against 21.2, 8191 62 against 60.
   a.wpt_shift = 0;
   int gy = 1;
   if (a.T < 800) {
